@@ -8,9 +8,13 @@ FusedConv README ("Description", "Inputs", "Outputs", "Attributes").
 from __future__ import annotations
 
 from ._binding import EXPORTS, FusedConvError, Handle, LIB_PATH, load
+from .transformer import (Attention, LayerNorm, Rotary, attention, attention_backward, layer_norm,
+                          layer_norm_backward, rotary)
 
 __all__ = ["fused_conv", "FusedConv", "Handle", "FusedConvError", "load", "LIB_PATH", "EXPORTS",
-           "ConvBackwardData", "ConvBackwardWeight", "conv_backward_data", "conv_backward_weight"]
+           "ConvBackwardData", "ConvBackwardWeight", "conv_backward_data", "conv_backward_weight",
+           "LayerNorm", "Rotary", "Attention", "layer_norm", "layer_norm_backward", "rotary",
+           "attention", "attention_backward"]
 
 _cache: dict = {}
 

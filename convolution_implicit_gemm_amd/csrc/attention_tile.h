@@ -1,0 +1,241 @@
+// Tiles of the attention kernels: matrix-core fragments, their LDS layout, and
+// the way a tile gets there.
+//
+// Everything is built on 32 x 32 products with 16 terms per step (a "step"):
+//   A: lane l holds row l % 32, terms 8 * (l / 32) .. + 7
+//   B: lane l holds column l % 32, the same terms
+//   C: lane l holds column l % 32; its value i is row 8 * (i / 4) + 4 * (l / 32) + i % 4
+// for f16 and bf16 one v_mfma_f32_32x32x16, for f32 eight v_mfma_f32_32x32x2
+// over the same terms.  C's rows map onto the next product's terms without
+// any exchange between lanes: values 8s .. 8s + 7 of C, rounded to T, are the
+// B fragment of step s of a product over those rows, if A's terms are taken in
+// the order {4h .. 4h + 3, 8 + 4h .. 8 + 4h + 3} (h = l / 32), which
+// load_columns does.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "transformer.h"
+#include "vec.h"
+
+namespace fc {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <typename T>
+struct Frag;
+template <>
+struct Frag<_Float16> {
+  typedef _Float16 type __attribute__((ext_vector_type(8)));
+};
+template <>
+struct Frag<__bf16> {
+  typedef __bf16 type __attribute__((ext_vector_type(8)));
+};
+template <>
+struct Frag<float> {
+  typedef float type __attribute__((ext_vector_type(8)));
+};
+template <typename T>
+using frag_t = typename Frag<T>::type;
+
+__device__ __forceinline__ f32x16 mma(frag_t<_Float16> a, frag_t<_Float16> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(frag_t<__bf16> a, frag_t<__bf16> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(frag_t<float> a, frag_t<float> b, f32x16 c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+  return c;
+}
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 c;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) c[i] = 0.f;
+  return c;
+}
+// Row of value i of C for lanes of half h.
+__device__ __forceinline__ int c_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+
+// max / sum of a lane's value with its partner's in the other half of the wave
+// (lanes l and l ^ 32 hold the two halves of a column of C).
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// A tile of ROWS rows of DP values in LDS, in 16-byte chunks.  Chunk c of row r
+// lies at chunk c ^ swizzle(r) of the row, so that both ways of reading a tile
+// spread over all banks: 32 rows at one chunk (load_rows), and 4 rows at two
+// neighbouring chunks (load_columns; hence the reversed bits, which set
+// neighbouring rows far apart).  DP * sizeof(T) is 64, 128, 192, ... bytes; for
+// odd multiples of 64 two rows share a line of 128 bytes.
+template <typename T, int DP>
+struct Tile {
+  static constexpr int CE = 16 / sizeof(T);  // values of a chunk
+  static constexpr int NC = DP / CE;         // chunks of a row
+  static constexpr bool kWhole = NC % 8 == 0;
+  static __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (kWhole) return ((row & 1) << 2) | (row & 2) | ((row >> 2) & 1);
+    else return (row & 2) | ((row >> 2) & 1);
+  }
+  static constexpr int bytes(int rows) { return rows * DP * (int)sizeof(T); }
+
+  // Terms 16 * step .. + 15 of rows row0 .. row0 + 31 (row0 a multiple of 32).
+  static __device__ __forceinline__ frag_t<T> load_rows(const T* tile, int row0, int step) {
+    const int l = threadIdx.x & 63, row = l & 31, h = l >> 5, s = swizzle(row);
+    const T* base = tile + (row0 + row) * DP;
+    if constexpr (sizeof(T) == 2) {
+      return *reinterpret_cast<const frag_t<T>*>(base + ((2 * step + h) ^ s) * CE);
+    } else {
+      typedef float f4 __attribute__((ext_vector_type(4)));
+      const f4 a = *reinterpret_cast<const f4*>(base + ((4 * step + 2 * h) ^ s) * CE);
+      const f4 b = *reinterpret_cast<const f4*>(base + ((4 * step + 2 * h + 1) ^ s) * CE);
+      return frag_t<T>{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+  }
+
+  // The transpose: "rows" are the values 32 * t .. + 31 of the tile's rows, the
+  // terms its rows row0 + {4h + 0 .. 3, 8 + 4h + 0 .. 3} (row0 a multiple of 16).
+  // 16-bit: ds_read_b64_tr_b16 turns a 4 x 16 block per 16 lanes, lane i
+  // fetching row i / 4, values 4 * (i % 4) .. + 3, and getting column i.
+  static __device__ __forceinline__ frag_t<T> load_columns(const T* tile, int row0, int t) {
+    const int l = threadIdx.x & 63, h = l >> 5;
+    if constexpr (sizeof(T) == 2) {
+      typedef short s4 __attribute__((ext_vector_type(4)));
+      typedef short s8 __attribute__((ext_vector_type(8)));
+      const int i = l & 15, g = (l >> 4) & 1;
+      const int row = 4 * h + (i >> 2);
+      const int chunk = (4 * t + 2 * g + ((i & 3) >> 1)) ^ swizzle(row);
+      const T* p = tile + (row0 + row) * DP + chunk * CE + 4 * (i & 1);
+      typedef __attribute__((address_space(3))) s4 lds_s4;
+      const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
+      const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 8 * DP));
+      return __builtin_bit_cast(frag_t<T>, s8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+    } else {
+      const int d = 32 * t + (l & 31);
+      frag_t<T> f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = (j >> 2) * 8 + 4 * h + (j & 3);
+        f[j] = tile[(row0 + row) * DP + ((d / CE) ^ swizzle(row)) * CE + d % CE];
+      }
+      return f;
+    }
+  }
+
+  // Start copying ROWS rows of `src` (row stride `stride` values; d values a
+  // row) into the tile, WAVES waves sharing the work; rows past `last` repeat
+  // row `last`, so nothing outside the tensor is read.  The copy goes straight
+  // to LDS (64 chunks of 16 bytes an instruction, in lane order: the swizzle is
+  // applied to the address a lane fetches).  Chunks past d stay as they are:
+  // clear_padding() has set them to zero.
+  template <int ROWS, int WAVES>
+  static __device__ __forceinline__ void fetch(T* tile, const T* src, int64_t stride, int last,
+                                               int d, int wave) {
+    constexpr int CALLS = ROWS * NC / 64;
+    static_assert(ROWS * NC % 64 == 0 && CALLS % WAVES == 0);
+    const int l = threadIdx.x & 63;
+    const uint32_t row_bytes = (uint32_t)stride * sizeof(T);
+#pragma unroll
+    for (int i = 0; i < CALLS / WAVES; ++i) {
+      const int call = wave + i * WAVES;
+      const int at = call * 64 + l;
+      const int row = at / NC;
+      const int chunk = (at % NC) ^ swizzle(row);
+      const uint32_t off = (uint32_t)min(row, last) * row_bytes + chunk * 16;
+      if (chunk * CE < d)
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)((const char*)src + off),
+            (__attribute__((address_space(3))) void*)(tile + call * 64 * CE), 16, 0, 0);
+    }
+  }
+
+  template <int ROWS>
+  static __device__ __forceinline__ void clear_padding(T* tile, int d, int thread, int threads) {
+    if (d == DP) return;
+    for (int at = thread; at < ROWS * NC; at += threads)
+      if (((at % NC) ^ swizzle(at / NC)) * CE >= d) {
+        typedef float f4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<f4*>(tile + at * CE) = f4{0.f, 0.f, 0.f, 0.f};
+      }
+  }
+};
+
+// Every copy this wave has started is in LDS, then the block meets: after it
+// all waves' copies can be read, and what was read before can be overwritten.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
+// B fragments of 32 rows of a matrix in memory (terms: the row's d values), for
+// all steps: lane l holds row row(l % 32).  negate: the operand's sign, for a
+// negative scale.  Values past d are zero.
+template <typename T, int DP>
+__device__ __forceinline__ void load_operand(frag_t<T> (&f)[DP / 16], const T* row_ptr, int d,
+                                             bool negate) {
+  const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int s = 0; s < DP / 16; ++s) {
+    const int at = 16 * s + 8 * h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[s][j] = (T)0.f;
+    if (at < d) f[s] = *reinterpret_cast<const frag_t<T>*>(row_ptr + at);
+    if (negate)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[s][j] = -f[s][j];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ frag_t<T> to_frag(const f32x16& c, int step) {
+  frag_t<T> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = (T)c[8 * step + j];
+  return f;
+}
+
+// Blocks go round the 8 XCDs in launch order; this deals each XCD a run of
+// consecutive work items, so that neighbours (which read the same keys, or the
+// same queries) share its L2.  The grid is 8 * ceil(total / 8); an item >= total
+// has no work.
+__device__ __forceinline__ int xcd_item(int block, int total) {
+  const int run = (total + 7) >> 3;
+  return (block & 7) * run + (block >> 3);
+}
+inline unsigned xcd_grid(int64_t total) { return (unsigned)((total + 7) / 8 * 8); }
+
+// What a batch entry's lengths and the window let a query see.
+struct Sight {
+  int nq, nk, left, right;
+  __device__ __forceinline__ int lo(int i) const {  // first key
+    return left < 0 ? 0 : max(0, i + nk - nq - left);
+  }
+  __device__ __forceinline__ int hi(int i) const {  // one past the last key; <= lo: none
+    if (i >= nq) return 0;
+    return right < 0 ? nk : min(nk, i + nk - nq + right + 1);
+  }
+  // the queries that see key j < nk
+  __device__ __forceinline__ int qlo(int j) const {
+    return right < 0 ? 0 : max(0, j - right - nk + nq);
+  }
+  __device__ __forceinline__ int qhi(int j) const {
+    return left < 0 ? nq : min(nq, j + left - nk + nq + 1);
+  }
+};
+__device__ __forceinline__ int length_of(const int32_t* lengths, int b, int most) {
+  return lengths ? min(max(lengths[b], 0), most) : most;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+}  // namespace fc

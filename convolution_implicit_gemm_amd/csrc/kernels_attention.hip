@@ -1,0 +1,452 @@
+// Attention, forward (include/fusedconv_transformer.h): one pass over the keys
+// with the running maximum and sum of the softmax.
+//
+// Compiled once per head size the tiles are made for (FC_DP = 32, 64, 96, 128);
+// unit 32 also holds the plan and the launcher.
+//
+// Scores are computed transposed, S^T = K Q^T: a lane then holds one query
+// (C's column) and half of a tile's keys, the softmax needs one exchange per
+// tile, and the probabilities are the B operand of O^T = V^T P^T as they stand.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "attention_tile.h"
+#include "fusedconv.h"
+#include "internal.h"
+#include "transformer.h"
+
+namespace fc {
+
+struct AttnK {
+  AttnParams p;
+  const void *q, *k, *v;
+  const int32_t *q_lengths, *k_lengths;
+  void* o;
+  float* lse;
+  float *part_o, *part_lse;  // split form: [units][splits][rows][d], [units][splits][rows]
+  float c;                   // |scale| * log2(e), at least the least normal number
+  int32_t tiles;             // row tiles of one head (tile form)
+  int32_t splits, rows, row_groups;
+};
+
+namespace {
+
+// Running softmax state of a lane's query: reference value m (raw score
+// units), sum of exponentials so far (this half's keys), output columns.
+template <int NT>
+struct Running {
+  float m, l;
+  f32x16 o[NT];
+  __device__ __forceinline__ void start() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t] = zero16();
+  }
+};
+
+// One block of 32 * KB keys: scores s (masked entries -inf) -> probabilities in
+// s, state updated.  The reference m follows the maximum only when that exceeds
+// it by 8 octaves, or is the first: factors up to 2^8 are exact in every T, the
+// sums are fp32, and the output is rescaled a few times instead of every tile.
+template <int KB, int NT>
+__device__ __forceinline__ void softmax_step(f32x16 (&s)[KB], Running<NT>& st, float c) {
+  float mx = s[0][0];
+#pragma unroll
+  for (int k = 0; k < KB; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[k][i]);
+  mx = half_max(mx);
+  if (__any(mx * c > st.m * c + 8.0f)) {
+    const float m = fmaxf(st.m, mx);
+    const float a = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((st.m - m) * c);
+    st.m = m;
+    st.l *= a;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st.o[t][i] *= a;
+  }
+  const float mc = st.m == -INFINITY ? 0.f : st.m * c;
+  float l = 0.f;
+#pragma unroll
+  for (int k = 0; k < KB; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[k][i] = __builtin_amdgcn_exp2f(fmaf(s[k][i], c, -mc));
+      l += s[k][i];
+    }
+  st.l += l;
+}
+
+// Keys key0 + c_row(...) outside [lo, hi) of this lane's query get -inf.
+template <int KB>
+__device__ __forceinline__ void mask_keys(f32x16 (&s)[KB], int key0, int lo, int hi, int h) {
+#pragma unroll
+  for (int k = 0; k < KB; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int j = key0 + 32 * k + c_row(i, h);
+      if (j < lo || j >= hi) s[k][i] = -INFINITY;
+    }
+}
+
+// ------------------------------------------------------------ many queries
+// A block has 128 queries of one head, 32 a wave, and walks the keys in tiles
+// of BN, double-buffered in LDS: tile j + 1 is on its way while j is used.
+template <typename T, int DP>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK a) {
+  using L = Tile<T, DP>;
+  constexpr int BN = sizeof(T) == 2 ? 64 : 32;
+  constexpr int KB = BN / 32, NT = DP / 32, NS = DP / 16;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  T* tiles = (T*)lds;  // [2 buffers][K, V][BN * DP]
+
+  const AttnParams& p = a.p;
+  const int total = p.batch * p.heads * a.tiles;
+  int item = xcd_item(blockIdx.x, total);
+  if (item >= total) return;
+  // the last rows first: under a causal window they have the most keys
+  const int tile_q = a.tiles - 1 - item % a.tiles;
+  item /= a.tiles;
+  const int head = item % p.heads, b = item / p.heads, kvh = head / p.group;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const Sight see{length_of(a.q_lengths, b, p.sq), length_of(a.k_lengths, b, p.sk), p.left, p.right};
+  const int row0 = tile_q * 128, last_row = min(row0 + 127, see.nq - 1);
+  const int i = row0 + wave * 32 + (lane & 31);
+
+  // keys of the block, of the wave, and those that all rows of the wave see
+  const int first = row0 < see.nq ? see.lo(row0) & ~(BN - 1) : 0;
+  const int end = row0 < see.nq ? see.hi(last_row) : 0;
+  const int w0 = row0 + wave * 32, w1 = min(w0 + 31, see.nq - 1);
+  const int wave_lo = see.lo(w0), wave_hi = w0 < see.nq ? see.hi(w1) : 0;
+  const int all_lo = see.lo(w1), all_hi = w0 + 31 < see.nq ? see.hi(w0) : 0;
+  const int lo = see.lo(i), hi = see.hi(i);
+
+  const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
+  const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
+  auto buffer = [&](int n) { return tiles + n * 2 * BN * DP; };
+  auto fetch = [&](int key0, int n) {
+    const int last = see.nk - 1 - key0;
+    L::template fetch<BN, 4>(buffer(n), kp + key0 * p.k.s, p.k.s, last, p.d, wave);
+    L::template fetch<BN, 4>(buffer(n) + BN * DP, vp + key0 * p.v.s, p.v.s, last, p.d, wave);
+  };
+
+  Running<NT> st;
+  st.start();
+  L::template clear_padding<4 * BN>(tiles, p.d, threadIdx.x, 256);
+  if (first < end) {
+    __syncthreads();
+    fetch(first, 0);
+    frag_t<T> q[NS];
+    const int qi = min(i, see.nq - 1);
+    load_operand<T, DP>(q, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d,
+                        p.scale < 0.f);
+    int n = 0;
+    for (int key0 = first; key0 < end; key0 += BN, n ^= 1) {
+      tile_barrier();  // tile n has arrived; everyone is done with the other buffer
+      if (key0 + BN < end) fetch(key0 + BN, n ^ 1);
+      if (key0 >= wave_hi || key0 + BN <= wave_lo) continue;
+      const T* kt = buffer(n);
+      const T* vt = kt + BN * DP;
+      f32x16 s[KB];
+#pragma unroll
+      for (int k = 0; k < KB; ++k) s[k] = zero16();
+#pragma unroll
+      for (int d = 0; d < NS; ++d)
+#pragma unroll
+        for (int k = 0; k < KB; ++k) s[k] = mma(L::load_rows(kt, 32 * k, d), q[d], s[k]);
+      if (key0 < all_lo || key0 + BN > all_hi) mask_keys(s, key0, lo, hi, h);
+      softmax_step(s, st, a.c);
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const frag_t<T> pf = to_frag<T>(s[k], d);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            st.o[t] = mma(L::load_columns(vt, 32 * k + 16 * d, t), pf, st.o[t]);
+        }
+    }
+  }
+  if (i >= p.sq) return;
+  const float l = half_sum(st.l);
+  const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;  // no key seen: zeros
+  T* o = (T*)a.o + b * p.o.b + i * p.o.s + head * p.o.h;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = 32 * t + 8 * g + 4 * h;
+      if (32 * t + 8 * g >= p.d) continue;
+      Piece<T, 4> po;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) po.v[j] = to_type<T>(st.o[t][4 * g + j] * inv);
+      store_piece<T, 4>(o + d, po);
+    }
+  if (a.lse && h == 0)
+    a.lse[((int64_t)b * p.heads + head) * p.sq + i] =
+        l == 0.f ? -INFINITY : st.m * a.c * kLn2 + logf(l);
+}
+
+// ------------------------------------------------------------- few queries
+// Up to 32 rows (queries x the heads that share a key head) fill one wave's
+// columns.  The keys an entry really has are split evenly over `splits` blocks
+// and there over the WAVES waves, tile by tile; each wave brings its own tiles
+// of 32 keys to its own LDS, two ahead of none but its own waits, so that no
+// barrier stops the stream from HBM, which bounds this form.  The waves meet in
+// LDS, the blocks in k_attention_join.
+template <typename T, int DP>
+struct Few {
+  static constexpr int kWaves = sizeof(T) * DP > 256 ? 2 : 4;
+  static constexpr int kTile = 32 * DP;               // values of a tile of 32 keys
+  static constexpr int kStream = kWaves * 4 * kTile * (int)sizeof(T);
+  static constexpr int kMerge = kWaves * (32 * (DP + 1) + 64) * 4;
+  static constexpr int kLds = kStream > kMerge ? kStream : kMerge;
+};
+
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
+  using L = Tile<T, DP>;
+  using F = Few<T, DP>;
+  constexpr int NT = DP / 32, NS = DP / 16, W = F::kWaves;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+
+  const AttnParams& p = a.p;
+  const int split = blockIdx.x % a.splits;
+  const int unit = blockIdx.x / a.splits;
+  const int group = unit % a.row_groups;
+  const int kvh = unit / a.row_groups % p.kv_heads, b = unit / a.row_groups / p.kv_heads;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const Sight see{length_of(a.q_lengths, b, p.sq), length_of(a.k_lengths, b, p.sk), p.left, p.right};
+  const int rows = min(a.rows - group * 32, 32);
+  const int r = group * 32 + min(lane & 31, rows - 1);
+  const int i = r / p.group, head = kvh * p.group + r % p.group;
+
+  const int i0 = group * 32 / p.group, i1 = min((group * 32 + rows - 1) / p.group, see.nq - 1);
+  const int first = i0 < see.nq ? see.lo(i0) & ~31 : 0, end = i0 < see.nq ? see.hi(i1) : 0;
+  const int count = max(end - first + 31, 0) >> 5;  // tiles of 32 keys
+  const int t0 = (int)((int64_t)count * split / a.splits);
+  const int t1 = (int)((int64_t)count * (split + 1) / a.splits);
+  const int lo = see.lo(i), hi = see.hi(i);
+  const int all_lo = see.lo(i1), all_hi = see.hi(i0);  // every row of the group sees [all_lo, all_hi)
+  const bool all_rows = (group * 32 + rows - 1) / p.group < see.nq;
+
+  const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
+  const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
+  T* mine = (T*)lds + wave * 4 * F::kTile;
+  auto fetch = [&](int tile, int n) {
+    const int key0 = first + 32 * tile;
+    const int last = see.nk - 1 - key0;
+    L::template fetch<32, 1>(mine + n * 2 * F::kTile, kp + key0 * p.k.s, p.k.s, last, p.d, 0);
+    L::template fetch<32, 1>(mine + (n * 2 + 1) * F::kTile, vp + key0 * p.v.s, p.v.s, last, p.d, 0);
+  };
+  constexpr int kLoads = 2 * 32 * L::NC / 64;  // of one fetch
+
+  Running<NT> st;
+  st.start();
+  L::template clear_padding<4 * 32>(mine, p.d, lane, 64);
+  int tile = t0 + wave;
+  if (tile < t1) {
+    frag_t<T> q[NS];
+    const int qi = max(min(i, see.nq - 1), 0);
+    load_operand<T, DP>(q, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d,
+                        p.scale < 0.f);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    fetch(tile, 0);
+    for (int n = 0; tile < t1; tile += W, n ^= 1) {
+      if (tile + W < t1) {
+        fetch(tile + W, n ^ 1);
+        // all but the loads of the tile just asked for
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads < 63 ? kLoads : 63) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      const T* kt = mine + n * 2 * F::kTile;
+      const T* vt = kt + F::kTile;
+      const int key0 = first + 32 * tile;
+      f32x16 s[1] = {zero16()};
+#pragma unroll
+      for (int d = 0; d < NS; ++d) s[0] = mma(L::load_rows(kt, 0, d), q[d], s[0]);
+      if (!all_rows || key0 < all_lo || key0 + 32 > all_hi) mask_keys(s, key0, lo, hi, h);
+      softmax_step(s, st, a.c);
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const frag_t<T> pf = to_frag<T>(s[0], d);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          st.o[t] = mma(L::load_columns(vt, 16 * d, t), pf, st.o[t]);
+      }
+      // the reads of this buffer have ended before the next copy into it starts
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  }
+
+  // The waves' states, side by side in LDS: [wave][row][DP + 1] outputs, then
+  // [wave][2][32] of (m * c, l).  The odd row length keeps the columns apart.
+  const float l = half_sum(st.l);
+  __syncthreads();
+  float* so = (float*)lds + wave * 32 * (DP + 1);
+  float* sm = (float*)lds + W * 32 * (DP + 1);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) so[(lane & 31) * (DP + 1) + 32 * t + c_row(j, h)] = st.o[t][j];
+  if (h == 0) {
+    sm[wave * 64 + lane] = st.m == -INFINITY ? -INFINITY : st.m * a.c;
+    sm[wave * 64 + 32 + lane] = l;
+  }
+  __syncthreads();
+  for (int at = threadIdx.x; at < rows * p.d; at += W * 64) {
+    const int row = at / p.d, d = at - row * p.d;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, sm[w * 64 + row]);
+    float sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[w * 64 + row] - m);
+      sum += f * sm[w * 64 + 32 + row];
+      acc += f * ((const float*)lds)[(w * 32 + row) * (DP + 1) + d];
+    }
+    const float out = sum > 0.f || sum != sum ? acc / sum : 0.f;
+    const float lse2 = sum == 0.f ? -INFINITY : m + log2f(sum);
+    const int rr = group * 32 + row, ri = rr / p.group, rh = kvh * p.group + rr % p.group;
+    if (a.splits > 1) {
+      const int64_t part = ((int64_t)(b * p.kv_heads + kvh) * a.splits + split) * a.rows + rr;
+      a.part_o[part * p.d + d] = out;
+      if (d == 0) a.part_lse[part] = lse2;
+    } else {
+      ((T*)a.o)[b * p.o.b + ri * p.o.s + rh * p.o.h + d] = to_type<T>(out);
+      if (d == 0 && a.lse)
+        a.lse[((int64_t)b * p.heads + rh) * p.sq + ri] = lse2 * kLn2;
+    }
+  }
+}
+
+// Joins the splits of a row: 64 threads a row, 4 rows a block.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attention_join(AttnK a) {
+  const AttnParams& p = a.p;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (at >= (int64_t)p.batch * p.kv_heads * a.rows) return;
+  const int64_t unit = at / a.rows;
+  const int r = (int)(at - unit * a.rows);
+  const int b = (int)(unit / p.kv_heads), kvh = (int)(unit % p.kv_heads);
+  const int i = r / p.group, head = kvh * p.group + r % p.group;
+  const float* lse = a.part_lse + unit * a.splits * a.rows + r;
+  const float* po = a.part_o + (unit * a.splits * a.rows + r) * p.d;
+  float m = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, lse[(int64_t)s * a.rows]);
+  float sum = 0.f, acc[2] = {0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float l = lse[(int64_t)s * a.rows];
+    const float f = l == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(l - m);
+    sum += f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 64 * e < p.d) acc[e] += f * po[(int64_t)s * a.rows * p.d + lane + 64 * e];
+  }
+  const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (lane + 64 * e < p.d)
+      ((T*)a.o)[b * p.o.b + i * p.o.s + head * p.o.h + lane + 64 * e] = to_type<T>(acc[e] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[((int64_t)b * p.heads + head) * p.sq + i] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+#define FC_DP_NAME(name) FC_CAT(name, FC_DP)
+
+}  // namespace
+
+int FC_DP_NAME(attention_forward_)(const AttnPlan& plan, const AttnK& k, hipStream_t st) {
+  int rc = FUSEDCONV_OK;
+  with_type(plan.dtype, [&](auto tag) {
+    using T = typename decltype(tag)::type;
+    const AttnParams& p = k.p;
+    if (plan.few) {
+      auto fn = k_attention_few<T, FC_DP>;
+      constexpr int bytes = Few<T, FC_DP>::kLds;
+      rc = set_max_dynamic_lds((const void*)fn, bytes);
+      if (rc != FUSEDCONV_OK) return;
+      hipLaunchKernelGGL(fn, dim3((unsigned)(p.batch * p.kv_heads * k.row_groups * k.splits)),
+                         dim3(64 * Few<T, FC_DP>::kWaves), bytes, st, k);
+      if (k.splits > 1)
+        hipLaunchKernelGGL((k_attention_join<T>),
+                           dim3((unsigned)(((int64_t)p.batch * p.kv_heads * k.rows + 3) / 4)),
+                           dim3(256), 0, st, k);
+    } else {
+      auto fn = k_attention<T, FC_DP>;
+      constexpr int bytes = 4 * Tile<T, FC_DP>::bytes(sizeof(T) == 2 ? 64 : 32);
+      rc = set_max_dynamic_lds((const void*)fn, bytes);
+      if (rc != FUSEDCONV_OK) return;
+      hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.heads * k.tiles)), dim3(256), bytes,
+                         st, k);
+    }
+  });
+  if (rc != FUSEDCONV_OK) return rc;
+  return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH;
+}
+
+#if FC_DP == 32
+int attention_forward_64(const AttnPlan&, const AttnK&, hipStream_t);
+int attention_forward_96(const AttnPlan&, const AttnK&, hipStream_t);
+int attention_forward_128(const AttnPlan&, const AttnK&, hipStream_t);
+
+// Bytes of the split form's partial results.
+static size_t split_bytes(const AttnParams& p, int splits) {
+  const size_t rows = (size_t)p.batch * p.kv_heads * splits * p.sq * p.group;
+  return rows * (p.d + 4) * sizeof(float);
+}
+
+void plan_attention(const AttnParams& p, AttnPlan& plan) {
+  plan.dp = p.d <= 32 ? 32 : p.d <= 64 ? 64 : p.d <= 96 ? 96 : 128;
+  const int64_t rows = (int64_t)p.sq * p.group;
+  plan.few = rows <= 32;
+  plan.splits = 1;
+  plan.forward_bytes = 0;
+  if (plan.few) {
+    // Blocks for every compute unit, of 256 keys (two tiles a wave) at least.
+    const int64_t units = (int64_t)p.batch * p.kv_heads;
+    int64_t splits = units > 0 ? (512 + units - 1) / units : 1;
+    const int64_t most = p.sk / 256;
+    splits = splits > most ? most : splits;
+    plan.splits = splits < 1 ? 1 : (int)splits;
+    if (plan.splits > 1) plan.forward_bytes = split_bytes(p, plan.splits);
+  }
+  // lse * log2(e) and rowsum(do * o), rows padded to whole tiles
+  plan.backward_bytes = (size_t)p.batch * p.heads * ((p.sq + 63) / 64 * 64) * 2 * sizeof(float);
+}
+
+int launch_attention_forward(const AttnParams& p, const AttnPlan& plan, const AttnArgs& a) {
+  AttnK k{};
+  k.p = p;
+  k.q = a.q; k.k = a.k; k.v = a.v;
+  k.q_lengths = a.q_lengths; k.k_lengths = a.k_lengths;
+  k.o = a.o; k.lse = a.lse;
+  k.c = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
+  k.tiles = (p.sq + 127) / 128;
+  k.splits = plan.splits;
+  k.rows = p.sq * p.group;
+  k.row_groups = (k.rows + 31) / 32;
+  if (plan.splits > 1) {
+    k.part_o = (float*)a.ws;
+    k.part_lse = k.part_o + (size_t)p.batch * p.kv_heads * plan.splits * k.rows * p.d;
+  }
+  const hipStream_t st = (hipStream_t)a.stream;
+  switch (plan.dp) {
+    case 32: return attention_forward_32(plan, k, st);
+    case 64: return attention_forward_64(plan, k, st);
+    case 96: return attention_forward_96(plan, k, st);
+    default: return attention_forward_128(plan, k, st);
+  }
+}
+#endif
+
+}  // namespace fc

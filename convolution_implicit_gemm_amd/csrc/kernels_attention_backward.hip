@@ -1,0 +1,354 @@
+// Attention, backward (include/fusedconv_transformer.h).  The probabilities are
+// recomputed from the scores and the forward pass's log-sum-exps.
+//
+// Three kernels, none with atomics: row sums of do * o; dk and dv by blocks of
+// keys that walk the queries; dq by blocks of queries that walk the keys.  The
+// scores and do v^T are computed twice, 7 products instead of 5, against the
+// 4 * q_len * head_dim bytes that every key block would otherwise add to dq in
+// memory, in an order that changes.
+//
+// Compiled once per head size the tiles are made for (FC_DP).
+#include <hip/hip_runtime.h>
+
+#include "attention_tile.h"
+#include "fusedconv.h"
+#include "internal.h"
+#include "transformer.h"
+
+namespace fc {
+
+struct AttnBwdK {
+  AttnParams p;
+  const void *q, *k, *v, *o, *dout;
+  const int32_t *q_lengths, *k_lengths;
+  const float* lse;
+  void *dq, *dk, *dv;
+  float *lse2, *delta;  // workspace [batch * heads][rows padded to 64]
+  float c;              // |scale| * log2(e), at least the least normal number
+  int32_t padded, q_tiles, k_tiles;
+};
+
+namespace {
+
+// lse2 = lse * log2(e); delta = rowsum(do * o).  Rows without a key, behind
+// the entry's queries or in the padding get lse2 = +inf: their probabilities
+// exp2(s - lse2) are then zero, and need no mask.  8 lanes a row.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
+  const AttnParams& p = a.p;
+  const int64_t at = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  if (at >= (int64_t)p.batch * p.heads * a.padded) return;
+  const int i = (int)(at % a.padded);
+  const int head = (int)(at / a.padded % p.heads), b = (int)(at / a.padded / p.heads);
+  const int nq = length_of(a.q_lengths, b, p.sq);
+  float s = 0.f, l2 = INFINITY;
+  if (i < nq) {
+    const T* o = (const T*)a.o + b * p.o.b + i * p.o.s + head * p.o.h;
+    const T* g = (const T*)a.dout + b * p.dout.b + i * p.dout.s + head * p.dout.h;
+    for (int d = (threadIdx.x & 7) * 8; d < p.d; d += 64) {
+      const frag_t<T> x = *reinterpret_cast<const frag_t<T>*>(o + d);
+      const frag_t<T> y = *reinterpret_cast<const frag_t<T>*>(g + d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += (float)x[j] * (float)y[j];
+    }
+    const float l = a.lse[((int64_t)b * p.heads + head) * p.sq + i];
+    if (l != -INFINITY) l2 = l * kLog2e;
+  }
+#pragma unroll
+  for (int off = 1; off < 8; off <<= 1) s += __shfl_xor(s, off, 64);
+  if ((threadIdx.x & 7) == 0) {
+    a.lse2[at] = l2;
+    a.delta[at] = l2 == INFINITY ? 0.f : s;
+  }
+}
+
+// ------------------------------------------------------------------ dk, dv
+// A block has 128 keys of one key head, 32 a wave: K and V rows as B operands,
+// so a lane holds one key and 16 of a tile's queries; dk^T and dv^T stay in
+// registers while the block walks the queries of every head that shares the
+// key head, BQ at a time, double-buffered.
+template <typename T, int DP>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dkdv(AttnBwdK a) {
+  using L = Tile<T, DP>;
+  constexpr int BQ = sizeof(T) == 2 ? 64 : 32;
+  constexpr int NT = DP / 32, NS = DP / 16;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  T* tiles = (T*)lds;                                    // [2][Q, dO][BQ * DP]
+  float* rows = (float*)(lds + 4 * L::bytes(BQ));        // [2][lse2, delta][64]
+
+  const AttnParams& p = a.p;
+  const int total = p.batch * p.kv_heads * a.k_tiles;
+  int item = xcd_item(blockIdx.x, total);
+  if (item >= total) return;
+  const int tile_k = item % a.k_tiles;  // the first keys first: a causal window shows them to most
+  item /= a.k_tiles;
+  const int kvh = item % p.kv_heads, b = item / p.kv_heads;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const Sight see{length_of(a.q_lengths, b, p.sq), length_of(a.k_lengths, b, p.sk), p.left, p.right};
+  const int key0 = tile_k * 128, last_key = min(key0 + 127, see.nk - 1);
+  const int w0 = key0 + wave * 32, w1 = min(w0 + 31, see.nk - 1);
+  const int j = w0 + (lane & 31);
+
+  const int first = key0 < see.nk ? see.qlo(key0) & ~(BQ - 1) : 0;
+  const int end = key0 < see.nk ? see.qhi(last_key) : 0;
+  const int wave_lo = see.qlo(w0), wave_hi = w0 < see.nk ? see.qhi(w1) : 0;
+  const int all_lo = see.qlo(w1), all_hi = see.qhi(w0);
+  const int lo = see.qlo(j), hi = see.qhi(j);
+
+  f32x16 dk[NT], dv[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) dk[t] = dv[t] = zero16();
+
+  L::template clear_padding<4 * BQ>(tiles, p.d, threadIdx.x, 256);
+  if (first < end) {
+    frag_t<T> kf[NS], vf[NS];
+    const int ji = min(j, see.nk - 1);
+    load_operand<T, DP>(kf, (const T*)a.k + b * p.k.b + ji * p.k.s + kvh * p.k.h, p.d, p.scale < 0.f);
+    load_operand<T, DP>(vf, (const T*)a.v + b * p.v.b + ji * p.v.s + kvh * p.v.h, p.d, false);
+
+    auto fetch = [&](int g, int row0, int n) {
+      const int head = kvh * p.group + g;
+      const int last = see.nq - 1 - row0;
+      const T* q = (const T*)a.q + b * p.q.b + head * p.q.h + row0 * p.q.s;
+      const T* o = (const T*)a.dout + b * p.dout.b + head * p.dout.h + row0 * p.dout.s;
+      L::template fetch<BQ, 4>(tiles + n * 2 * BQ * DP, q, p.q.s, last, p.d, wave);
+      L::template fetch<BQ, 4>(tiles + (n * 2 + 1) * BQ * DP, o, p.dout.s, last, p.d, wave);
+      if (wave < 2 && lane < BQ) {
+        const float* src = (wave ? a.delta : a.lse2) + ((int64_t)b * p.heads + head) * a.padded + row0;
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(src + lane),
+            (__attribute__((address_space(3))) void*)(rows + n * 128 + wave * 64), 4, 0, 0);
+      }
+    };
+    __syncthreads();
+    fetch(0, first, 0);
+    int n = 0, g = 0, row0 = first;
+    while (g < p.group) {
+      int next = row0 + BQ, gn = g;
+      if (next >= end) next = first, ++gn;
+      tile_barrier();
+      if (gn < p.group) fetch(gn, next, n ^ 1);
+      if (row0 < wave_hi && row0 + BQ > wave_lo) {
+        const T* qt = tiles + n * 2 * BQ * DP;
+        const T* ot = qt + BQ * DP;
+        const bool masked = row0 < all_lo || row0 + BQ > all_hi;
+#pragma unroll
+        for (int r = 0; r < BQ; r += 32) {
+          f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+          for (int d = 0; d < NS; ++d) {
+            s = mma(L::load_rows(qt, r, d), kf[d], s);
+            dp = mma(L::load_rows(ot, r, d), vf[d], dp);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float l2 = rows[n * 128 + r + c_row(i, h)];
+            const float delta = rows[n * 128 + 64 + r + c_row(i, h)];
+            s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.c, -l2));
+            if (masked) {
+              const int at = row0 + r + c_row(i, h);
+              if (at < lo || at >= hi) s[i] = 0.f;
+            }
+            dp[i] = s[i] * (dp[i] - delta);
+          }
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            const frag_t<T> pf = to_frag<T>(s, d), df = to_frag<T>(dp, d);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              dv[t] = mma(L::load_columns(ot, r + 16 * d, t), pf, dv[t]);
+              dk[t] = mma(L::load_columns(qt, r + 16 * d, t), df, dk[t]);
+            }
+          }
+        }
+      }
+      g = gn;
+      row0 = next;
+      n ^= 1;
+    }
+  }
+  if (j >= p.sk) return;
+  const float keep = j < see.nk ? 1.f : 0.f;
+  T* dkp = (T*)a.dk + b * p.dk.b + j * p.dk.s + kvh * p.dk.h;
+  T* dvp = (T*)a.dv + b * p.dv.b + j * p.dv.s + kvh * p.dv.h;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (32 * t + 8 * g >= p.d) continue;
+      Piece<T, 4> pk, pv;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        pk.v[e] = to_type<T>(keep != 0.f ? dk[t][4 * g + e] * p.scale : 0.f);
+        pv.v[e] = to_type<T>(keep != 0.f ? dv[t][4 * g + e] : 0.f);
+      }
+      store_piece<T, 4>(dkp + 32 * t + 8 * g + 4 * h, pk);
+      store_piece<T, 4>(dvp + 32 * t + 8 * g + 4 * h, pv);
+    }
+}
+
+// ---------------------------------------------------------------------- dq
+// A block has 128 queries of one head, 32 a wave, and walks the keys as the
+// forward pass does: Q and dO rows are the B operands, a lane has one query.
+template <typename T, int DP>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttnBwdK a) {
+  using L = Tile<T, DP>;
+  constexpr int BN = sizeof(T) == 2 ? 64 : 32;
+  constexpr int NT = DP / 32, NS = DP / 16;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  T* tiles = (T*)lds;  // [2][K, V][BN * DP]
+
+  const AttnParams& p = a.p;
+  const int total = p.batch * p.heads * a.q_tiles;
+  int item = xcd_item(blockIdx.x, total);
+  if (item >= total) return;
+  const int tile_q = a.q_tiles - 1 - item % a.q_tiles;
+  item /= a.q_tiles;
+  const int head = item % p.heads, b = item / p.heads, kvh = head / p.group;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const Sight see{length_of(a.q_lengths, b, p.sq), length_of(a.k_lengths, b, p.sk), p.left, p.right};
+  const int row0 = tile_q * 128, last_row = min(row0 + 127, see.nq - 1);
+  const int w0 = row0 + wave * 32, w1 = min(w0 + 31, see.nq - 1);
+  const int i = w0 + (lane & 31);
+
+  const int first = row0 < see.nq ? see.lo(row0) & ~(BN - 1) : 0;
+  const int end = row0 < see.nq ? see.hi(last_row) : 0;
+  const int wave_lo = see.lo(w0), wave_hi = w0 < see.nq ? see.hi(w1) : 0;
+  const int all_lo = see.lo(w1), all_hi = w0 + 31 < see.nq ? see.hi(w0) : 0;
+  const int lo = see.lo(i), hi = see.hi(i);
+
+  f32x16 dq[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) dq[t] = zero16();
+  L::template clear_padding<4 * BN>(tiles, p.d, threadIdx.x, 256);
+  if (first < end) {
+    const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
+    const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
+    auto fetch = [&](int key0, int n) {
+      const int last = see.nk - 1 - key0;
+      L::template fetch<BN, 4>(tiles + n * 2 * BN * DP, kp + key0 * p.k.s, p.k.s, last, p.d, wave);
+      L::template fetch<BN, 4>(tiles + (n * 2 + 1) * BN * DP, vp + key0 * p.v.s, p.v.s, last, p.d, wave);
+    };
+    frag_t<T> qf[NS], of[NS];
+    const int qi = min(i, see.nq - 1);
+    load_operand<T, DP>(qf, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d, p.scale < 0.f);
+    load_operand<T, DP>(of, (const T*)a.dout + b * p.dout.b + qi * p.dout.s + head * p.dout.h, p.d, false);
+    const int64_t at = ((int64_t)b * p.heads + head) * a.padded;
+    const float l2 = i < a.padded ? a.lse2[at + i] : INFINITY;
+    const float delta = i < a.padded ? a.delta[at + i] : 0.f;
+    __syncthreads();
+    fetch(first, 0);
+    int n = 0;
+    for (int key0 = first; key0 < end; key0 += BN, n ^= 1) {
+      tile_barrier();
+      if (key0 + BN < end) fetch(key0 + BN, n ^ 1);
+      if (key0 >= wave_hi || key0 + BN <= wave_lo) continue;
+      const T* kt = tiles + n * 2 * BN * DP;
+      const T* vt = kt + BN * DP;
+      const bool masked = key0 < all_lo || key0 + BN > all_hi;
+#pragma unroll
+      for (int r = 0; r < BN; r += 32) {
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int d = 0; d < NS; ++d) {
+          s = mma(L::load_rows(kt, r, d), qf[d], s);
+          dp = mma(L::load_rows(vt, r, d), of[d], dp);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float pr = __builtin_amdgcn_exp2f(fmaf(s[e], a.c, -l2));
+          if (masked) {
+            const int key = key0 + r + c_row(e, h);
+            if (key < lo || key >= hi) pr = 0.f;
+          }
+          dp[e] = pr * (dp[e] - delta);
+        }
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const frag_t<T> df = to_frag<T>(dp, d);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) dq[t] = mma(L::load_columns(kt, r + 16 * d, t), df, dq[t]);
+        }
+      }
+    }
+  }
+  if (i >= p.sq) return;
+  T* out = (T*)a.dq + b * p.dq.b + i * p.dq.s + head * p.dq.h;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (32 * t + 8 * g >= p.d) continue;
+      Piece<T, 4> po;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) po.v[e] = to_type<T>(i < see.nq ? dq[t][4 * g + e] * p.scale : 0.f);
+      store_piece<T, 4>(out + 32 * t + 8 * g + 4 * h, po);
+    }
+}
+
+#define FC_DP_NAME(name) FC_CAT(name, FC_DP)
+
+}  // namespace
+
+int FC_DP_NAME(attention_backward_)(const AttnPlan& plan, const AttnBwdK& k, hipStream_t st) {
+  int rc = FUSEDCONV_OK;
+  with_type(plan.dtype, [&](auto tag) {
+    using T = typename decltype(tag)::type;
+    const AttnParams& p = k.p;
+    constexpr int rows = sizeof(T) == 2 ? 64 : 32;
+    constexpr int tile_bytes = 4 * Tile<T, FC_DP>::bytes(rows);
+    if (p.sq > 0)
+      hipLaunchKernelGGL((k_attention_rows<T>),
+                         dim3((unsigned)(((int64_t)p.batch * p.heads * k.padded + 31) / 32)),
+                         dim3(256), 0, st, k);
+    if (p.sk > 0) {
+      auto fn = k_attention_dkdv<T, FC_DP>;
+      constexpr int bytes = tile_bytes + 2 * 2 * 64 * (int)sizeof(float);
+      rc = set_max_dynamic_lds((const void*)fn, bytes);
+      if (rc != FUSEDCONV_OK) return;
+      hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.kv_heads * k.k_tiles)), dim3(256),
+                         bytes, st, k);
+    }
+    if (p.sq > 0) {
+      auto fn = k_attention_dq<T, FC_DP>;
+      rc = set_max_dynamic_lds((const void*)fn, tile_bytes);
+      if (rc != FUSEDCONV_OK) return;
+      hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.heads * k.q_tiles)), dim3(256),
+                         tile_bytes, st, k);
+    }
+  });
+  if (rc != FUSEDCONV_OK) return rc;
+  return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH;
+}
+
+#if FC_DP == 32
+int attention_backward_64(const AttnPlan&, const AttnBwdK&, hipStream_t);
+int attention_backward_96(const AttnPlan&, const AttnBwdK&, hipStream_t);
+int attention_backward_128(const AttnPlan&, const AttnBwdK&, hipStream_t);
+
+int launch_attention_backward(const AttnParams& p, const AttnPlan& plan, const AttnArgs& a) {
+  AttnBwdK k{};
+  k.p = p;
+  k.q = a.q; k.k = a.k; k.v = a.v; k.o = a.o_in; k.dout = a.dout;
+  k.q_lengths = a.q_lengths; k.k_lengths = a.k_lengths;
+  k.lse = a.lse_in;
+  k.dq = a.dq; k.dk = a.dk; k.dv = a.dv;
+  k.padded = (p.sq + 63) / 64 * 64;
+  k.lse2 = (float*)a.ws;
+  k.delta = k.lse2 + (size_t)p.batch * p.heads * k.padded;
+  k.c = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
+  k.q_tiles = (p.sq + 127) / 128;
+  k.k_tiles = (p.sk + 127) / 128;
+  const hipStream_t st = (hipStream_t)a.stream;
+  switch (plan.dp) {
+    case 32: return attention_backward_32(plan, k, st);
+    case 64: return attention_backward_64(plan, k, st);
+    case 96: return attention_backward_96(plan, k, st);
+    default: return attention_backward_128(plan, k, st);
+  }
+}
+#endif
+
+}  // namespace fc

@@ -1,0 +1,754 @@
+// Layer norm, forward and backward (include/fusedconv_transformer.h), over
+// token rows and over the channels of NCHW images.
+//
+// All four kernels are bound by HBM: they hold a row's values (NCHW: a pixel
+// tile's) in registers between the statistics and the result, so every value
+// is read once and written once.  The variance is the mean of squares about
+// the mean (a second pass over registers), not a difference of two sums, so a
+// large common offset costs no digits.
+//
+// Sizes whose rows do not fit the registers take the LOOP variants, which read
+// X again for each pass (from the caches, as a row is short next to them).
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "fusedconv.h"
+#include "transformer.h"
+#include "vec.h"
+
+namespace fc {
+namespace {
+
+struct NormK {
+  const void *x, *dy, *w, *b;
+  void* out;
+  float *mean, *rstd;
+  float* part;  // [gridDim.x][2][c]
+  int64_t x_stride, dy_stride;
+  int32_t n, c, inner;
+  int32_t tiles;  // NCHW: pixel tiles of one image
+  float eps;
+};
+
+constexpr int kLoopThreads = 256;
+
+// Sum over the TPR threads that share a row.  TPR <= 64: lanes of one wave.
+// Otherwise the whole block (TPR = blockDim.x): waves meet in LDS; the two
+// barriers also keep one call's values from the next one's.
+template <int TPR, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K]) {
+#pragma unroll
+  for (int off = 1; off < (TPR < 64 ? TPR : 64); off <<= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], off, 64);
+  if constexpr (TPR > 64) {
+    __shared__ float red[TPR / 64][K];
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) red[wave][k] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPR / 64; ++i) s += red[i][k];
+      v[k] = s;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------- token rows
+// TPR threads share a row and hold NCH pieces of V values each: thread t has
+// the pieces t, t + TPR, ...  256 threads a block.
+
+template <typename T, int V, int TPR, int NCH>
+__global__ __launch_bounds__(256) void k_norm_rows(NormK a) {
+  constexpr int RPB = 256 / TPR;
+  const int t = threadIdx.x % TPR;
+  const T* w = (const T*)a.w;
+  const T* b = (const T*)a.b;
+  for (int row = blockIdx.x * RPB + threadIdx.x / TPR; row < a.n; row += gridDim.x * RPB) {
+    const T* x = (const T*)a.x + (int64_t)row * a.x_stride;
+    Piece<T, V> px[NCH];
+    float sum[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int at = (t + i * TPR) * V;
+      if (at < a.c) px[i] = load_piece<T, V>(x + at);
+      else
+#pragma unroll
+        for (int j = 0; j < V; ++j) px[i].v[j] = (T)0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[0] += (float)px[i].v[j];
+    }
+    row_sum<TPR>(sum);
+    const float mean = sum[0] / (float)a.c;
+    float sq[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if ((t + i * TPR) * V < a.c)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = (float)px[i].v[j] - mean;
+          sq[0] += d * d;
+        }
+    row_sum<TPR>(sq);
+    const float rstd = 1.0f / sqrtf(sq[0] / (float)a.c + a.eps);
+    if (t == 0 && a.mean) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+    T* y = (T*)a.out + (int64_t)row * a.c;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int at = (t + i * TPR) * V;
+      if (at >= a.c) continue;
+      Piece<T, V> pw, pb, py;
+      if (w) pw = load_piece<T, V>(w + at);
+      if (b) pb = load_piece<T, V>(b + at);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float v = ((float)px[i].v[j] - mean) * rstd;
+        if (w) v *= (float)pw.v[j];
+        if (b) v += (float)pb.v[j];
+        py.v[j] = to_type<T>(v);
+      }
+      store_piece<T, V>(y + at, py);
+    }
+  }
+}
+
+// Backward.  A thread keeps its columns' sums of dy and dy * xh over the rows
+// its group visits; the block's groups then meet in LDS, one group after the
+// other, and the block writes one partial row of both.
+template <typename T, int V, int TPR, int NCH>
+__global__ __launch_bounds__(256) void k_norm_rows_bwd(NormK a) {
+  constexpr int RPB = 256 / TPR;
+  const int t = threadIdx.x % TPR;
+  const int group = threadIdx.x / TPR;
+  const T* w = (const T*)a.w;
+  float dw[NCH * V], db[NCH * V];
+  Piece<T, V> pw[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH * V; ++i) dw[i] = db[i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int at = (t + i * TPR) * V;
+    if (w && at < a.c) pw[i] = load_piece<T, V>(w + at);
+    else
+#pragma unroll
+      for (int j = 0; j < V; ++j) pw[i].v[j] = (T)1.f;
+  }
+  for (int row = blockIdx.x * RPB + group; row < a.n; row += gridDim.x * RPB) {
+    const T* x = (const T*)a.x + (int64_t)row * a.x_stride;
+    const T* dy = (const T*)a.dy + (int64_t)row * a.dy_stride;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    Piece<T, V> px[NCH], pd[NCH];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int at = (t + i * TPR) * V;
+      if (at < a.c) {
+        px[i] = load_piece<T, V>(x + at);
+        pd[i] = load_piece<T, V>(dy + at);
+      }
+    }
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if ((t + i * TPR) * V < a.c)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float xh = ((float)px[i].v[j] - mean) * rstd;
+          const float d = (float)pd[i].v[j];
+          const float g = d * (float)pw[i].v[j];
+          s[0] += g;
+          s[1] += g * xh;
+          dw[i * V + j] += d * xh;
+          db[i * V + j] += d;
+        }
+    row_sum<TPR>(s);
+    const float c1 = s[0] / (float)a.c, c2 = s[1] / (float)a.c;
+    T* dx = (T*)a.out + (int64_t)row * a.c;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int at = (t + i * TPR) * V;
+      if (at >= a.c) continue;
+      Piece<T, V> po;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float xh = ((float)px[i].v[j] - mean) * rstd;
+        const float g = (float)pd[i].v[j] * (float)pw[i].v[j];
+        po.v[j] = to_type<T>(rstd * (g - c1 - xh * c2));
+      }
+      store_piece<T, V>(dx + at, po);
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
+  if constexpr (RPB == 1) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int at = (t + i * TPR) * V + j;
+        if (at < a.c) {
+          out[at] = dw[i * V + j];
+          out[a.c + at] = db[i * V + j];
+        }
+      }
+  } else {
+    __shared__ float acc[2][NCH * V][TPR];
+    for (int g = 0; g < RPB; ++g) {
+      if (g == group)
+#pragma unroll
+        for (int i = 0; i < NCH * V; ++i) {
+          acc[0][i][t] = (g ? acc[0][i][t] : 0.f) + dw[i];
+          acc[1][i][t] = (g ? acc[1][i][t] : 0.f) + db[i];
+        }
+      __syncthreads();
+    }
+    for (int at = threadIdx.x; at < a.c; at += 256) {
+      const int piece = at / V, j = (piece / TPR) * V + at % V;
+      out[at] = acc[0][j][piece % TPR];
+      out[a.c + at] = acc[1][j][piece % TPR];
+    }
+  }
+}
+
+// Rows too long for the registers: one block a row, X read once per pass.
+template <typename T>
+__global__ __launch_bounds__(kLoopThreads) void k_norm_rows_loop(NormK a) {
+  for (int row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const T* x = (const T*)a.x + (int64_t)row * a.x_stride;
+    float s[1] = {0.f}, sq[1] = {0.f};
+    for (int i = threadIdx.x; i < a.c; i += kLoopThreads) s[0] += (float)x[i];
+    row_sum<kLoopThreads>(s);
+    const float mean = s[0] / (float)a.c;
+    for (int i = threadIdx.x; i < a.c; i += kLoopThreads) {
+      const float d = (float)x[i] - mean;
+      sq[0] += d * d;
+    }
+    row_sum<kLoopThreads>(sq);
+    const float rstd = 1.0f / sqrtf(sq[0] / (float)a.c + a.eps);
+    if (threadIdx.x == 0 && a.mean) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+    T* y = (T*)a.out + (int64_t)row * a.c;
+    for (int i = threadIdx.x; i < a.c; i += kLoopThreads) {
+      float v = ((float)x[i] - mean) * rstd;
+      if (a.w) v *= (float)((const T*)a.w)[i];
+      if (a.b) v += (float)((const T*)a.b)[i];
+      y[i] = to_type<T>(v);
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kLoopThreads) void k_norm_rows_bwd_loop(NormK a) {
+  for (int row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const T* x = (const T*)a.x + (int64_t)row * a.x_stride;
+    const T* dy = (const T*)a.dy + (int64_t)row * a.dy_stride;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s[2] = {0.f, 0.f};
+    for (int i = threadIdx.x; i < a.c; i += kLoopThreads) {
+      const float g = (float)dy[i] * (a.w ? (float)((const T*)a.w)[i] : 1.f);
+      s[0] += g;
+      s[1] += g * ((float)x[i] - mean) * rstd;
+    }
+    row_sum<kLoopThreads>(s);
+    const float c1 = s[0] / (float)a.c, c2 = s[1] / (float)a.c;
+    T* dx = (T*)a.out + (int64_t)row * a.c;
+    for (int i = threadIdx.x; i < a.c; i += kLoopThreads) {
+      const float g = (float)dy[i] * (a.w ? (float)((const T*)a.w)[i] : 1.f);
+      dx[i] = to_type<T>(rstd * (g - c1 - ((float)x[i] - mean) * rstd * c2));
+    }
+  }
+}
+
+// Column sums for the loop form: block (x: row range, y: 256 columns).
+template <typename T>
+__global__ __launch_bounds__(kLoopThreads) void k_norm_columns(NormK a) {
+  const int col = blockIdx.y * kLoopThreads + threadIdx.x;
+  if (col >= a.c) return;
+  float dw = 0.f, db = 0.f;
+  for (int row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const float d = (float)((const T*)a.dy)[(int64_t)row * a.dy_stride + col];
+    const float x = (float)((const T*)a.x)[(int64_t)row * a.x_stride + col];
+    dw += d * ((x - a.mean[row]) * a.rstd[row]);
+    db += d;
+  }
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
+  out[col] = dw;
+  out[a.c + col] = db;
+}
+
+// ------------------------------------------------------------- NCHW images
+// A block has a tile of PL * V consecutive pixels of one image, all channels:
+// lane p of PL holds V pixels, channel group g of CG the channels g, g + CG,
+// ...  A wave's accesses are 64 / PL channels of PL * V * sizeof(T) bytes
+// (128 for the vector forms) each.
+
+constexpr int kPlaneThreads = 512;
+
+// Sum over the channel groups of the block, for every pixel of the tile.
+template <int PL, int V, int K>
+__device__ __forceinline__ void pixel_sum(float (&v)[K][V]) {
+#pragma unroll
+  for (int off = PL; off < 64; off <<= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[k][j] += __shfl_xor(v[k][j], off, 64);
+  __shared__ float red[kPlaneThreads / 64][K][V][PL];
+  const int wave = threadIdx.x >> 6, p = threadIdx.x % PL;
+  if ((threadIdx.x & 63) < PL)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) red[wave][k][j][p] = v[k][j];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPlaneThreads / 64; ++i) s += red[i][k][j][p];
+      v[k][j] = s;
+    }
+  __syncthreads();
+}
+
+// NCH: channels a thread holds; 0: any number, read again for each pass.
+template <typename T, int V, int PL, int NCH>
+__global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
+  constexpr int CG = kPlaneThreads / PL;
+  const int p = threadIdx.x % PL, g = threadIdx.x / PL;
+  const int image = blockIdx.x / a.tiles;
+  const int pixel = ((blockIdx.x - image * a.tiles) * PL + p) * V;
+  const bool live = pixel < a.inner;
+  const T* x = (const T*)a.x + (int64_t)image * a.x_stride + pixel;
+  T* y = (T*)a.out + (int64_t)image * a.c * a.inner + pixel;
+  const T* w = (const T*)a.w;
+  const T* b = (const T*)a.b;
+  constexpr int HELD = NCH ? NCH : 1;
+  Piece<T, V> px[HELD];
+  float sum[1][V], sq[1][V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) sum[0][j] = sq[0][j] = 0.f;
+  auto each = [&](auto&& f) {
+    if constexpr (NCH > 0) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (live && g + i * CG < a.c) f(i, g + i * CG);
+    } else {
+      if (live)
+        for (int ch = g; ch < a.c; ch += CG) {
+          px[0] = load_piece<T, V>(x + (int64_t)ch * a.inner);
+          f(0, ch);
+        }
+    }
+  };
+  if constexpr (NCH > 0)
+    each([&](int i, int ch) { px[i] = load_piece<T, V>(x + (int64_t)ch * a.inner); });
+  each([&](int i, int) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[0][j] += (float)px[i].v[j];
+  });
+  pixel_sum<PL, V, 1>(sum);
+  float mean[V], rstd[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) mean[j] = sum[0][j] / (float)a.c;
+  each([&](int i, int) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float d = (float)px[i].v[j] - mean[j];
+      sq[0][j] += d * d;
+    }
+  });
+  pixel_sum<PL, V, 1>(sq);
+#pragma unroll
+  for (int j = 0; j < V; ++j) rstd[j] = 1.0f / sqrtf(sq[0][j] / (float)a.c + a.eps);
+  if (g == 0 && live && a.mean) {
+    const int64_t at = (int64_t)image * a.inner + pixel;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      a.mean[at + j] = mean[j];
+      a.rstd[at + j] = rstd[j];
+    }
+  }
+  each([&](int i, int ch) {
+    const float wc = w ? (float)w[ch] : 1.f, bc = b ? (float)b[ch] : 0.f;
+    Piece<T, V> py;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      py.v[j] = to_type<T>(((float)px[i].v[j] - mean[j]) * rstd[j] * wc + bc);
+    store_piece<T, V>(y + (int64_t)ch * a.inner, py);
+  });
+}
+
+// Backward: blocks walk the tiles of all images; a thread keeps the sums of
+// its channels over its own pixels, the PL lanes of a channel meet at the end.
+template <typename T, int V, int PL, int NCH>
+__global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
+  constexpr int CG = kPlaneThreads / PL;
+  const int p = threadIdx.x % PL, g = threadIdx.x / PL;
+  const T* w = (const T*)a.w;
+  float dw[NCH], db[NCH], wc[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    dw[i] = db[i] = 0.f;
+    wc[i] = w && g + i * CG < a.c ? (float)w[g + i * CG] : 1.f;
+  }
+  const int64_t all = (int64_t)a.n * a.tiles;
+  for (int64_t tile = blockIdx.x; tile < all; tile += gridDim.x) {
+    const int image = (int)(tile / a.tiles);
+    const int pixel = ((int)(tile - (int64_t)image * a.tiles) * PL + p) * V;
+    const bool live = pixel < a.inner;
+    const T* x = (const T*)a.x + (int64_t)image * a.x_stride + pixel;
+    const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride + pixel;
+    T* dx = (T*)a.out + (int64_t)image * a.c * a.inner + pixel;
+    Piece<T, V> px[NCH], pd[NCH];
+    float mean[V], rstd[V], s[2][V];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if (live && g + i * CG < a.c) {
+        px[i] = load_piece<T, V>(x + (int64_t)(g + i * CG) * a.inner);
+        pd[i] = load_piece<T, V>(dy + (int64_t)(g + i * CG) * a.inner);
+      }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      mean[j] = live ? a.mean[(int64_t)image * a.inner + pixel + j] : 0.f;
+      rstd[j] = live ? a.rstd[(int64_t)image * a.inner + pixel + j] : 0.f;
+      s[0][j] = s[1][j] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if (live && g + i * CG < a.c)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float xh = ((float)px[i].v[j] - mean[j]) * rstd[j];
+          const float d = (float)pd[i].v[j];
+          s[0][j] += d * wc[i];
+          s[1][j] += d * wc[i] * xh;
+          dw[i] += d * xh;
+          db[i] += d;
+        }
+    pixel_sum<PL, V, 2>(s);
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if (live && g + i * CG < a.c) {
+        Piece<T, V> po;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float xh = ((float)px[i].v[j] - mean[j]) * rstd[j];
+          const float gr = (float)pd[i].v[j] * wc[i];
+          po.v[j] = to_type<T>(rstd[j] * (gr - s[0][j] / (float)a.c - xh * (s[1][j] / (float)a.c)));
+        }
+        store_piece<T, V>(dx + (int64_t)(g + i * CG) * a.inner, po);
+      }
+  }
+  if (!a.part) return;
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+#pragma unroll
+    for (int off = 1; off < PL; off <<= 1) {
+      dw[i] += __shfl_xor(dw[i], off, 64);
+      db[i] += __shfl_xor(db[i], off, 64);
+    }
+    if (p == 0 && g + i * CG < a.c) {
+      out[g + i * CG] = dw[i];
+      out[a.c + g + i * CG] = db[i];
+    }
+  }
+}
+
+// Any number of channels: X and dY read again for the second pass, and dx
+// alone; the weight gradients come from k_norm_plane_sums.
+template <typename T, int V, int PL>
+__global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd_loop(NormK a) {
+  constexpr int CG = kPlaneThreads / PL;
+  const int p = threadIdx.x % PL, g = threadIdx.x / PL;
+  const T* w = (const T*)a.w;
+  const int image = blockIdx.x / a.tiles;
+  const int pixel = ((blockIdx.x - image * a.tiles) * PL + p) * V;
+  const bool live = pixel < a.inner;
+  const T* x = (const T*)a.x + (int64_t)image * a.x_stride + pixel;
+  const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride + pixel;
+  T* dx = (T*)a.out + (int64_t)image * a.c * a.inner + pixel;
+  float mean[V], rstd[V], s[2][V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    mean[j] = live ? a.mean[(int64_t)image * a.inner + pixel + j] : 0.f;
+    rstd[j] = live ? a.rstd[(int64_t)image * a.inner + pixel + j] : 0.f;
+    s[0][j] = s[1][j] = 0.f;
+  }
+  for (int ch = g; live && ch < a.c; ch += CG) {
+    const Piece<T, V> px = load_piece<T, V>(x + (int64_t)ch * a.inner);
+    const Piece<T, V> pd = load_piece<T, V>(dy + (int64_t)ch * a.inner);
+    const float wc = w ? (float)w[ch] : 1.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float gr = (float)pd.v[j] * wc;
+      s[0][j] += gr;
+      s[1][j] += gr * ((float)px.v[j] - mean[j]) * rstd[j];
+    }
+  }
+  pixel_sum<PL, V, 2>(s);
+  for (int ch = g; live && ch < a.c; ch += CG) {
+    const Piece<T, V> px = load_piece<T, V>(x + (int64_t)ch * a.inner);
+    const Piece<T, V> pd = load_piece<T, V>(dy + (int64_t)ch * a.inner);
+    const float wc = w ? (float)w[ch] : 1.f;
+    Piece<T, V> po;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float xh = ((float)px.v[j] - mean[j]) * rstd[j];
+      po.v[j] = to_type<T>(rstd[j] * ((float)pd.v[j] * wc - s[0][j] / (float)a.c -
+                                      xh * (s[1][j] / (float)a.c)));
+    }
+    store_piece<T, V>(dx + (int64_t)ch * a.inner, po);
+  }
+}
+
+// One channel (blockIdx.y) over the images blockIdx.x, + gridDim.x, ...
+template <typename T>
+__global__ __launch_bounds__(kLoopThreads) void k_norm_plane_sums(NormK a) {
+  const int ch = blockIdx.y;
+  float s[2] = {0.f, 0.f};
+  for (int image = blockIdx.x; image < a.n; image += gridDim.x) {
+    const T* x = (const T*)a.x + (int64_t)image * a.x_stride + (int64_t)ch * a.inner;
+    const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride + (int64_t)ch * a.inner;
+    const float* mean = a.mean + (int64_t)image * a.inner;
+    const float* rstd = a.rstd + (int64_t)image * a.inner;
+    for (int i = threadIdx.x; i < a.inner; i += kLoopThreads) {
+      const float d = (float)dy[i];
+      s[0] += d * (((float)x[i] - mean[i]) * rstd[i]);
+      s[1] += d;
+    }
+  }
+  row_sum<kLoopThreads>(s);
+  if (threadIdx.x == 0) {
+    float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
+    out[ch] = s[0];
+    out[a.c + ch] = s[1];
+  }
+}
+
+// ------------------------------------------------------------- weight gradients
+// part [blocks][2][c] -> dw[c], db[c]: 64 columns a block, 16 threads a
+// column, each a strided share of the blocks, joined in LDS in a fixed order.
+__global__ __launch_bounds__(1024) void k_norm_join(const float* part, int blocks, int c, float* dw,
+                                                    float* db) {
+  __shared__ float acc[16][64];
+  const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (col < 2 * c)
+#pragma unroll 4
+    for (int i = share; i < blocks; i += 16) s += part[(int64_t)i * 2 * c + col];
+  acc[share][lane] = s;
+  __syncthreads();
+  if (share == 0 && col < 2 * c) {
+    for (int i = 1; i < 16; ++i) s += acc[i][lane];
+    if (col < c) {
+      if (dw) dw[col] = s;
+    } else if (db) {
+      db[col - c] = s;
+    }
+  }
+}
+
+// Nothing to sum (n = 0): the gradients of the weights are zero.
+__global__ void k_norm_zero(float* dw, float* db, int c) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < c) {
+    if (dw) dw[i] = 0.f;
+    if (db) db[i] = 0.f;
+  }
+}
+
+// ------------------------------------------------------------- variants
+struct NormPlan {
+  bool planes, loop;
+  int v;        // values an access moves
+  int tpr;      // rows: threads a row; planes: pixel lanes
+  int nch;      // pieces (planes: channels) a thread holds
+  int blocks;   // backward: blocks that leave a partial
+  int tiles;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The wide form needs every row (plane) to start on a 16-byte border and to
+// be whole pieces; otherwise single values are moved.
+NormPlan plan_norm(const NormProblem& p, bool backward) {
+  NormPlan q{};
+  const int es = p.dtype == FUSEDCONV_F32 ? 4 : 2;
+  q.planes = p.inner > 1;
+  const int wide = 16 / es;
+  const int64_t run = q.planes ? p.inner : p.c;
+  const bool strided = p.x_stride % wide || (backward && p.dy_stride % wide);
+  q.v = run % wide == 0 && !strided ? wide : 1;
+  if (!q.planes) {
+    const int64_t pieces = ceil_div(p.c, q.v);
+    // Up to 64 pieces a row: the smallest power of two of lanes, one piece
+    // each.  Up to four pieces a lane, one wave a row (no barrier); then one
+    // block a row.
+    q.tpr = 8;
+    while (q.tpr < 64 && q.tpr < pieces) q.tpr *= 2;
+    q.nch = 1;
+    if (pieces > 64) {
+      q.tpr = pieces <= 256 ? 64 : 256;
+      while (q.nch * q.tpr < pieces) q.nch *= 2;
+    }
+    q.loop = q.nch > 8;
+    const int64_t rows_a_block = q.loop ? 1 : 256 / q.tpr;
+    // 1024 partial rows at most: enough waves to fill the chip (4 blocks a
+    // CU), and the partials stay a few percent of what a large call reads.
+    q.blocks = (int)(ceil_div(p.n, rows_a_block) < 1024 ? ceil_div(p.n, rows_a_block) : 1024);
+    if (q.loop && q.blocks > 64) q.blocks = 64;
+    return q;
+  }
+  q.tpr = q.v == 1 ? 32 : 8;
+  const int cg = kPlaneThreads / q.tpr;
+  q.nch = 1;
+  while (q.nch * cg < p.c) q.nch = q.nch < 4 ? q.nch * 2 : q.nch + 4;
+  const int most = 16;
+  q.loop = q.nch > most;
+  q.tiles = (int)ceil_div(p.inner, (int64_t)q.tpr * q.v);
+  const int64_t all = p.n * q.tiles;
+  q.blocks = (int)(all < 512 ? all : 512);
+  if (q.loop && q.blocks > p.n) q.blocks = (int)p.n;
+  if (q.loop && q.blocks > 64) q.blocks = 64;
+  return q;
+}
+
+NormK kernel_args(const NormProblem& p, const NormArgs& a, const NormPlan& q) {
+  NormK k{};
+  k.x = a.x; k.dy = a.dy; k.w = a.w; k.b = a.b; k.out = a.out;
+  k.mean = a.mean; k.rstd = a.rstd;
+  k.part = a.dw || a.db ? a.part : nullptr;
+  k.x_stride = p.x_stride; k.dy_stride = p.dy_stride;
+  k.n = (int32_t)p.n; k.c = (int32_t)p.c; k.inner = (int32_t)p.inner;
+  k.tiles = q.tiles;
+  k.eps = p.eps;
+  return k;
+}
+
+template <int I>
+using int_c = std::integral_constant<int, I>;
+
+// f(V, TPR, NCH) as compile-time constants for a register-held row plan.
+template <typename T, typename F>
+void with_rows(const NormPlan& q, F&& f) {
+  auto pick = [&](auto v) {
+    if (q.tpr == 8) f(v, int_c<8>{}, int_c<1>{});
+    else if (q.tpr == 16) f(v, int_c<16>{}, int_c<1>{});
+    else if (q.tpr == 32) f(v, int_c<32>{}, int_c<1>{});
+    else if (q.tpr == 64 && q.nch == 1) f(v, int_c<64>{}, int_c<1>{});
+    else if (q.tpr == 64 && q.nch == 2) f(v, int_c<64>{}, int_c<2>{});
+    else if (q.tpr == 64) f(v, int_c<64>{}, int_c<4>{});
+    else if (q.nch == 2) f(v, int_c<256>{}, int_c<2>{});
+    else if (q.nch == 4) f(v, int_c<256>{}, int_c<4>{});
+    else f(v, int_c<256>{}, int_c<8>{});
+  };
+  if (q.v == 1) pick(int_c<1>{});
+  else pick(int_c<16 / sizeof(T)>{});
+}
+
+// f(V, PL, NCH) for a plane plan; NCH = 0: the looped form.
+template <typename T, typename F>
+void with_planes(const NormPlan& q, F&& f) {
+  auto pick = [&](auto v, auto pl) {
+    if (q.loop) f(v, pl, int_c<0>{});
+    else if (q.nch == 1) f(v, pl, int_c<1>{});
+    else if (q.nch == 2) f(v, pl, int_c<2>{});
+    else if (q.nch == 4) f(v, pl, int_c<4>{});
+    else if (q.nch == 8) f(v, pl, int_c<8>{});
+    else if (q.nch == 12) f(v, pl, int_c<12>{});
+    else f(v, pl, int_c<16>{});
+  };
+  if (q.v == 1) pick(int_c<1>{}, int_c<32>{});
+  else pick(int_c<16 / sizeof(T)>{}, int_c<8>{});
+}
+
+int status() { return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH; }
+
+}  // namespace
+
+size_t norm_workspace(const NormProblem& p) {
+  if (p.n == 0) return 0;
+  return (size_t)plan_norm(p, true).blocks * 2 * p.c * sizeof(float);
+}
+
+int launch_norm_forward(const NormProblem& p, const NormArgs& a) {
+  const NormPlan q = plan_norm(p, false);
+  const NormK k = kernel_args(p, a, q);
+  const hipStream_t st = (hipStream_t)a.stream;
+  with_type(p.dtype, [&](auto tag) {
+    using T = typename decltype(tag)::type;
+    if (q.planes)
+      with_planes<T>(q, [&](auto v, auto pl, auto nch) {
+        hipLaunchKernelGGL((k_norm_planes<T, v, pl, nch>), dim3((unsigned)(p.n * q.tiles)),
+                           dim3(kPlaneThreads), 0, st, k);
+      });
+    else if (q.loop)
+      hipLaunchKernelGGL((k_norm_rows_loop<T>), dim3((unsigned)p.n), dim3(kLoopThreads), 0, st, k);
+    else
+      with_rows<T>(q, [&](auto v, auto tpr, auto nch) {
+        hipLaunchKernelGGL((k_norm_rows<T, v, tpr, nch>),
+                           dim3((unsigned)ceil_div(p.n, 256 / tpr)), dim3(256), 0, st, k);
+      });
+  });
+  return status();
+}
+
+int launch_norm_backward(const NormProblem& p, const NormArgs& a) {
+  const hipStream_t st = (hipStream_t)a.stream;
+  if (p.n == 0) {
+    if (a.dw || a.db)
+      hipLaunchKernelGGL(k_norm_zero, dim3((unsigned)ceil_div(p.c, 256)), dim3(256), 0, st, a.dw,
+                         a.db, (int)p.c);
+    return status();
+  }
+  const NormPlan q = plan_norm(p, true);
+  const NormK k = kernel_args(p, a, q);
+  with_type(p.dtype, [&](auto tag) {
+    using T = typename decltype(tag)::type;
+    if (q.planes) {
+      with_planes<T>(q, [&](auto v, auto pl, auto nch) {
+        if constexpr (nch == 0) {
+          hipLaunchKernelGGL((k_norm_planes_bwd_loop<T, v, pl>), dim3((unsigned)(p.n * q.tiles)),
+                             dim3(kPlaneThreads), 0, st, k);
+          if (k.part)
+            hipLaunchKernelGGL((k_norm_plane_sums<T>), dim3(q.blocks, (unsigned)p.c),
+                               dim3(kLoopThreads), 0, st, k);
+        } else {
+          hipLaunchKernelGGL((k_norm_planes_bwd<T, v, pl, nch>), dim3(q.blocks),
+                             dim3(kPlaneThreads), 0, st, k);
+        }
+      });
+    } else if (q.loop) {
+      hipLaunchKernelGGL((k_norm_rows_bwd_loop<T>), dim3((unsigned)p.n), dim3(kLoopThreads), 0, st, k);
+      if (k.part)
+        hipLaunchKernelGGL((k_norm_columns<T>),
+                           dim3(q.blocks, (unsigned)ceil_div(p.c, kLoopThreads)),
+                           dim3(kLoopThreads), 0, st, k);
+    } else {
+      with_rows<T>(q, [&](auto v, auto tpr, auto nch) {
+        hipLaunchKernelGGL((k_norm_rows_bwd<T, v, tpr, nch>), dim3(q.blocks), dim3(256), 0, st, k);
+      });
+    }
+  });
+  if (k.part)
+    hipLaunchKernelGGL(k_norm_join, dim3((unsigned)ceil_div(2 * p.c, 64)), dim3(1024), 0, st,
+                       k.part, q.blocks, (int)p.c, a.dw, a.db);
+  return status();
+}
+
+}  // namespace fc
