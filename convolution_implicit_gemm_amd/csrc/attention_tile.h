@@ -60,6 +60,19 @@ __device__ __forceinline__ f32x16 zero16() {
 // Row of value i of C for lanes of half h.
 __device__ __forceinline__ int c_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
+// C with row r's values set to v[r], for 32 values in LDS.
+__device__ __forceinline__ f32x16 load_c_rows(const float* v, int h) {
+  typedef float f4 __attribute__((ext_vector_type(4)));
+  f32x16 c;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const f4 x = *reinterpret_cast<const f4*>(v + 8 * g + 4 * h);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[4 * g + j] = x[j];
+  }
+  return c;
+}
+
 // max / sum of a lane's value with its partner's in the other half of the wave
 // (lanes l and l ^ 32 hold the two halves of a column of C).
 __device__ __forceinline__ float half_max(float v) {
@@ -69,6 +82,29 @@ __device__ __forceinline__ float half_max(float v) {
 __device__ __forceinline__ float half_sum(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The byte offset of a pointer into LDS.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// Copy BYTES (4 or 16) a lane from base + off to LDS at to + BYTES * lane; to
+// and base are the same for the whole wave.  In assembly because the compiler,
+// which cannot tell which LDS reads such a copy concerns, waits for it before
+// every transposing read; here the kernels wait (tile_barrier, vmcnt) where a
+// tile is needed.  The instruction has no output register, and its address is
+// read when it is issued.
+template <int BYTES>
+__device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t off, const void* base) {
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to),
+                 "v"(off), "s"(base)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to),
+                 "v"(off), "s"(base)
+                 : "memory");
 }
 
 // A tile of ROWS rows of DP values in LDS, in 16-byte chunks.  Chunk c of row r
@@ -131,32 +167,60 @@ struct Tile {
     }
   }
 
-  // Start copying ROWS rows of `src` (row stride `stride` values; d values a
-  // row) into the tile, WAVES waves sharing the work; rows past `last` repeat
-  // row `last`, so nothing outside the tensor is read.  The copy goes straight
-  // to LDS (64 chunks of 16 bytes an instruction, in lane order: the swizzle is
-  // applied to the address a lane fetches).  Chunks past d stay as they are:
-  // clear_padding() has set them to zero.
+  // Copies tiles of ROWS rows (d values each, `stride` values apart) to LDS,
+  // WAVES waves sharing the work.  The data goes straight to LDS, 64 chunks of
+  // 16 bytes an instruction in lane order: the swizzle is applied to the address
+  // a lane fetches.  Chunks past d stay as they are (clear_padding() has set them
+  // to zero).  A wave's instructions repeat their lanes' pattern every kPeriod,
+  // kStep rows further on, so a lane keeps kPeriod offsets.
   template <int ROWS, int WAVES>
-  static __device__ __forceinline__ void fetch(T* tile, const T* src, int64_t stride, int last,
-                                               int d, int wave) {
-    constexpr int CALLS = ROWS * NC / 64;
-    static_assert(ROWS * NC % 64 == 0 && CALLS % WAVES == 0);
-    const int l = threadIdx.x & 63;
-    const uint32_t row_bytes = (uint32_t)stride * sizeof(T);
-#pragma unroll
-    for (int i = 0; i < CALLS / WAVES; ++i) {
-      const int call = wave + i * WAVES;
-      const int at = call * 64 + l;
-      const int row = at / NC;
-      const int chunk = (at % NC) ^ swizzle(row);
-      const uint32_t off = (uint32_t)min(row, last) * row_bytes + chunk * 16;
-      if (chunk * CE < d)
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)((const char*)src + off),
-            (__attribute__((address_space(3))) void*)(tile + call * 64 * CE), 16, 0, 0);
+  struct Copier {
+    static constexpr int kCalls = ROWS * NC / 64 / WAVES;  // of one wave
+    static_assert(ROWS * NC % (64 * WAVES) == 0);
+    static constexpr int period() {
+      int p = 1;
+      while (p * 64 * WAVES % (8 * NC)) ++p;
+      return p < kCalls ? p : kCalls;
     }
-  }
+    static constexpr int kPeriod = period();
+    static constexpr int kStep = kPeriod * 64 * WAVES / NC;
+    uint32_t off[kPeriod];
+    uint32_t row_bytes, dead;  // dead: bit i: this lane's chunk of call i is padding
+
+    static __device__ __forceinline__ int place(int wave, int i) {
+      return (wave + i * WAVES) * 64 + (threadIdx.x & 63);
+    }
+    __device__ __forceinline__ void init(int64_t stride, int d, int wave) {
+      row_bytes = (uint32_t)stride * sizeof(T);
+      dead = 0;
+#pragma unroll
+      for (int i = 0; i < kPeriod; ++i) {
+        const int row = place(wave, i) / NC, chunk = place(wave, i) % NC ^ swizzle(row);
+        off[i] = row * row_bytes + chunk * 16;
+        if (chunk * CE >= d) dead |= 1u << i;
+      }
+    }
+    // Start copying; rows past `last` repeat row `last`, so nothing outside the
+    // tensor is read.  tile_barrier() (or a wait of the wave's own) ends it.
+    __device__ __forceinline__ void start(T* tile, const T* src, int last, int wave) const {
+      const uint32_t to = lds_offset(tile) + wave * 1024;
+      if (last >= ROWS - 1) {
+#pragma unroll
+        for (int i = 0; i < kCalls; ++i)
+          if (!(dead >> i % kPeriod & 1))
+            copy_to_lds<16>(to + i * WAVES * 1024, off[i % kPeriod],
+                            (const char*)src + (uint32_t)(i / kPeriod * kStep) * (uint64_t)row_bytes);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCalls; ++i) {
+          const int row = place(wave, i) / NC, chunk = place(wave, i) % NC ^ swizzle(row);
+          if (!(dead >> i % kPeriod & 1))
+            copy_to_lds<16>(to + i * WAVES * 1024, (uint32_t)min(row, last) * row_bytes + chunk * 16,
+                            src);
+        }
+      }
+    }
+  };
 
   template <int ROWS>
   static __device__ __forceinline__ void clear_padding(T* tile, int d, int thread, int threads) {
@@ -235,6 +299,10 @@ __device__ __forceinline__ int length_of(const int32_t* lengths, int b, int most
   return lengths ? min(max(lengths[b], 0), most) : most;
 }
 
+// Scores enter the exponential as c * s with c = |scale| * log2(e) (a negative
+// scale's sign is taken into an operand).  c is kept above this so that masked
+// scores, -inf, stay so at a scale of zero, and lse / c stays finite.
+constexpr float kLeastC = 1e-20f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

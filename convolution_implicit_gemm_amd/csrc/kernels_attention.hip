@@ -25,7 +25,7 @@ struct AttnK {
   void* o;
   float* lse;
   float *part_o, *part_lse;  // split form: [units][splits][rows][d], [units][splits][rows]
-  float c;                   // |scale| * log2(e), at least the least normal number
+  float c;                   // |scale| * log2(e), at least kLeastC
   int32_t tiles;             // row tiles of one head (tile form)
   int32_t splits, rows, row_groups;
 };
@@ -127,30 +127,30 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
 
   const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
   const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
-  auto buffer = [&](int n) { return tiles + n * 2 * BN * DP; };
-  auto fetch = [&](int key0, int n) {
-    const int last = see.nk - 1 - key0;
-    L::template fetch<BN, 4>(buffer(n), kp + key0 * p.k.s, p.k.s, last, p.d, wave);
-    L::template fetch<BN, 4>(buffer(n) + BN * DP, vp + key0 * p.v.s, p.v.s, last, p.d, wave);
-  };
-
   Running<NT> st;
   st.start();
   L::template clear_padding<4 * BN>(tiles, p.d, threadIdx.x, 256);
   if (first < end) {
-    __syncthreads();
-    fetch(first, 0);
+    typename L::template Copier<BN, 4> ck, cv;
+    ck.init(p.k.s, p.d, wave);
+    cv.init(p.v.s, p.d, wave);
     frag_t<T> q[NS];
     const int qi = min(i, see.nq - 1);
     load_operand<T, DP>(q, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d,
                         p.scale < 0.f);
-    int n = 0;
-    for (int key0 = first; key0 < end; key0 += BN, n ^= 1) {
-      tile_barrier();  // tile n has arrived; everyone is done with the other buffer
-      if (key0 + BN < end) fetch(key0 + BN, n ^ 1);
-      if (key0 >= wave_hi || key0 + BN <= wave_lo) continue;
-      const T* kt = buffer(n);
+    __syncthreads();
+    auto fetch = [&](int key0, T* to) {
+      ck.start(to, kp + key0 * p.k.s, see.nk - 1 - key0, wave);
+      cv.start(to + BN * DP, vp + key0 * p.v.s, see.nk - 1 - key0, wave);
+    };
+    fetch(first, tiles);
+    // one tile, from buffer N (a constant, so that it is part of the addresses)
+    auto step = [&](int key0, auto N) {
+      const T* kt = tiles + N * 2 * BN * DP;
       const T* vt = kt + BN * DP;
+      tile_barrier();  // the tile has arrived; everyone is done with the other buffer
+      if (key0 + BN < end) fetch(key0 + BN, tiles + (N ^ 1) * 2 * BN * DP);
+      if (key0 >= wave_hi || key0 + BN <= wave_lo) return;
       f32x16 s[KB];
 #pragma unroll
       for (int k = 0; k < KB; ++k) s[k] = zero16();
@@ -169,6 +169,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
           for (int t = 0; t < NT; ++t)
             st.o[t] = mma(L::load_columns(vt, 32 * k + 16 * d, t), pf, st.o[t]);
         }
+    };
+    for (int key0 = first; key0 < end; key0 += 2 * BN) {
+      step(key0, std::integral_constant<int, 0>{});
+      if (key0 + BN >= end) break;
+      step(key0 + BN, std::integral_constant<int, 1>{});
     }
   }
   if (i >= p.sq) return;
@@ -238,13 +243,15 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
   const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
   const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
   T* mine = (T*)lds + wave * 4 * F::kTile;
+  typename L::template Copier<32, 1> ck, cv;
+  ck.init(p.k.s, p.d, 0);
+  cv.init(p.v.s, p.d, 0);
   auto fetch = [&](int tile, int n) {
     const int key0 = first + 32 * tile;
-    const int last = see.nk - 1 - key0;
-    L::template fetch<32, 1>(mine + n * 2 * F::kTile, kp + key0 * p.k.s, p.k.s, last, p.d, 0);
-    L::template fetch<32, 1>(mine + (n * 2 + 1) * F::kTile, vp + key0 * p.v.s, p.v.s, last, p.d, 0);
+    ck.start(mine + n * 2 * F::kTile, kp + key0 * p.k.s, see.nk - 1 - key0, 0);
+    cv.start(mine + (n * 2 + 1) * F::kTile, vp + key0 * p.v.s, see.nk - 1 - key0, 0);
   };
-  constexpr int kLoads = 2 * 32 * L::NC / 64;  // of one fetch
+  constexpr int kLoads = 2 * L::template Copier<32, 1>::kCalls;  // of one fetch
 
   Running<NT> st;
   st.start();
@@ -420,7 +427,7 @@ void plan_attention(const AttnParams& p, AttnPlan& plan) {
     plan.splits = splits < 1 ? 1 : (int)splits;
     if (plan.splits > 1) plan.forward_bytes = split_bytes(p, plan.splits);
   }
-  // lse * log2(e) and rowsum(do * o), rows padded to whole tiles
+  // -lse and -rowsum(do * o), rows padded to whole tiles
   plan.backward_bytes = (size_t)p.batch * p.heads * ((p.sq + 63) / 64 * 64) * 2 * sizeof(float);
 }
 
@@ -430,7 +437,7 @@ int launch_attention_forward(const AttnParams& p, const AttnPlan& plan, const At
   k.q = a.q; k.k = a.k; k.v = a.v;
   k.q_lengths = a.q_lengths; k.k_lengths = a.k_lengths;
   k.o = a.o; k.lse = a.lse;
-  k.c = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
+  k.c = fmaxf(fabsf(p.scale) * kLog2e, kLeastC);
   k.tiles = (p.sq + 127) / 128;
   k.splits = plan.splits;
   k.rows = p.sq * p.group;

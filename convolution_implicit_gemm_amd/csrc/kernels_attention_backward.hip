@@ -10,6 +10,8 @@
 // Compiled once per head size the tiles are made for (FC_DP).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attention_tile.h"
 #include "fusedconv.h"
 #include "internal.h"
@@ -23,16 +25,18 @@ struct AttnBwdK {
   const int32_t *q_lengths, *k_lengths;
   const float* lse;
   void *dq, *dk, *dv;
-  float *lse2, *delta;  // workspace [batch * heads][rows padded to 64]
-  float c;              // |scale| * log2(e), at least the least normal number
+  float *nlse, *ndelta; // workspace [batch * heads][rows padded to 64]
+  float c;              // |scale| * log2(e), at least kLeastC
   int32_t padded, q_tiles, k_tiles;
 };
 
 namespace {
 
-// lse2 = lse * log2(e); delta = rowsum(do * o).  Rows without a key, behind
-// the entry's queries or in the padding get lse2 = +inf: their probabilities
-// exp2(s - lse2) are then zero, and need no mask.  8 lanes a row.
+// nlse = -lse in units of the raw scores, ndelta = -rowsum(do * o): what the
+// products q k^T and do v^T start from, so that the probability is
+// exp2(c * sum) and ds is p times the other sum, with no further operation.
+// Rows without a key, behind the entry's queries or in the padding get nlse =
+// -inf: their probabilities are then zero, and need no mask.  8 lanes a row.
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
   const AttnParams& p = a.p;
@@ -41,7 +45,7 @@ __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
   const int i = (int)(at % a.padded);
   const int head = (int)(at / a.padded % p.heads), b = (int)(at / a.padded / p.heads);
   const int nq = length_of(a.q_lengths, b, p.sq);
-  float s = 0.f, l2 = INFINITY;
+  float s = 0.f, l = -INFINITY;
   if (i < nq) {
     const T* o = (const T*)a.o + b * p.o.b + i * p.o.s + head * p.o.h;
     const T* g = (const T*)a.dout + b * p.dout.b + i * p.dout.s + head * p.dout.h;
@@ -51,14 +55,13 @@ __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += (float)x[j] * (float)y[j];
     }
-    const float l = a.lse[((int64_t)b * p.heads + head) * p.sq + i];
-    if (l != -INFINITY) l2 = l * kLog2e;
+    l = a.lse[((int64_t)b * p.heads + head) * p.sq + i];
   }
 #pragma unroll
   for (int off = 1; off < 8; off <<= 1) s += __shfl_xor(s, off, 64);
   if ((threadIdx.x & 7) == 0) {
-    a.lse2[at] = l2;
-    a.delta[at] = l2 == INFINITY ? 0.f : s;
+    a.nlse[at] = l == -INFINITY ? l : -l * kLog2e / a.c;
+    a.ndelta[at] = l == -INFINITY ? 0.f : -s;
   }
 }
 
@@ -68,19 +71,35 @@ __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
 // registers while the block walks the queries of every head that shares the
 // key head, BQ at a time, double-buffered.
 template <typename T, int DP>
+struct KeyBlock {
+  // dk, dv, K and V of 32 keys are 4 * DP / 2 registers a lane, all of the 256
+  // that two waves a SIMD leave at DP = 128: there V is read from LDS, a fifth
+  // more LDS reads, and the query tiles are half as long to make room.
+  static constexpr bool kVInLds = DP == 128;
+  static constexpr int kRows = sizeof(T) == 2 && !kVInLds ? 64 : 32;
+  static constexpr int kLds = Tile<T, DP>::bytes(4 * kRows + (kVInLds ? 128 : 0)) + 256 * 4;
+};
+
+template <typename T, int DP>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dkdv(AttnBwdK a) {
   using L = Tile<T, DP>;
-  constexpr int BQ = sizeof(T) == 2 ? 64 : 32;
+  using B = KeyBlock<T, DP>;
+  constexpr int BQ = B::kRows;
   constexpr int NT = DP / 32, NS = DP / 16;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   T* tiles = (T*)lds;                                    // [2][Q, dO][BQ * DP]
-  float* rows = (float*)(lds + 4 * L::bytes(BQ));        // [2][lse2, delta][64]
+  T* vt = tiles + 4 * BQ * DP;                           // V [128 * DP], where it is not in registers
+  float* rows = (float*)(lds + B::kLds) - 256;           // [2][nlse, ndelta][64]
 
   const AttnParams& p = a.p;
   const int total = p.batch * p.kv_heads * a.k_tiles;
   int item = xcd_item(blockIdx.x, total);
   if (item >= total) return;
-  const int tile_k = item % a.k_tiles;  // the first keys first: a causal window shows them to most
+  // The first keys first: a causal window shows them to most queries.  Where
+  // all blocks are resident at once (two on each of 256 compute units) every
+  // other head goes the other way, which pairs long blocks with short ones.
+  const int turn = total <= 512 ? item / a.k_tiles & 1 : 0;
+  const int tile_k = turn ? a.k_tiles - 1 - item % a.k_tiles : item % a.k_tiles;
   item /= a.k_tiles;
   const int kvh = item % p.kv_heads, b = item / p.kv_heads;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -100,72 +119,84 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dkdv(
 #pragma unroll
   for (int t = 0; t < NT; ++t) dk[t] = dv[t] = zero16();
 
-  L::template clear_padding<4 * BQ>(tiles, p.d, threadIdx.x, 256);
+  L::template clear_padding<4 * BQ + (B::kVInLds ? 128 : 0)>(tiles, p.d, threadIdx.x, 256);
   if (first < end) {
-    frag_t<T> kf[NS], vf[NS];
+    frag_t<T> kf[NS], vf[B::kVInLds ? 1 : NS];
     const int ji = min(j, see.nk - 1);
     load_operand<T, DP>(kf, (const T*)a.k + b * p.k.b + ji * p.k.s + kvh * p.k.h, p.d, p.scale < 0.f);
-    load_operand<T, DP>(vf, (const T*)a.v + b * p.v.b + ji * p.v.s + kvh * p.v.h, p.d, false);
+    const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
+    if constexpr (!B::kVInLds) load_operand<T, DP>(vf, vp + ji * p.v.s, p.d, false);
 
-    auto fetch = [&](int g, int row0, int n) {
-      const int head = kvh * p.group + g;
-      const int last = see.nq - 1 - row0;
-      const T* q = (const T*)a.q + b * p.q.b + head * p.q.h + row0 * p.q.s;
-      const T* o = (const T*)a.dout + b * p.dout.b + head * p.dout.h + row0 * p.dout.s;
-      L::template fetch<BQ, 4>(tiles + n * 2 * BQ * DP, q, p.q.s, last, p.d, wave);
-      L::template fetch<BQ, 4>(tiles + (n * 2 + 1) * BQ * DP, o, p.dout.s, last, p.d, wave);
-      if (wave < 2 && lane < BQ) {
-        const float* src = (wave ? a.delta : a.lse2) + ((int64_t)b * p.heads + head) * a.padded + row0;
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(src + lane),
-            (__attribute__((address_space(3))) void*)(rows + n * 128 + wave * 64), 4, 0, 0);
-      }
+    typename L::template Copier<BQ, 4> cq, co;
+    cq.init(p.q.s, p.d, wave);
+    co.init(p.dout.s, p.d, wave);
+    const int items = (end - first + BQ - 1) / BQ;
+    // query tile `it` of query head g of the group, to buffer N
+    auto fetch = [&](int g, int it, auto N) {
+      const int head = kvh * p.group + g, row0 = first + it * BQ;
+      T* to = tiles + N * 2 * BQ * DP;
+      cq.start(to, (const T*)a.q + b * p.q.b + head * p.q.h + row0 * p.q.s, see.nq - 1 - row0, wave);
+      co.start(to + BQ * DP, (const T*)a.dout + b * p.dout.b + head * p.dout.h + row0 * p.dout.s,
+               see.nq - 1 - row0, wave);
+      if (wave < 2 && lane < BQ)
+        copy_to_lds<4>(lds_offset(rows + N * 128 + wave * 64), lane * 4,
+                       (wave ? a.ndelta : a.nlse) + ((int64_t)b * p.heads + head) * a.padded + row0);
     };
     __syncthreads();
-    fetch(0, first, 0);
-    int n = 0, g = 0, row0 = first;
-    while (g < p.group) {
-      int next = row0 + BQ, gn = g;
-      if (next >= end) next = first, ++gn;
+    if constexpr (B::kVInLds) {
+      typename L::template Copier<128, 4> cv;
+      cv.init(p.v.s, p.d, wave);
+      cv.start(vt, vp + key0 * p.v.s, see.nk - 1 - key0, wave);
+    }
+    fetch(0, 0, std::integral_constant<int, 0>{});
+    int g = 0, it = 0;
+    auto step = [&](auto N) {
+      const int row0 = first + it * BQ;
+      if (++it == items) it = 0, ++g;
       tile_barrier();
-      if (gn < p.group) fetch(gn, next, n ^ 1);
-      if (row0 < wave_hi && row0 + BQ > wave_lo) {
-        const T* qt = tiles + n * 2 * BQ * DP;
-        const T* ot = qt + BQ * DP;
-        const bool masked = row0 < all_lo || row0 + BQ > all_hi;
+      if (g < p.group) fetch(g, it, std::integral_constant<int, N ^ 1>{});
+      if (row0 >= wave_hi || row0 + BQ <= wave_lo) return;
+      const T* qt = tiles + N * 2 * BQ * DP;
+      const T* ot = qt + BQ * DP;
+      const float* rt = rows + N * 128;
+      const bool masked = row0 < all_lo || row0 + BQ > all_hi;
 #pragma unroll
-        for (int r = 0; r < BQ; r += 32) {
-          f32x16 s = zero16(), dp = zero16();
+      for (int r = 0; r < BQ; r += 32) {
+        f32x16 s = load_c_rows(rt + r, h), dp = load_c_rows(rt + 64 + r, h);
 #pragma unroll
-          for (int d = 0; d < NS; ++d) {
-            s = mma(L::load_rows(qt, r, d), kf[d], s);
+        for (int d = 0; d < NS; ++d) {
+          s = mma(L::load_rows(qt, r, d), kf[d], s);
+          if constexpr (B::kVInLds)
+            dp = mma(L::load_rows(ot, r, d), L::load_rows(vt, wave * 32, d), dp);
+          else
             dp = mma(L::load_rows(ot, r, d), vf[d], dp);
-          }
+        }
+        if (masked)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float l2 = rows[n * 128 + r + c_row(i, h)];
-            const float delta = rows[n * 128 + 64 + r + c_row(i, h)];
-            s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.c, -l2));
-            if (masked) {
-              const int at = row0 + r + c_row(i, h);
-              if (at < lo || at >= hi) s[i] = 0.f;
-            }
-            dp[i] = s[i] * (dp[i] - delta);
+            const int at = row0 + r + c_row(i, h);
+            if (at < lo || at >= hi) s[i] = -INFINITY;
           }
 #pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            const frag_t<T> pf = to_frag<T>(s, d), df = to_frag<T>(dp, d);
+        for (int i = 0; i < 16; ++i) {
+          s[i] = __builtin_amdgcn_exp2f(s[i] * a.c);
+          dp[i] *= s[i];
+        }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              dv[t] = mma(L::load_columns(ot, r + 16 * d, t), pf, dv[t]);
-              dk[t] = mma(L::load_columns(qt, r + 16 * d, t), df, dk[t]);
-            }
+        for (int d = 0; d < 2; ++d) {
+          const frag_t<T> pf = to_frag<T>(s, d), df = to_frag<T>(dp, d);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            dv[t] = mma(L::load_columns(ot, r + 16 * d, t), pf, dv[t]);
+            dk[t] = mma(L::load_columns(qt, r + 16 * d, t), df, dk[t]);
           }
         }
       }
-      g = gn;
-      row0 = next;
-      n ^= 1;
+    };
+    while (g < p.group) {
+      step(std::integral_constant<int, 0>{});
+      if (g >= p.group) break;
+      step(std::integral_constant<int, 1>{});
     }
   }
   if (j >= p.sk) return;
@@ -226,45 +257,47 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(At
   if (first < end) {
     const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
     const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
-    auto fetch = [&](int key0, int n) {
-      const int last = see.nk - 1 - key0;
-      L::template fetch<BN, 4>(tiles + n * 2 * BN * DP, kp + key0 * p.k.s, p.k.s, last, p.d, wave);
-      L::template fetch<BN, 4>(tiles + (n * 2 + 1) * BN * DP, vp + key0 * p.v.s, p.v.s, last, p.d, wave);
+    typename L::template Copier<BN, 4> ck, cv;
+    ck.init(p.k.s, p.d, wave);
+    cv.init(p.v.s, p.d, wave);
+    auto fetch = [&](int key0, T* to) {
+      ck.start(to, kp + key0 * p.k.s, see.nk - 1 - key0, wave);
+      cv.start(to + BN * DP, vp + key0 * p.v.s, see.nk - 1 - key0, wave);
     };
     frag_t<T> qf[NS], of[NS];
     const int qi = min(i, see.nq - 1);
     load_operand<T, DP>(qf, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d, p.scale < 0.f);
     load_operand<T, DP>(of, (const T*)a.dout + b * p.dout.b + qi * p.dout.s + head * p.dout.h, p.d, false);
     const int64_t at = ((int64_t)b * p.heads + head) * a.padded;
-    const float l2 = i < a.padded ? a.lse2[at + i] : INFINITY;
-    const float delta = i < a.padded ? a.delta[at + i] : 0.f;
+    const float nlse = i < a.padded ? a.nlse[at + i] : -INFINITY;
+    const float ndelta = i < a.padded ? a.ndelta[at + i] : 0.f;
     __syncthreads();
-    fetch(first, 0);
-    int n = 0;
-    for (int key0 = first; key0 < end; key0 += BN, n ^= 1) {
+    fetch(first, tiles);
+    auto step = [&](int key0, auto N) {
       tile_barrier();
-      if (key0 + BN < end) fetch(key0 + BN, n ^ 1);
-      if (key0 >= wave_hi || key0 + BN <= wave_lo) continue;
-      const T* kt = tiles + n * 2 * BN * DP;
+      if (key0 + BN < end) fetch(key0 + BN, tiles + (N ^ 1) * 2 * BN * DP);
+      if (key0 >= wave_hi || key0 + BN <= wave_lo) return;
+      const T* kt = tiles + N * 2 * BN * DP;
       const T* vt = kt + BN * DP;
       const bool masked = key0 < all_lo || key0 + BN > all_hi;
 #pragma unroll
       for (int r = 0; r < BN; r += 32) {
-        f32x16 s = zero16(), dp = zero16();
+        f32x16 s, dp;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = nlse, dp[e] = ndelta;
 #pragma unroll
         for (int d = 0; d < NS; ++d) {
           s = mma(L::load_rows(kt, r, d), qf[d], s);
           dp = mma(L::load_rows(vt, r, d), of[d], dp);
         }
+        if (masked)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float pr = __builtin_amdgcn_exp2f(fmaf(s[e], a.c, -l2));
-          if (masked) {
+          for (int e = 0; e < 16; ++e) {
             const int key = key0 + r + c_row(e, h);
-            if (key < lo || key >= hi) pr = 0.f;
+            if (key < lo || key >= hi) s[e] = -INFINITY;
           }
-          dp[e] = pr * (dp[e] - delta);
-        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dp[e] *= __builtin_amdgcn_exp2f(s[e] * a.c);
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
           const frag_t<T> df = to_frag<T>(dp, d);
@@ -272,6 +305,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(At
           for (int t = 0; t < NT; ++t) dq[t] = mma(L::load_columns(kt, r + 16 * d, t), df, dq[t]);
         }
       }
+    };
+    for (int key0 = first; key0 < end; key0 += 2 * BN) {
+      step(key0, std::integral_constant<int, 0>{});
+      if (key0 + BN >= end) break;
+      step(key0 + BN, std::integral_constant<int, 1>{});
     }
   }
   if (i >= p.sq) return;
@@ -305,7 +343,7 @@ int FC_DP_NAME(attention_backward_)(const AttnPlan& plan, const AttnBwdK& k, hip
                          dim3(256), 0, st, k);
     if (p.sk > 0) {
       auto fn = k_attention_dkdv<T, FC_DP>;
-      constexpr int bytes = tile_bytes + 2 * 2 * 64 * (int)sizeof(float);
+      constexpr int bytes = KeyBlock<T, FC_DP>::kLds;
       rc = set_max_dynamic_lds((const void*)fn, bytes);
       if (rc != FUSEDCONV_OK) return;
       hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.kv_heads * k.k_tiles)), dim3(256),
@@ -336,9 +374,9 @@ int launch_attention_backward(const AttnParams& p, const AttnPlan& plan, const A
   k.lse = a.lse_in;
   k.dq = a.dq; k.dk = a.dk; k.dv = a.dv;
   k.padded = (p.sq + 63) / 64 * 64;
-  k.lse2 = (float*)a.ws;
-  k.delta = k.lse2 + (size_t)p.batch * p.heads * k.padded;
-  k.c = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
+  k.nlse = (float*)a.ws;
+  k.ndelta = k.nlse + (size_t)p.batch * p.heads * k.padded;
+  k.c = fmaxf(fabsf(p.scale) * kLog2e, kLeastC);
   k.q_tiles = (p.sq + 127) / 128;
   k.k_tiles = (p.sk + 127) / 128;
   const hipStream_t st = (hipStream_t)a.stream;
