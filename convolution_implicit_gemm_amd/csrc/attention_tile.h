@@ -267,16 +267,6 @@ __device__ __forceinline__ frag_t<T> to_frag(const f32x16& c, int step) {
   return f;
 }
 
-// Blocks go round the 8 XCDs in launch order; this deals each XCD a run of
-// consecutive work items, so that neighbours (which read the same keys, or the
-// same queries) share its L2.  The grid is 8 * ceil(total / 8); an item >= total
-// has no work.
-__device__ __forceinline__ int xcd_item(int block, int total) {
-  const int run = (total + 7) >> 3;
-  return (block & 7) * run + (block >> 3);
-}
-inline unsigned xcd_grid(int64_t total) { return (unsigned)((total + 7) / 8 * 8); }
-
 // What a batch entry's lengths and the window let a query see.
 struct Sight {
   int nq, nk, left, right;

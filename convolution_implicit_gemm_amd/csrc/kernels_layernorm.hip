@@ -39,9 +39,7 @@ constexpr int kLoopThreads = 256;
 template <int TPR, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K]) {
 #pragma unroll
-  for (int off = 1; off < (TPR < 64 ? TPR : 64); off <<= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], off, 64);
+  for (int k = 0; k < K; ++k) v[k] = lane_sum<1, (TPR < 64 ? TPR : 64)>(v[k]);
   if constexpr (TPR > 64) {
     __shared__ float red[TPR / 64][K];
     const int wave = threadIdx.x >> 6;
@@ -142,19 +140,32 @@ __global__ __launch_bounds__(256) void k_norm_rows_bwd(NormK a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) pw[i].v[j] = (T)1.f;
   }
-  for (int row = blockIdx.x * RPB + group; row < a.n; row += gridDim.x * RPB) {
+  // the next row is on its way while one is worked on
+  Piece<T, V> nx[NCH], nd[NCH];
+  float nmean = 0.f, nrstd = 0.f;
+  auto fetch = [&](int row) {
+    if (row >= a.n) return;
     const T* x = (const T*)a.x + (int64_t)row * a.x_stride;
     const T* dy = (const T*)a.dy + (int64_t)row * a.dy_stride;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    Piece<T, V> px[NCH], pd[NCH];
+    nmean = a.mean[row];
+    nrstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int at = (t + i * TPR) * V;
       if (at < a.c) {
-        px[i] = load_piece<T, V>(x + at);
-        pd[i] = load_piece<T, V>(dy + at);
+        nx[i] = load_piece<T, V>(x + at);
+        nd[i] = load_piece<T, V>(dy + at);
       }
     }
+  };
+  const int first = blockIdx.x * RPB + group;
+  fetch(first);
+  for (int row = first; row < a.n; row += gridDim.x * RPB) {
+    Piece<T, V> px[NCH], pd[NCH];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) px[i] = nx[i], pd[i] = nd[i];
+    const float mean = nmean, rstd = nrstd;
+    fetch(row + gridDim.x * RPB);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
@@ -289,57 +300,82 @@ __global__ __launch_bounds__(kLoopThreads) void k_norm_columns(NormK a) {
 // ------------------------------------------------------------- NCHW images
 // A block has a tile of PL * V consecutive pixels of one image, all channels:
 // lane p of PL holds V pixels, channel group g of CG the channels g, g + CG,
-// ...  A wave's accesses are 64 / PL channels of PL * V * sizeof(T) bytes
-// (128 for the vector forms) each.
+// ... (NCH of them).  A wave's accesses are 64 / PL channels of PL * V *
+// sizeof(T) bytes (128 or more for the vector forms) each.
 
-constexpr int kPlaneThreads = 512;
+constexpr int kPlaneThreads = 256;
+constexpr int kPlaneWaves = kPlaneThreads / 64;
 
-// Sum over the channel groups of the block, for every pixel of the tile.
+// The piece (of V values) `off` bytes behind a block's base pointer: one 32-bit
+// offset a lane for all its channels, whose distances go into the base.
+template <typename T, int V>
+__device__ __forceinline__ Piece<T, V> load_at(const T* base, int64_t step, uint32_t off) {
+  return *reinterpret_cast<const Piece<T, V>*>((const char*)(base + step) + off);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_at(T* base, int64_t step, uint32_t off, const Piece<T, V>& v) {
+  *reinterpret_cast<Piece<T, V>*>((char*)(base + step) + off) = v;
+}
+
+// Values of the block's waves for every pixel of a tile: [wave][k][lane][j].
+template <int PL, int V, int K>
+struct Meeting {
+  float v[kPlaneWaves][K][PL][V];
+  // This wave's values (its channel groups already added up), then all waves' are there.
+  __device__ __forceinline__ void put(const float (&x)[K][V]) {
+    if ((threadIdx.x & 63) < PL)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[threadIdx.x >> 6][k][threadIdx.x % PL][j] = x[k][j];
+    __syncthreads();
+  }
+};
+
+// Sum over the channel groups of the block.  The second barrier keeps the next
+// tile's values out of LDS while these are read.
 template <int PL, int V, int K>
 __device__ __forceinline__ void pixel_sum(float (&v)[K][V]) {
-#pragma unroll
-  for (int off = PL; off < 64; off <<= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[k][j] += __shfl_xor(v[k][j], off, 64);
-  __shared__ float red[kPlaneThreads / 64][K][V][PL];
-  const int wave = threadIdx.x >> 6, p = threadIdx.x % PL;
-  if ((threadIdx.x & 63) < PL)
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int j = 0; j < V; ++j) red[wave][k][j][p] = v[k][j];
-  __syncthreads();
+  __shared__ Meeting<PL, V, K> all;
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float s = 0.f;
+    for (int j = 0; j < V; ++j) v[k][j] = lane_sum<PL, 64>(v[k][j]);
+  all.put(v);
 #pragma unroll
-      for (int i = 0; i < kPlaneThreads / 64; ++i) s += red[i][k][j][p];
-      v[k][j] = s;
-    }
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[k][j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPlaneWaves; ++i)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[k][j] += all.v[i][k][threadIdx.x % PL][j];
   __syncthreads();
 }
 
+// Statistics with one exchange between the waves: a wave takes the mean of its
+// own channels and the squares about that; the parts' squares about the common
+// mean follow from the distances of the means (exact, nothing cancels).
 // NCH: channels a thread holds; 0: any number, read again for each pass.
 template <typename T, int V, int PL, int NCH>
 __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
   constexpr int CG = kPlaneThreads / PL;
+  constexpr int GW = 64 / PL;  // channel groups of a wave
   const int p = threadIdx.x % PL, g = threadIdx.x / PL;
-  const int image = blockIdx.x / a.tiles;
-  const int pixel = ((blockIdx.x - image * a.tiles) * PL + p) * V;
+  const int tile = blockIdx.x;
+  const int image = tile / a.tiles;
+  const int pixel = ((tile - image * a.tiles) * PL + p) * V;
   const bool live = pixel < a.inner;
-  const T* x = (const T*)a.x + (int64_t)image * a.x_stride + pixel;
-  T* y = (T*)a.out + (int64_t)image * a.c * a.inner + pixel;
+  const T* x = (const T*)a.x + (int64_t)image * a.x_stride;
+  T* y = (T*)a.out + (int64_t)image * a.c * a.inner;
+  const uint32_t off = (uint32_t)(g * a.inner + pixel) * sizeof(T);
+  const int64_t step = (int64_t)CG * a.inner;
   const T* w = (const T*)a.w;
   const T* b = (const T*)a.b;
   constexpr int HELD = NCH ? NCH : 1;
   Piece<T, V> px[HELD];
-  float sum[1][V], sq[1][V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) sum[0][j] = sq[0][j] = 0.f;
   auto each = [&](auto&& f) {
     if constexpr (NCH > 0) {
 #pragma unroll
@@ -347,32 +383,60 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
         if (live && g + i * CG < a.c) f(i, g + i * CG);
     } else {
       if (live)
-        for (int ch = g; ch < a.c; ch += CG) {
-          px[0] = load_piece<T, V>(x + (int64_t)ch * a.inner);
-          f(0, ch);
+        for (int i = 0; g + i * CG < a.c; ++i) {
+          px[0] = load_at<T, V>(x, i * step, off);
+          f(i, g + i * CG);
         }
     }
   };
   if constexpr (NCH > 0)
-    each([&](int i, int ch) { px[i] = load_piece<T, V>(x + (int64_t)ch * a.inner); });
+    each([&](int i, int) { px[i] = load_at<T, V>(x, i * step, off); });
+  // channels of a wave: whole rounds of CG, and its share of the last one
+  auto channels = [&](int wave) {
+    const int rest = a.c % CG - wave * GW;
+    return (float)(a.c / CG * GW + (rest < 0 ? 0 : rest > GW ? GW : rest));
+  };
+  const int wave = threadIdx.x >> 6;
+  const float own = channels(wave);
+  float part[2][V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) part[0][j] = part[1][j] = 0.f;
   each([&](int i, int) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum[0][j] += (float)px[i].v[j];
+    for (int j = 0; j < V; ++j) part[0][j] += (float)px[HELD > 1 ? i : 0].v[j];
   });
-  pixel_sum<PL, V, 1>(sum);
-  float mean[V], rstd[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) mean[j] = sum[0][j] / (float)a.c;
+  for (int j = 0; j < V; ++j) part[0][j] = own > 0.f ? lane_sum<PL, 64>(part[0][j]) / own : 0.f;
   each([&](int i, int) {
+    stay_packed(px[HELD > 1 ? i : 0]);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float d = (float)px[i].v[j] - mean[j];
-      sq[0][j] += d * d;
+      const float d = (float)px[HELD > 1 ? i : 0].v[j] - part[0][j];
+      part[1][j] += d * d;
     }
   });
-  pixel_sum<PL, V, 1>(sq);
 #pragma unroll
-  for (int j = 0; j < V; ++j) rstd[j] = 1.0f / sqrtf(sq[0][j] / (float)a.c + a.eps);
+  for (int j = 0; j < V; ++j) part[1][j] = lane_sum<PL, 64>(part[1][j]);
+  __shared__ Meeting<PL, V, 2> all;
+  all.put(part);
+  float mean[V], rstd[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) mean[j] = rstd[j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPlaneWaves; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) mean[j] += all.v[i][0][p][j] * channels(i);
+#pragma unroll
+  for (int j = 0; j < V; ++j) mean[j] /= (float)a.c;
+#pragma unroll
+  for (int i = 0; i < kPlaneWaves; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float d = all.v[i][0][p][j] - mean[j];
+      rstd[j] += all.v[i][1][p][j] + channels(i) * d * d;
+    }
+#pragma unroll
+  for (int j = 0; j < V; ++j) rstd[j] = 1.0f / sqrtf(rstd[j] / (float)a.c + a.eps);
   if (g == 0 && live && a.mean) {
     const int64_t at = (int64_t)image * a.inner + pixel;
 #pragma unroll
@@ -383,11 +447,12 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
   }
   each([&](int i, int ch) {
     const float wc = w ? (float)w[ch] : 1.f, bc = b ? (float)b[ch] : 0.f;
+    stay_packed(px[HELD > 1 ? i : 0]);
     Piece<T, V> py;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      py.v[j] = to_type<T>(((float)px[i].v[j] - mean[j]) * rstd[j] * wc + bc);
-    store_piece<T, V>(y + (int64_t)ch * a.inner, py);
+      py.v[j] = to_type<T>(((float)px[HELD > 1 ? i : 0].v[j] - mean[j]) * rstd[j] * wc + bc);
+    store_at<T, V>(y, i * step, off, py);
   });
 }
 
@@ -398,27 +463,27 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
   constexpr int CG = kPlaneThreads / PL;
   const int p = threadIdx.x % PL, g = threadIdx.x / PL;
   const T* w = (const T*)a.w;
-  float dw[NCH], db[NCH], wc[NCH];
+  const int64_t step = (int64_t)CG * a.inner;
+  const float per = 1.0f / (float)a.c;
+  float dw[NCH], db[NCH];
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    dw[i] = db[i] = 0.f;
-    wc[i] = w && g + i * CG < a.c ? (float)w[g + i * CG] : 1.f;
-  }
-  const int64_t all = (int64_t)a.n * a.tiles;
-  for (int64_t tile = blockIdx.x; tile < all; tile += gridDim.x) {
-    const int image = (int)(tile / a.tiles);
-    const int pixel = ((int)(tile - (int64_t)image * a.tiles) * PL + p) * V;
+  for (int i = 0; i < NCH; ++i) dw[i] = db[i] = 0.f;
+  const int all = a.n * a.tiles;
+  for (int tile = blockIdx.x; tile < all; tile += gridDim.x) {
+    const int image = tile / a.tiles;
+    const int pixel = ((tile - image * a.tiles) * PL + p) * V;
     const bool live = pixel < a.inner;
-    const T* x = (const T*)a.x + (int64_t)image * a.x_stride + pixel;
-    const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride + pixel;
-    T* dx = (T*)a.out + (int64_t)image * a.c * a.inner + pixel;
+    const T* x = (const T*)a.x + (int64_t)image * a.x_stride;
+    const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride;
+    T* dx = (T*)a.out + (int64_t)image * a.c * a.inner;
+    const uint32_t off = (uint32_t)(g * a.inner + pixel) * sizeof(T);
     Piece<T, V> px[NCH], pd[NCH];
     float mean[V], rstd[V], s[2][V];
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
       if (live && g + i * CG < a.c) {
-        px[i] = load_piece<T, V>(x + (int64_t)(g + i * CG) * a.inner);
-        pd[i] = load_piece<T, V>(dy + (int64_t)(g + i * CG) * a.inner);
+        px[i] = load_at<T, V>(x, i * step, off);
+        pd[i] = load_at<T, V>(dy, i * step, off);
       }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -428,39 +493,42 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
     }
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
-      if (live && g + i * CG < a.c)
+      if (live && g + i * CG < a.c) {
+        const float wc = w ? (float)w[g + i * CG] : 1.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float xh = ((float)px[i].v[j] - mean[j]) * rstd[j];
           const float d = (float)pd[i].v[j];
-          s[0][j] += d * wc[i];
-          s[1][j] += d * wc[i] * xh;
+          s[0][j] += d * wc;
+          s[1][j] += d * wc * xh;
           dw[i] += d * xh;
           db[i] += d;
         }
-    pixel_sum<PL, V, 2>(s);
+      }
+    pixel_sum<PL, V>(s);
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[0][j] *= per, s[1][j] *= per;
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
       if (live && g + i * CG < a.c) {
+        const float wc = w ? (float)w[g + i * CG] : 1.f;
+        stay_packed(px[i]);
+        stay_packed(pd[i]);
         Piece<T, V> po;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float xh = ((float)px[i].v[j] - mean[j]) * rstd[j];
-          const float gr = (float)pd[i].v[j] * wc[i];
-          po.v[j] = to_type<T>(rstd[j] * (gr - s[0][j] / (float)a.c - xh * (s[1][j] / (float)a.c)));
+          po.v[j] = to_type<T>(rstd[j] * ((float)pd[i].v[j] * wc - s[0][j] - xh * s[1][j]));
         }
-        store_piece<T, V>(dx + (int64_t)(g + i * CG) * a.inner, po);
+        store_at<T, V>(dx, i * step, off, po);
       }
   }
   if (!a.part) return;
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-#pragma unroll
-    for (int off = 1; off < PL; off <<= 1) {
-      dw[i] += __shfl_xor(dw[i], off, 64);
-      db[i] += __shfl_xor(db[i], off, 64);
-    }
+    dw[i] = lane_sum<1, PL>(dw[i]);
+    db[i] = lane_sum<1, PL>(db[i]);
     if (p == 0 && g + i * CG < a.c) {
       out[g + i * CG] = dw[i];
       out[a.c + g + i * CG] = db[i];
@@ -499,7 +567,7 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd_loop(NormK a)
       s[1][j] += gr * ((float)px.v[j] - mean[j]) * rstd[j];
     }
   }
-  pixel_sum<PL, V, 2>(s);
+  pixel_sum<PL, V>(s);
   for (int ch = g; live && ch < a.c; ch += CG) {
     const Piece<T, V> px = load_piece<T, V>(x + (int64_t)ch * a.inner);
     const Piece<T, V> pd = load_piece<T, V>(dy + (int64_t)ch * a.inner);
@@ -540,25 +608,26 @@ __global__ __launch_bounds__(kLoopThreads) void k_norm_plane_sums(NormK a) {
 }
 
 // ------------------------------------------------------------- weight gradients
-// part [blocks][2][c] -> dw[c], db[c]: 64 columns a block, 16 threads a
+// part [blocks][2][c] -> dw[c], db[c]: 32 columns a block, 32 threads a
 // column, each a strided share of the blocks, joined in LDS in a fixed order.
 __global__ __launch_bounds__(1024) void k_norm_join(const float* part, int blocks, int c, float* dw,
                                                     float* db) {
-  __shared__ float acc[16][64];
-  const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+  __shared__ float acc[32][33];
+  const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (col < 2 * c)
-#pragma unroll 4
-    for (int i = share; i < blocks; i += 16) s += part[(int64_t)i * 2 * c + col];
+#pragma unroll 8
+    for (int i = share; i < blocks; i += 32) s += part[(int64_t)i * 2 * c + col];
   acc[share][lane] = s;
   __syncthreads();
-  if (share == 0 && col < 2 * c) {
-    for (int i = 1; i < 16; ++i) s += acc[i][lane];
-    if (col < c) {
-      if (dw) dw[col] = s;
+  s = lane_sum<1, 32>(acc[lane][share]);
+  const int mine = blockIdx.x * 32 + share;
+  if (lane == 0 && mine < 2 * c) {
+    if (mine < c) {
+      if (dw) dw[mine] = s;
     } else if (db) {
-      db[col - c] = s;
+      db[mine - c] = s;
     }
   }
 }
@@ -614,15 +683,26 @@ NormPlan plan_norm(const NormProblem& p, bool backward) {
     if (q.loop && q.blocks > 64) q.blocks = 64;
     return q;
   }
-  q.tpr = q.v == 1 ? 32 : 8;
+  if (q.v == 1 && p.inner % (wide / 2) == 0 && p.x_stride % (wide / 2) == 0 &&
+      (!backward || p.dy_stride % (wide / 2) == 0))
+    q.v = wide / 2;
+  // Pixel lanes: as many as leave a thread 16 channels or fewer.  Long runs of a
+  // plane and many values in flight per thread both count (f16, 128 channels of
+  // 192 x 192, forward: 8 / 16 / 32 lanes 157 / 123 / 122 us; 384 of 56 x 56: 71 /
+  // 80 / 105, the last two with 24 and 48 channels a thread), but not where the
+  // planes are shorter than the lanes or the tiles too few for the chip.
+  q.tpr = 32;
+  while (q.tpr > 8 && (p.c * q.tpr > 16 * kPlaneThreads || q.tpr / 2 * q.v >= p.inner ||
+                       p.n * ceil_div(p.inner, (int64_t)q.tpr * q.v) < 512))
+    q.tpr /= 2;
   const int cg = kPlaneThreads / q.tpr;
-  q.nch = 1;
-  while (q.nch * cg < p.c) q.nch = q.nch < 4 ? q.nch * 2 : q.nch + 4;
-  const int most = 16;
-  q.loop = q.nch > most;
+  q.nch = 2;
+  while (q.nch * cg < p.c && q.nch <= 32) q.nch = q.nch < 4 ? 4 : q.nch < 16 ? q.nch + 4 : q.nch + 8;
+  q.loop = q.nch > (backward ? 16 : 32);
   q.tiles = (int)ceil_div(p.inner, (int64_t)q.tpr * q.v);
   const int64_t all = p.n * q.tiles;
-  q.blocks = (int)(all < 512 ? all : 512);
+  const int64_t most = q.nch <= 8 ? 768 : 512;  // blocks that fit the chip's registers at once
+  q.blocks = (int)(all < most ? all : most);
   if (q.loop && q.blocks > p.n) q.blocks = (int)p.n;
   if (q.loop && q.blocks > 64) q.blocks = 64;
   return q;
@@ -662,19 +742,29 @@ void with_rows(const NormPlan& q, F&& f) {
 }
 
 // f(V, PL, NCH) for a plane plan; NCH = 0: the looped form.
-template <typename T, typename F>
+template <typename T, bool BACKWARD, typename F>
 void with_planes(const NormPlan& q, F&& f) {
   auto pick = [&](auto v, auto pl) {
     if (q.loop) f(v, pl, int_c<0>{});
-    else if (q.nch == 1) f(v, pl, int_c<1>{});
     else if (q.nch == 2) f(v, pl, int_c<2>{});
     else if (q.nch == 4) f(v, pl, int_c<4>{});
     else if (q.nch == 8) f(v, pl, int_c<8>{});
     else if (q.nch == 12) f(v, pl, int_c<12>{});
-    else f(v, pl, int_c<16>{});
+    else if (q.nch == 16) f(v, pl, int_c<16>{});
+    else if constexpr (!BACKWARD) {
+      if (q.nch == 24) f(v, pl, int_c<24>{});
+      else f(v, pl, int_c<32>{});
+    }
   };
-  if (q.v == 1) pick(int_c<1>{}, int_c<32>{});
-  else pick(int_c<16 / sizeof(T)>{}, int_c<8>{});
+  auto lanes = [&](auto v) {
+    if (q.tpr == 8) pick(v, int_c<8>{});
+    else if (q.tpr == 16) pick(v, int_c<16>{});
+    else pick(v, int_c<32>{});
+  };
+  constexpr int wide = 16 / sizeof(T);
+  if (q.v == 1) lanes(int_c<1>{});
+  else if (q.v == wide) lanes(int_c<wide>{});
+  else lanes(int_c<wide / 2>{});
 }
 
 int status() { return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH; }
@@ -693,7 +783,7 @@ int launch_norm_forward(const NormProblem& p, const NormArgs& a) {
   with_type(p.dtype, [&](auto tag) {
     using T = typename decltype(tag)::type;
     if (q.planes)
-      with_planes<T>(q, [&](auto v, auto pl, auto nch) {
+      with_planes<T, false>(q, [&](auto v, auto pl, auto nch) {
         hipLaunchKernelGGL((k_norm_planes<T, v, pl, nch>), dim3((unsigned)(p.n * q.tiles)),
                            dim3(kPlaneThreads), 0, st, k);
       });
@@ -721,7 +811,7 @@ int launch_norm_backward(const NormProblem& p, const NormArgs& a) {
   with_type(p.dtype, [&](auto tag) {
     using T = typename decltype(tag)::type;
     if (q.planes) {
-      with_planes<T>(q, [&](auto v, auto pl, auto nch) {
+      with_planes<T, true>(q, [&](auto v, auto pl, auto nch) {
         if constexpr (nch == 0) {
           hipLaunchKernelGGL((k_norm_planes_bwd_loop<T, v, pl>), dim3((unsigned)(p.n * q.tiles)),
                              dim3(kPlaneThreads), 0, st, k);
@@ -746,7 +836,7 @@ int launch_norm_backward(const NormProblem& p, const NormArgs& a) {
     }
   });
   if (k.part)
-    hipLaunchKernelGGL(k_norm_join, dim3((unsigned)ceil_div(2 * p.c, 64)), dim3(1024), 0, st,
+    hipLaunchKernelGGL(k_norm_join, dim3((unsigned)ceil_div(2 * p.c, 32)), dim3(1024), 0, st,
                        k.part, q.blocks, (int)p.c, a.dw, a.db);
   return status();
 }

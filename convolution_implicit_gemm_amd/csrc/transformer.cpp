@@ -102,9 +102,9 @@ int fusedconv_layer_norm_create(const fusedconv_layer_norm_desc* d, fusedconv_la
     return fail(FUSEDCONV_ERR_OUTPUT_SHAPE, "n must be >= 0, c and inner >= 1");
   if (!(d->eps > 0.0f) || !isfinite(d->eps))
     return fail(FUSEDCONV_ERR_ATTR_VALUE, "eps must be positive and finite");
-  if (d->c > (1 << 24) || d->inner > INT32_MAX / 2 || product(1, d->c, d->inner, INT32_MAX / 2) < 0 ||
+  if (d->c > (1 << 24) || d->inner > INT32_MAX / 2 || product(1, d->c, d->inner, INT32_MAX / 4) < 0 ||
       product(d->n, d->c, d->inner, kMaxElements) < 0 || d->n > INT32_MAX / 2 ||
-      (d->inner > 1 && product(d->n, d->inner / 32 + 1, 1, INT32_MAX) < 0))
+      (d->inner > 1 && product(d->n, d->inner / 32 + 1, 1, INT32_MAX / 2) < 0))
     return fail(FUSEDCONV_ERR_TOO_LARGE, "X exceeds the index limits");
   const int64_t row = d->c * d->inner;
   if (d->n > 1 && (d->x_stride < row || d->dy_stride < row))

@@ -1,4 +1,5 @@
-// Element types of the transformer operators and 16-byte pieces of them.
+// Element types of the transformer operators, 16-byte pieces of them, sums over
+// lanes and the order of blocks.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,6 +28,51 @@ template <typename T, int V>
 __device__ __forceinline__ void store_piece(T* p, const Piece<T, V>& v) {
   *reinterpret_cast<Piece<T, V>*>(p) = v;
 }
+
+// Keeps the compiler from holding on to a piece's values converted to float
+// from one use to the next (twice the registers): it sees a new piece here.
+template <typename T, int V>
+__device__ __forceinline__ void stay_packed(Piece<T, V>& p) {
+  if constexpr (sizeof(Piece<T, V>) == 16 && sizeof(T) == 2) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    u4 r = __builtin_bit_cast(u4, p);
+    asm volatile("" : "+v"(r));
+    p = __builtin_bit_cast(Piece<T, V>, r);
+  }
+}
+
+// v plus the value of the lane OFF away (lane ^ OFF), without LDS.  OFF = 4 and
+// 8 read a mirrored lane: the same value once the offsets below have been
+// added, so sums over 8 or more lanes add 1, 2, 4, ... in this order.
+template <int OFF>
+__device__ __forceinline__ float add_lane(float v) {
+  if constexpr (OFF <= 8) {
+    constexpr int ctrl = OFF == 1 ? 0xB1 : OFF == 2 ? 0x4E : OFF == 4 ? 0x141 : 0x128;
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
+  } else if constexpr (OFF == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+}
+// Sum over the lanes that differ in the bits FROM, 2 * FROM, ... below TO.
+template <int FROM, int TO>
+__device__ __forceinline__ float lane_sum(float v) {
+  if constexpr (FROM < TO) return lane_sum<2 * FROM, TO>(add_lane<FROM>(v));
+  else return v;
+}
+
+// Blocks go round the 8 XCDs in launch order; this deals each XCD a run of
+// consecutive work items, so that neighbours (which read the same keys, or the
+// same queries) share its L2.  The grid is 8 * ceil(total / 8); an item >= total
+// has no work.
+__device__ __forceinline__ int xcd_item(int block, int total) {
+  const int run = (total + 7) >> 3;
+  return (block & 7) * run + (block >> 3);
+}
+inline unsigned xcd_grid(int64_t total) { return (unsigned)((total + 7) / 8 * 8); }
 
 // Run f(tag<T>) for the element type of a FUSEDCONV_* code.
 template <typename T>

@@ -14,7 +14,6 @@ results and the workspace are then allocated too.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -99,20 +98,26 @@ def _check(rc):
         raise FusedConvError(rc, _lib.fusedconv_last_error().decode())
 
 
-_DTYPES = None
+torch = None      # imported on first use, as the package itself does not need it
+_DTYPES = {}
+_current_handle = None
 
 
-def _dtypes():
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: _binding.F32, torch.float16: _binding.F16,
-                   torch.bfloat16: BF16}
-    return _DTYPES
+def _setup():
+    """First use: torch and the library."""
+    global torch, _current_handle
+    import torch
+    _load()
+    # the current stream's raw handle without a Stream object, where torch offers it: a third
+    # of what a small call costs on the host
+    _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _DTYPES.update({torch.float32: _binding.F32, torch.float16: _binding.F16,
+                    torch.bfloat16: BF16})
 
 
 def _code(t):
-    code = _dtypes().get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise FusedConvError(-2, f"dtype {t.dtype} is not float32, float16 or bfloat16")
     return code
@@ -138,22 +143,54 @@ def _expect_whole(name, t, shape, dtype, device):
 
 
 def _ptr(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr()
 
 
-@contextlib.contextmanager
+def _meta(t):
+    """What a call's checks and plan depend on, of one tensor: a call whose tensors' are those
+    of an earlier one runs its plan without further checks."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+class _On:
+    """Run on a device and stream (None: the device's current one), with torch allocating
+    there too: `with _On(device, stream) as handle`."""
+
+    def __init__(self, device, stream):
+        if stream is None:
+            self._context = torch.cuda.device(device)
+            self._device = device
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self._context = torch.cuda.stream(stream)
+            self._device = stream.device
+
+    def __enter__(self):
+        self._context.__enter__()
+        return torch.cuda.current_stream(self._device).cuda_stream
+
+    def __exit__(self, *error):
+        return self._context.__exit__(*error)
+
+
+class _Here:
+    """_On for the current stream of the current device: nothing to switch."""
+
+    def __init__(self, handle):
+        self._handle = handle
+
+    def __enter__(self):
+        return self._handle
+
+    def __exit__(self, *error):
+        return None
+
+
 def _on(device, stream):
-    """Run on `stream` (None: the device's current one): yields its raw handle, with torch
-    allocating on the same device and stream."""
-    import torch
-    if stream is None:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        yield stream.cuda_stream
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(_current_handle(device.index))
+    return _On(device, stream)
 
 
 def _strides(t):
@@ -186,14 +223,17 @@ class _Plan:
             self._h = None
 
 
-_plans: dict = {}
+_calls: dict = {}   # what a call's arguments look like -> its plan and its results' shapes
+_MOST_CALLS = 4096
 
 
-def _plan(cls, *key):
-    op = _plans.get((cls, key))
-    if op is None:
-        op = _plans[cls, key] = cls(*key)
-    return op
+def _remember(key, value):
+    """Keep at most _MOST_CALLS kinds of calls (a loop over growing views makes a new one
+    each time)."""
+    if len(_calls) >= _MOST_CALLS:
+        _calls.clear()
+    _calls[key] = value
+    return value
 
 
 # ---------------------------------------------------------------------- layer norm
@@ -268,13 +308,7 @@ def _stat_shape(t, axis):
     return shape[:-1] if axis == -1 else shape[:1] + shape[2:]
 
 
-def layer_norm(x, weight=None, bias=None, *, axis=-1, eps=1e-5, stats=False, out=None,
-               stream=None):
-    """y = (x - mean) * rstd * weight + bias over `axis` (-1: token rows, 1: the channels of an
-    NCHW tensor); (y, mean, rstd) with stats=True, the statistics in float32 with x's shape
-    without `axis`, as layer_norm_backward takes them.  weight and bias: [c], x's dtype.  x may
-    be a view whose rows (images) lie at one stride."""
-    import torch
+def _plan_layer_norm(x, weight, bias, axis, eps, out):
     code = _code(x)
     axis = _norm_axis(x, axis)
     if not x.is_cuda:
@@ -283,28 +317,36 @@ def layer_norm(x, weight=None, bias=None, *, axis=-1, eps=1e-5, stats=False, out
     for name, t in (("weight", weight), ("bias", bias)):
         if t is not None:
             _expect_whole(name, t, (c,), x.dtype, x.device)
-    op = _plan(LayerNorm, code, n, c, inner, step, c * inner, weight is not None,
-               bias is not None, float(eps))
+    if out is not None:
+        _expect_whole("out", out, tuple(x.shape), x.dtype, x.device)
+    op = LayerNorm(code, n, c, inner, step, c * inner, weight is not None, bias is not None,
+                   float(eps))
+    return op, _stat_shape(x, axis)
+
+
+def layer_norm(x, weight=None, bias=None, *, axis=-1, eps=1e-5, stats=False, out=None,
+               stream=None):
+    """y = (x - mean) * rstd * weight + bias over `axis` (-1: token rows, 1: the channels of an
+    NCHW tensor); (y, mean, rstd) with stats=True, the statistics in float32 with x's shape
+    without `axis`, as layer_norm_backward takes them.  weight and bias: [c], x's dtype.  x may
+    be a view whose rows (images) lie at one stride."""
+    if torch is None:
+        _setup()
+    key = ("layer_norm", _meta(x), _meta(weight), _meta(bias), axis, eps, _meta(out))
+    op, stat_shape = _calls.get(key) or _remember(
+        key, _plan_layer_norm(x, weight, bias, axis, eps, out))
     with _on(x.device, stream) as st:
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _expect_whole("out", out, tuple(x.shape), x.dtype, x.device)
         mean = rstd = None
         if stats:
-            shape = _stat_shape(x, axis)
-            mean = torch.empty(shape, dtype=torch.float32, device=x.device)
-            rstd = torch.empty(shape, dtype=torch.float32, device=x.device)
+            mean = torch.empty(stat_shape, dtype=torch.float32, device=x.device)
+            rstd = torch.empty(stat_shape, dtype=torch.float32, device=x.device)
         op.forward(x, weight, bias, out, mean, rstd, st)
     return (out, mean, rstd) if stats else out
 
 
-def layer_norm_backward(dy, x, weight, mean, rstd, *, axis=-1, weight_grad=True, bias_grad=True,
-                        stream=None):
-    """(dx, dweight, dbias) of layer_norm; mean and rstd are its statistics, weight None where it
-    had none.  dx has x's dtype, the weights' gradients are float32 [c] (None where not asked
-    for)."""
-    import torch
+def _plan_layer_norm_backward(dy, x, weight, mean, rstd, axis):
     code = _code(x)
     axis = _norm_axis(x, axis)
     if not x.is_cuda:
@@ -317,7 +359,20 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, axis=-1, weight_grad=True,
     shape = _stat_shape(x, axis)
     _expect_whole("mean", mean, shape, torch.float32, x.device)
     _expect_whole("rstd", rstd, shape, torch.float32, x.device)
-    op = _plan(LayerNorm, code, n, c, inner, step, dy_step, weight is not None, False, 1e-5)
+    return LayerNorm(code, n, c, inner, step, dy_step, weight is not None, False, 1e-5), c
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, axis=-1, weight_grad=True, bias_grad=True,
+                        stream=None):
+    """(dx, dweight, dbias) of layer_norm; mean and rstd are its statistics, weight None where it
+    had none.  dx has x's dtype, the weights' gradients are float32 [c] (None where not asked
+    for)."""
+    if torch is None:
+        _setup()
+    key = ("layer_norm_backward", _meta(dy), _meta(x), _meta(weight), _meta(mean), _meta(rstd),
+           axis)
+    op, c = _calls.get(key) or _remember(
+        key, _plan_layer_norm_backward(dy, x, weight, mean, rstd, axis))
     with _on(x.device, stream) as st:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dw = torch.empty(c, dtype=torch.float32, device=x.device) if weight_grad else None
@@ -348,6 +403,42 @@ class Rotary(_Plan):
                                          _ptr(inv_freq), _ptr(axes), _ptr(qo), _ptr(ko), stream))
 
 
+def _plan_rotary(q, k, positions, inv_freq, axes, interleaved, inverse, out_q, out_k):
+    code = _code(q)
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, len, heads, head_dim]")
+    b, s, h, d = (int(v) for v in q.shape)
+    hk = 0 if k is None else int(k.shape[2]) if k.dim() == 4 else -1
+    if hk < 0 or (k is not None and hk == 0):
+        raise ValueError("k must be [batch, len, kv_heads, head_dim] with at least one head")
+    if k is None and out_k is not None:
+        raise ValueError("out_k given without k")
+    qs = _heads_tensor("q", q, (b, s, h, d), q.dtype, q.device)
+    ks = kos = (0, 0, 0)
+    qos = _dense(b, s, h, d)
+    if out_q is not None:
+        qos = _heads_tensor("out_q", out_q, (b, s, h, d), q.dtype, q.device)
+    if k is not None:
+        ks = _heads_tensor("k", k, (b, s, hk, d), q.dtype, q.device)
+        kos = _dense(b, s, hk, d)
+        if out_k is not None:
+            kos = _heads_tensor("out_k", out_k, (b, s, hk, d), q.dtype, q.device)
+    pos_types = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+    if positions.dtype not in pos_types:
+        raise FusedConvError(-2, "positions are not int32, int64 or float32")
+    if positions.dim() != 3 or positions.shape[0] not in (1, b) or positions.shape[1] != s:
+        raise ValueError(f"positions must be [{b} or 1, {s}, num_axes]")
+    num_axes = int(positions.shape[2])
+    _expect_whole("positions", positions, tuple(positions.shape), positions.dtype, q.device)
+    pairs = int(inv_freq.numel())
+    _expect_whole("inv_freq", inv_freq, (pairs,), torch.float32, q.device)
+    _expect_whole("axes", axes, (pairs,), torch.int32, q.device)
+    op = Rotary(code, pos_types[positions.dtype], b, s, h, hk, d, pairs, num_axes,
+                0 if positions.shape[0] == 1 else s * num_axes, bool(interleaved),
+                bool(inverse), qs, ks, qos, kos)
+    return op, (b, s, h, d), (b, s, hk, d)
+
+
 def rotary(q, k, positions, inv_freq, axes, *, interleaved=False, inverse=False, out_q=None,
            out_k=None, stream=None):
     """Turn every head's pairs of values by their positions: (q', k'), or q' alone with k=None.
@@ -359,39 +450,18 @@ def rotary(q, k, positions, inv_freq, axes, *, interleaved=False, inverse=False,
     inv_freq[p].  Pair p is the values p and p + pairs, or 2p and 2p + 1 with interleaved=True;
     values behind 2 * pairs are copied.  inverse=True turns back: the gradient of the call.
     out_q / out_k: where to write (q and k themselves are allowed)."""
-    import torch
-    code = _code(q)
-    if q.dim() != 4:
-        raise ValueError("q must be [batch, len, heads, head_dim]")
-    b, s, h, d = (int(v) for v in q.shape)
-    hk = 0 if k is None else int(k.shape[2]) if k.dim() == 4 else -1
-    if hk < 0 or (k is not None and hk == 0):
-        raise ValueError("k must be [batch, len, kv_heads, head_dim] with at least one head")
-    qs = _heads_tensor("q", q, (b, s, h, d), q.dtype, q.device)
-    ks = _heads_tensor("k", k, (b, s, hk, d), q.dtype, q.device) if k is not None else (0, 0, 0)
-    pos_types = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
-    if positions.dtype not in pos_types:
-        raise FusedConvError(-2, "positions are not int32, int64 or float32")
-    if positions.dim() != 3 or positions.shape[0] not in (1, b) or positions.shape[1] != s:
-        raise ValueError(f"positions must be [{b} or 1, {s}, num_axes]")
-    num_axes = int(positions.shape[2])
-    _expect_whole("positions", positions, tuple(positions.shape), positions.dtype, q.device)
-    pairs = int(inv_freq.numel())
-    _expect_whole("inv_freq", inv_freq, (pairs,), torch.float32, q.device)
-    _expect_whole("axes", axes, (pairs,), torch.int32, q.device)
+    if torch is None:
+        _setup()
+    key = ("rotary", _meta(q), _meta(k), _meta(positions), _meta(inv_freq), _meta(axes),
+           interleaved, inverse, _meta(out_q), _meta(out_k))
+    op, q_shape, k_shape = _calls.get(key) or _remember(
+        key, _plan_rotary(q, k, positions, inv_freq, axes, interleaved, inverse, out_q, out_k))
     with _on(q.device, stream) as st:
         if out_q is None:
-            out_q = torch.empty((b, s, h, d), dtype=q.dtype, device=q.device)
+            out_q = torch.empty(q_shape, dtype=q.dtype, device=q.device)
         if k is not None and out_k is None:
-            out_k = torch.empty((b, s, hk, d), dtype=q.dtype, device=q.device)
-        qos = _heads_tensor("out_q", out_q, (b, s, h, d), q.dtype, q.device)
-        kos = (0, 0, 0)
-        if k is not None:
-            kos = _heads_tensor("out_k", out_k, (b, s, hk, d), q.dtype, q.device)
-        op = _plan(Rotary, code, pos_types[positions.dtype], b, s, h, hk, d, pairs, num_axes,
-                   0 if positions.shape[0] == 1 else s * num_axes, bool(interleaved),
-                   bool(inverse), qs, ks, qos, kos)
-        op.run(q, k, positions, inv_freq, axes, out_q, out_k if k is not None else None, st)
+            out_k = torch.empty(k_shape, dtype=q.dtype, device=q.device)
+        op.run(q, k, positions, inv_freq, axes, out_q, out_k, st)
     return out_q if k is None else (out_q, out_k)
 
 
@@ -425,7 +495,6 @@ class Attention(_Plan):
 
 def _attention_sizes(q, k, v, scale, causal, window, q_lengths, k_lengths):
     """Shapes, limits and strides of a call, checked: the first arguments of Attention."""
-    import torch
     code = _code(q)
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be [batch, len, heads, head_dim]")
@@ -455,6 +524,16 @@ def _dense(b, s, h, d):
     return (s * h * d if b > 1 else 0, h * d if s > 1 else 0, d if h > 1 else 0)
 
 
+def _plan_attention(q, k, v, scale, causal, window, q_lengths, k_lengths, out):
+    sizes, strides = _attention_sizes(q, k, v, scale, causal, window, q_lengths, k_lengths)
+    b, sq, sk, h, hk, d = sizes[1:7]
+    os_ = _dense(b, sq, h, d)
+    if out is not None:
+        os_ = _heads_tensor("out", out, (b, sq, h, d), q.dtype, q.device)
+    kd = _dense(b, sk, hk, d)
+    return Attention(*sizes, *strides, os_, os_, os_, kd, kd), (b, sq, h, d), (b, h, sq)
+
+
 def attention(q, k, v, *, scale=None, causal=False, window=None, q_lengths=None, k_lengths=None,
               lse=False, out=None, stream=None):
     """softmax(scale * q k^T) v: [batch, q_len, heads, head_dim]; (o, lse) with lse=True, the
@@ -467,16 +546,18 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, q_lengths=None,
     stands at k_length - q_length + i.  window=(left, right): the keys a query sees around its
     position, -1 without limit; causal=True is a window of 0 to the right.  A query that sees no
     key gets zeros and -inf."""
-    import torch
-    sizes, strides = _attention_sizes(q, k, v, scale, causal, window, q_lengths, k_lengths)
-    b, sq, sk, h, hk, d = sizes[1:7]
+    if torch is None:
+        _setup()
+    if window is not None:
+        window = tuple(window)
+    key = ("attention", _meta(q), _meta(k), _meta(v), scale, causal, window, _meta(q_lengths),
+           _meta(k_lengths), _meta(out))
+    op, shape, lse_shape = _calls.get(key) or _remember(
+        key, _plan_attention(q, k, v, scale, causal, window, q_lengths, k_lengths, out))
     with _on(q.device, stream) as st:
         if out is None:
-            out = torch.empty((b, sq, h, d), dtype=q.dtype, device=q.device)
-        os_ = _heads_tensor("out", out, (b, sq, h, d), q.dtype, q.device)
-        kd = _dense(b, sk, hk, d)
-        op = _plan(Attention, *sizes, *strides, os_, os_, os_, kd, kd)
-        sums = torch.empty((b, h, sq), dtype=torch.float32, device=q.device) if lse else None
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        sums = torch.empty(lse_shape, dtype=torch.float32, device=q.device) if lse else None
         ws = None
         if op.forward_bytes:
             ws = torch.empty(op.forward_bytes, dtype=torch.uint8, device=q.device)
@@ -484,28 +565,42 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, q_lengths=None,
     return (out, sums) if lse else out
 
 
-def attention_backward(do, q, k, v, o, lse, *, scale=None, causal=False, window=None,
-                       q_lengths=None, k_lengths=None, out=None, stream=None):
-    """(dq, dk, dv) of attention, from its output o and log-sum-exps; the other arguments as
-    there.  dk and dv sum over the query heads that share a key head.  out: the three tensors to
-    write (views of one packed gradient, say)."""
-    import torch
+def _plan_attention_backward(do, q, k, v, o, lse, scale, causal, window, q_lengths, k_lengths,
+                             out):
     sizes, strides = _attention_sizes(q, k, v, scale, causal, window, q_lengths, k_lengths)
     b, sq, sk, h, hk, d = sizes[1:7]
     os_ = _heads_tensor("o", o, (b, sq, h, d), q.dtype, q.device)
     dos = _heads_tensor("do", do, (b, sq, h, d), q.dtype, q.device)
     _expect_whole("lse", lse, (b, h, sq), torch.float32, q.device)
+    shapes = ((b, sq, h, d), (b, sk, hk, d), (b, sk, hk, d))
+    if out is None:
+        grads = [_dense(*shape) for shape in shapes]
+    else:
+        grads = [_heads_tensor(name, t, shape, q.dtype, q.device)
+                 for name, t, shape in zip(("dq", "dk", "dv"), out, shapes)]
+    return Attention(*sizes, *strides, os_, dos, *grads), shapes
+
+
+def attention_backward(do, q, k, v, o, lse, *, scale=None, causal=False, window=None,
+                       q_lengths=None, k_lengths=None, out=None, stream=None):
+    """(dq, dk, dv) of attention, from its output o and log-sum-exps; the other arguments as
+    there.  dk and dv sum over the query heads that share a key head.  out: the three tensors to
+    write (views of one packed gradient, say)."""
+    if torch is None:
+        _setup()
+    if window is not None:
+        window = tuple(window)
+    if out is not None:
+        out = tuple(out)
+    key = ("attention_backward", _meta(do), _meta(q), _meta(k), _meta(v), _meta(o), _meta(lse),
+           scale, causal, window, _meta(q_lengths), _meta(k_lengths),
+           None if out is None else tuple(_meta(t) for t in out))
+    op, shapes = _calls.get(key) or _remember(
+        key, _plan_attention_backward(do, q, k, v, o, lse, scale, causal, window, q_lengths,
+                                      k_lengths, out))
     with _on(q.device, stream) as st:
         if out is None:
-            dq = torch.empty((b, sq, h, d), dtype=q.dtype, device=q.device)
-            dk = torch.empty((b, sk, hk, d), dtype=q.dtype, device=q.device)
-            dv = torch.empty((b, sk, hk, d), dtype=q.dtype, device=q.device)
-        else:
-            dq, dk, dv = out
-        dqs = _heads_tensor("dq", dq, (b, sq, h, d), q.dtype, q.device)
-        dks = _heads_tensor("dk", dk, (b, sk, hk, d), q.dtype, q.device)
-        dvs = _heads_tensor("dv", dv, (b, sk, hk, d), q.dtype, q.device)
-        op = _plan(Attention, *sizes, *strides, os_, dos, dqs, dks, dvs)
+            out = tuple(torch.empty(shape, dtype=q.dtype, device=q.device) for shape in shapes)
         ws = torch.empty(op.backward_bytes, dtype=torch.uint8, device=q.device)
-        op.backward(do, q, k, v, o, lse, q_lengths, k_lengths, dq, dk, dv, ws, st)
-    return dq, dk, dv
+        op.backward(do, q, k, v, o, lse, q_lengths, k_lengths, *out, ws, st)
+    return out
