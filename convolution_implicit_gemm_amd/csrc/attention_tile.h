@@ -16,12 +16,18 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "sync.h"
 #include "transformer.h"
 #include "vec.h"
 
 namespace fc {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int I>
+using int_c = std::integral_constant<int, I>;
 
 template <typename T>
 struct Frag;
@@ -97,6 +103,7 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // read when it is issued.
 template <int BYTES>
 __device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t off, const void* base) {
+  to = __builtin_amdgcn_readfirstlane(to);
   if constexpr (BYTES == 16)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to),
                  "v"(off), "s"(base)
@@ -109,18 +116,21 @@ __device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t off, const voi
 
 // A tile of ROWS rows of DP values in LDS, in 16-byte chunks.  Chunk c of row r
 // lies at chunk c ^ swizzle(r) of the row, so that both ways of reading a tile
-// spread over all banks: 32 rows at one chunk (load_rows), and 4 rows at two
-// neighbouring chunks (load_columns; hence the reversed bits, which set
-// neighbouring rows far apart).  DP * sizeof(T) is 64, 128, 192, ... bytes; for
-// odd multiples of 64 two rows share a line of 128 bytes.
+// use all 64 banks (16 chunks) in every cycle: load_rows reads one chunk of 16
+// consecutive rows, load_columns four neighbouring chunks of 4 consecutive
+// rows.  Rows of 16 chunks (or 32) begin in the same bank: the swizzle takes 16
+// values, neighbouring rows 4 chunks apart.  Rows of 8 (24) chunks alternate
+// between two halves, and rows of 4 (12) run through four quarters by
+// themselves; the swizzle spreads the rows that meet.  With one that spread
+// over 32 banks only, half of all LDS cycles were conflicts.
 template <typename T, int DP>
 struct Tile {
   static constexpr int CE = 16 / sizeof(T);  // values of a chunk
   static constexpr int NC = DP / CE;         // chunks of a row
-  static constexpr bool kWhole = NC % 8 == 0;
   static __device__ __forceinline__ int swizzle(int row) {
-    if constexpr (kWhole) return ((row & 1) << 2) | (row & 2) | ((row >> 2) & 1);
-    else return (row & 2) | ((row >> 2) & 1);
+    if constexpr (NC % 16 == 0) return ((row & 3) << 2) | ((row >> 2) & 3);
+    else if constexpr (NC % 8 == 0) return ((row & 2) << 1) | ((row >> 2) & 3);
+    else return (row >> 2) & 3;
   }
   static constexpr int bytes(int rows) { return rows * DP * (int)sizeof(T); }
 
@@ -148,12 +158,12 @@ struct Tile {
       typedef short s4 __attribute__((ext_vector_type(4)));
       typedef short s8 __attribute__((ext_vector_type(8)));
       const int i = l & 15, g = (l >> 4) & 1;
-      const int row = 4 * h + (i >> 2);
-      const int chunk = (4 * t + 2 * g + ((i & 3) >> 1)) ^ swizzle(row);
-      const T* p = tile + (row0 + row) * DP + chunk * CE + 4 * (i & 1);
+      const int row = 4 * h + (i >> 2), chunk = 4 * t + 2 * g + ((i & 3) >> 1);
+      const T* p = tile + (row0 + row) * DP + 4 * (i & 1);
       typedef __attribute__((address_space(3))) s4 lds_s4;
-      const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
-      const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 8 * DP));
+      const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + (chunk ^ swizzle(row)) * CE));
+      const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s4*)(p + 8 * DP + (chunk ^ swizzle(row + 8)) * CE));
       return __builtin_bit_cast(frag_t<T>, s8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     } else {
       const int d = 32 * t + (l & 31);
@@ -179,7 +189,7 @@ struct Tile {
     static_assert(ROWS * NC % (64 * WAVES) == 0);
     static constexpr int period() {
       int p = 1;
-      while (p * 64 * WAVES % (8 * NC)) ++p;
+      while (p * 64 * WAVES % (16 * NC)) ++p;
       return p < kCalls ? p : kCalls;
     }
     static constexpr int kPeriod = period();
@@ -233,11 +243,14 @@ struct Tile {
   }
 };
 
-// Every copy this wave has started is in LDS, then the block meets: after it
-// all waves' copies can be read, and what was read before can be overwritten.
+// Waits until all but the last KEPT copies that this wave has started are in
+// LDS, then for the block: after it the tile in question can be read by all
+// waves, and what was read before can be overwritten.
+template <int KEPT>
 __device__ __forceinline__ void tile_barrier() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  static_assert(KEPT < 64);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(KEPT) : "memory");
+  lds_barrier();
 }
 
 // B fragments of 32 rows of a matrix in memory (terms: the row's d values), for
@@ -265,6 +278,35 @@ __device__ __forceinline__ frag_t<T> to_frag(const f32x16& c, int step) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = (T)c[8 * step + j];
   return f;
+}
+
+// The order in which a block of four waves walks tiles 0 .. count - 1 of two
+// matrices (waves 0 and 1 copy one, waves 2 and 3 the other; COPIES instructions
+// a wave): a ring of STAGES buffers, STAGES - 1 tiles ahead.  start(tile, buffer)
+// starts a tile's copies, use(tile, buffer) works on it; buffers are constants.
+template <int STAGES, int COPIES, typename Start, typename Use>
+__device__ __forceinline__ void walk_tiles(int count, Start&& start, Use&& use) {
+  static_assert(STAGES == 2 || STAGES == 3);
+  start(0, int_c<0>{});
+  if (STAGES == 3 && count > 1) start(1, int_c<1>{});
+  auto step = [&](int tile, auto N) {
+    // the tile has arrived (the one after it may be on its way), and everyone
+    // has left the buffer that is filled next
+    if (STAGES == 3 && tile + 1 < count) tile_barrier<(STAGES - 2) * COPIES>();
+    else tile_barrier<0>();
+    if (tile + STAGES - 1 < count) start(tile + STAGES - 1, int_c<(N + STAGES - 1) % STAGES>{});
+    use(tile, N);
+  };
+  for (int tile = 0;; tile += STAGES) {
+    step(tile, int_c<0>{});
+    if (tile + 1 >= count) return;
+    step(tile + 1, int_c<1>{});
+    if (tile + 2 >= count) return;
+    if constexpr (STAGES == 3) {
+      step(tile + 2, int_c<2>{});
+      if (tile + 3 >= count) return;
+    }
+  }
 }
 
 // What a batch entry's lengths and the window let a query see.

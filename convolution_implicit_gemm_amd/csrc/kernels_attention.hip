@@ -83,25 +83,33 @@ __device__ __forceinline__ void softmax_step(f32x16 (&s)[KB], Running<NT>& st, f
 // Keys key0 + c_row(...) outside [lo, hi) of this lane's query get -inf.
 template <int KB>
 __device__ __forceinline__ void mask_keys(f32x16 (&s)[KB], int key0, int lo, int hi, int h) {
+  const int from = key0 + 4 * h - lo;
+  const uint32_t many = max(hi - lo, 0);
 #pragma unroll
   for (int k = 0; k < KB; ++k)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int j = key0 + 32 * k + c_row(i, h);
-      if (j < lo || j >= hi) s[k][i] = -INFINITY;
+      if ((uint32_t)(from + 32 * k + c_row(i, 0)) >= many) s[k][i] = -INFINITY;
     }
 }
 
 // ------------------------------------------------------------ many queries
 // A block has 128 queries of one head, 32 a wave, and walks the keys in tiles
-// of BN, double-buffered in LDS: tile j + 1 is on its way while j is used.
+// of 32 through a ring of three LDS buffers.
+template <typename T, int DP>
+struct Many {
+  static constexpr int kStages = 3;
+  static constexpr int kTile = 32 * DP;  // values of a tile of K or V
+  static constexpr int kLds = kStages * 2 * kTile * (int)sizeof(T);
+};
+
 template <typename T, int DP>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK a) {
   using L = Tile<T, DP>;
-  constexpr int BN = sizeof(T) == 2 ? 64 : 32;
-  constexpr int KB = BN / 32, NT = DP / 32, NS = DP / 16;
+  using M = Many<T, DP>;
+  constexpr int NT = DP / 32, NS = DP / 16;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  T* tiles = (T*)lds;  // [2 buffers][K, V][BN * DP]
+  T* tiles = (T*)lds;  // [stages][K, V][32 * DP]
 
   const AttnParams& p = a.p;
   const int total = p.batch * p.heads * a.tiles;
@@ -118,63 +126,52 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
   const int i = row0 + wave * 32 + (lane & 31);
 
   // keys of the block, of the wave, and those that all rows of the wave see
-  const int first = row0 < see.nq ? see.lo(row0) & ~(BN - 1) : 0;
+  const int first = row0 < see.nq ? see.lo(row0) & ~31 : 0;
   const int end = row0 < see.nq ? see.hi(last_row) : 0;
   const int w0 = row0 + wave * 32, w1 = min(w0 + 31, see.nq - 1);
   const int wave_lo = see.lo(w0), wave_hi = w0 < see.nq ? see.hi(w1) : 0;
   const int all_lo = see.lo(w1), all_hi = w0 + 31 < see.nq ? see.hi(w0) : 0;
   const int lo = see.lo(i), hi = see.hi(i);
 
-  const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
-  const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
   Running<NT> st;
   st.start();
-  L::template clear_padding<4 * BN>(tiles, p.d, threadIdx.x, 256);
+  L::template clear_padding<M::kStages * 2 * 32>(tiles, p.d, threadIdx.x, 256);
   if (first < end) {
-    typename L::template Copier<BN, 4> ck, cv;
-    ck.init(p.k.s, p.d, wave);
-    cv.init(p.v.s, p.d, wave);
+    // waves 0 and 1 copy K, waves 2 and 3 V
+    typename L::template Copier<32, 2> copy;
+    const bool second = wave >= 2;
+    const T* src = second ? (const T*)a.v + b * p.v.b + kvh * p.v.h
+                          : (const T*)a.k + b * p.k.b + kvh * p.k.h;
+    const int64_t stride = second ? p.v.s : p.k.s;
+    copy.init(stride, p.d, wave & 1);
     frag_t<T> q[NS];
     const int qi = min(i, see.nq - 1);
     load_operand<T, DP>(q, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d,
                         p.scale < 0.f);
-    __syncthreads();
-    auto fetch = [&](int key0, T* to) {
-      ck.start(to, kp + key0 * p.k.s, see.nk - 1 - key0, wave);
-      cv.start(to + BN * DP, vp + key0 * p.v.s, see.nk - 1 - key0, wave);
+    lds_barrier();  // the padding is clear
+    auto start = [&](int tile, auto N) {
+      const int key0 = first + 32 * tile;
+      copy.start(tiles + (2 * N + second) * M::kTile, src + key0 * stride, see.nk - 1 - key0, wave & 1);
     };
-    fetch(first, tiles);
-    // one tile, from buffer N (a constant, so that it is part of the addresses)
-    auto step = [&](int key0, auto N) {
-      const T* kt = tiles + N * 2 * BN * DP;
-      const T* vt = kt + BN * DP;
-      tile_barrier();  // the tile has arrived; everyone is done with the other buffer
-      if (key0 + BN < end) fetch(key0 + BN, tiles + (N ^ 1) * 2 * BN * DP);
-      if (key0 >= wave_hi || key0 + BN <= wave_lo) return;
-      f32x16 s[KB];
+    auto use = [&](int tile, auto N) {
+      const int key0 = first + 32 * tile;
+      if (key0 >= wave_hi || key0 + 32 <= wave_lo) return;
+      const T* kt = tiles + 2 * N * M::kTile;
+      const T* vt = kt + M::kTile;
+      f32x16 s[1] = {zero16()};
 #pragma unroll
-      for (int k = 0; k < KB; ++k) s[k] = zero16();
-#pragma unroll
-      for (int d = 0; d < NS; ++d)
-#pragma unroll
-        for (int k = 0; k < KB; ++k) s[k] = mma(L::load_rows(kt, 32 * k, d), q[d], s[k]);
-      if (key0 < all_lo || key0 + BN > all_hi) mask_keys(s, key0, lo, hi, h);
+      for (int d = 0; d < NS; ++d) s[0] = mma(L::load_rows(kt, 0, d), q[d], s[0]);
+      if (key0 < all_lo || key0 + 32 > all_hi) mask_keys(s, key0, lo, hi, h);
       softmax_step(s, st, a.c);
 #pragma unroll
-      for (int k = 0; k < KB; ++k)
+      for (int d = 0; d < 2; ++d) {
+        const frag_t<T> pf = to_frag<T>(s[0], d);
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const frag_t<T> pf = to_frag<T>(s[k], d);
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-            st.o[t] = mma(L::load_columns(vt, 32 * k + 16 * d, t), pf, st.o[t]);
-        }
+        for (int t = 0; t < NT; ++t)
+          st.o[t] = mma(L::load_columns(vt, 16 * d, t), pf, st.o[t]);
+      }
     };
-    for (int key0 = first; key0 < end; key0 += 2 * BN) {
-      step(key0, std::integral_constant<int, 0>{});
-      if (key0 + BN >= end) break;
-      step(key0 + BN, std::integral_constant<int, 1>{});
-    }
+    walk_tiles<M::kStages, decltype(copy)::kCalls>((end - first + 31) / 32, start, use);
   }
   if (i >= p.sq) return;
   const float l = half_sum(st.l);
@@ -390,7 +387,7 @@ int FC_DP_NAME(attention_forward_)(const AttnPlan& plan, const AttnK& k, hipStre
                            dim3(256), 0, st, k);
     } else {
       auto fn = k_attention<T, FC_DP>;
-      constexpr int bytes = 4 * Tile<T, FC_DP>::bytes(sizeof(T) == 2 ? 64 : 32);
+      constexpr int bytes = Many<T, FC_DP>::kLds;
       rc = set_max_dynamic_lds((const void*)fn, bytes);
       if (rc != FUSEDCONV_OK) return;
       hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.heads * k.tiles)), dim3(256), bytes,

@@ -69,27 +69,28 @@ __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
 // A block has 128 keys of one key head, 32 a wave: K and V rows as B operands,
 // so a lane holds one key and 16 of a tile's queries; dk^T and dv^T stay in
 // registers while the block walks the queries of every head that shares the
-// key head, BQ at a time, double-buffered.
+// key head, 32 at a time.
 template <typename T, int DP>
 struct KeyBlock {
   // dk, dv, K and V of 32 keys are 4 * DP / 2 registers a lane, all of the 256
   // that two waves a SIMD leave at DP = 128: there V is read from LDS, a fifth
-  // more LDS reads, and the query tiles are half as long to make room.
+  // more LDS reads, and the ring is one buffer shorter to make room.
   static constexpr bool kVInLds = DP == 128;
-  static constexpr int kRows = sizeof(T) == 2 && !kVInLds ? 64 : 32;
-  static constexpr int kLds = Tile<T, DP>::bytes(4 * kRows + (kVInLds ? 128 : 0)) + 256 * 4;
+  static constexpr int kStages = kVInLds ? 2 : 3;
+  static constexpr int kTile = 32 * DP;  // values of a tile of Q or dO
+  static constexpr int kLds =
+      (kStages * 2 + (kVInLds ? 4 : 0)) * kTile * (int)sizeof(T) + kStages * 64 * 4;
 };
 
 template <typename T, int DP>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dkdv(AttnBwdK a) {
   using L = Tile<T, DP>;
   using B = KeyBlock<T, DP>;
-  constexpr int BQ = B::kRows;
   constexpr int NT = DP / 32, NS = DP / 16;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  T* tiles = (T*)lds;                                    // [2][Q, dO][BQ * DP]
-  T* vt = tiles + 4 * BQ * DP;                           // V [128 * DP], where it is not in registers
-  float* rows = (float*)(lds + B::kLds) - 256;           // [2][nlse, ndelta][64]
+  T* tiles = (T*)lds;                             // [stages][Q, dO][32 * DP]
+  T* vt = tiles + B::kStages * 2 * B::kTile;      // V [128 * DP], where it is not in registers
+  float* rows = (float*)(lds + B::kLds) - B::kStages * 64;  // [stages][nlse, ndelta][32]
 
   const AttnParams& p = a.p;
   const int total = p.batch * p.kv_heads * a.k_tiles;
@@ -109,17 +110,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dkdv(
   const int w0 = key0 + wave * 32, w1 = min(w0 + 31, see.nk - 1);
   const int j = w0 + (lane & 31);
 
-  const int first = key0 < see.nk ? see.qlo(key0) & ~(BQ - 1) : 0;
+  const int first = key0 < see.nk ? see.qlo(key0) & ~31 : 0;
   const int end = key0 < see.nk ? see.qhi(last_key) : 0;
   const int wave_lo = see.qlo(w0), wave_hi = w0 < see.nk ? see.qhi(w1) : 0;
   const int all_lo = see.qlo(w1), all_hi = see.qhi(w0);
-  const int lo = see.qlo(j), hi = see.qhi(j);
+  const int lo = see.qlo(j);
+  const uint32_t many = max(see.qhi(j) - lo, 0);
 
   f32x16 dk[NT], dv[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) dk[t] = dv[t] = zero16();
 
-  L::template clear_padding<4 * BQ + (B::kVInLds ? 128 : 0)>(tiles, p.d, threadIdx.x, 256);
+  L::template clear_padding<B::kStages * 64 + (B::kVInLds ? 128 : 0)>(tiles, p.d, threadIdx.x, 256);
   if (first < end) {
     frag_t<T> kf[NS], vf[B::kVInLds ? 1 : NS];
     const int ji = min(j, see.nk - 1);
@@ -127,77 +129,70 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dkdv(
     const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
     if constexpr (!B::kVInLds) load_operand<T, DP>(vf, vp + ji * p.v.s, p.d, false);
 
-    typename L::template Copier<BQ, 4> cq, co;
-    cq.init(p.q.s, p.d, wave);
-    co.init(p.dout.s, p.d, wave);
-    const int items = (end - first + BQ - 1) / BQ;
-    // query tile `it` of query head g of the group, to buffer N
-    auto fetch = [&](int g, int it, auto N) {
-      const int head = kvh * p.group + g, row0 = first + it * BQ;
-      T* to = tiles + N * 2 * BQ * DP;
-      cq.start(to, (const T*)a.q + b * p.q.b + head * p.q.h + row0 * p.q.s, see.nq - 1 - row0, wave);
-      co.start(to + BQ * DP, (const T*)a.dout + b * p.dout.b + head * p.dout.h + row0 * p.dout.s,
-               see.nq - 1 - row0, wave);
-      if (wave < 2 && lane < BQ)
-        copy_to_lds<4>(lds_offset(rows + N * 128 + wave * 64), lane * 4,
-                       (wave ? a.ndelta : a.nlse) + ((int64_t)b * p.heads + head) * a.padded + row0);
-    };
-    __syncthreads();
+    // waves 0 and 1 copy Q and nlse, waves 2 and 3 dO and ndelta
+    typename L::template Copier<32, 2> copy;
+    const bool second = wave >= 2;
+    const Strides3 st = second ? p.dout : p.q;
+    const T* src = (second ? (const T*)a.dout : (const T*)a.q) + b * st.b + kvh * p.group * st.h;
+    const float* row_src = (second ? a.ndelta : a.nlse) +
+                           ((int64_t)b * p.heads + kvh * p.group) * a.padded;
+    copy.init(st.s, p.d, wave & 1);
+    lds_barrier();  // the padding is clear
     if constexpr (B::kVInLds) {
       typename L::template Copier<128, 4> cv;
       cv.init(p.v.s, p.d, wave);
       cv.start(vt, vp + key0 * p.v.s, see.nk - 1 - key0, wave);
     }
-    fetch(0, 0, std::integral_constant<int, 0>{});
-    int g = 0, it = 0;
-    auto step = [&](auto N) {
-      const int row0 = first + it * BQ;
-      if (++it == items) it = 0, ++g;
-      tile_barrier();
-      if (g < p.group) fetch(g, it, std::integral_constant<int, N ^ 1>{});
-      if (row0 >= wave_hi || row0 + BQ <= wave_lo) return;
-      const T* qt = tiles + N * 2 * BQ * DP;
-      const T* ot = qt + BQ * DP;
-      const float* rt = rows + N * 128;
-      const bool masked = row0 < all_lo || row0 + BQ > all_hi;
+    const int items = (end - first + 31) / 32;
+    // Tiles are numbered through the heads of the group: where the next one to
+    // copy and the next one to use are.
+    int start_g = 0, start_row = first, use_row = first;
+    auto start = [&](int, auto N) {
+      copy.start(tiles + (2 * N + second) * B::kTile,
+                 src + start_g * st.h + start_row * st.s, see.nq - 1 - start_row, wave & 1);
+      if (lane < 32)
+        copy_to_lds<4>(lds_offset(rows + N * 64 + second * 32), lane * 4,
+                       row_src + (int64_t)start_g * a.padded + start_row);
+      start_row += 32;
+      if (start_row >= end) start_row = first, ++start_g;
+    };
+    auto use = [&](int, auto N) {
+      const int row0 = use_row;
+      use_row += 32;
+      if (use_row >= end) use_row = first;
+      if (row0 >= wave_hi || row0 + 32 <= wave_lo) return;
+      const T* qt = tiles + 2 * N * B::kTile;
+      const T* ot = qt + B::kTile;
+      const float* rt = rows + N * 64;
+      f32x16 s = load_c_rows(rt, h), dp = load_c_rows(rt + 32, h);
 #pragma unroll
-      for (int r = 0; r < BQ; r += 32) {
-        f32x16 s = load_c_rows(rt + r, h), dp = load_c_rows(rt + 64 + r, h);
+      for (int d = 0; d < NS; ++d) {
+        s = mma(L::load_rows(qt, 0, d), kf[d], s);
+        if constexpr (B::kVInLds)
+          dp = mma(L::load_rows(ot, 0, d), L::load_rows(vt, wave * 32, d), dp);
+        else
+          dp = mma(L::load_rows(ot, 0, d), vf[d], dp);
+      }
+      if (row0 < all_lo || row0 + 32 > all_hi)
 #pragma unroll
-        for (int d = 0; d < NS; ++d) {
-          s = mma(L::load_rows(qt, r, d), kf[d], s);
-          if constexpr (B::kVInLds)
-            dp = mma(L::load_rows(ot, r, d), L::load_rows(vt, wave * 32, d), dp);
-          else
-            dp = mma(L::load_rows(ot, r, d), vf[d], dp);
-        }
-        if (masked)
+        for (int i = 0; i < 16; ++i)
+          if ((uint32_t)(row0 + 4 * h - lo + c_row(i, 0)) >= many) s[i] = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = row0 + r + c_row(i, h);
-            if (at < lo || at >= hi) s[i] = -INFINITY;
-          }
+      for (int i = 0; i < 16; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(s[i] * a.c);
+        dp[i] *= s[i];
+      }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[i] = __builtin_amdgcn_exp2f(s[i] * a.c);
-          dp[i] *= s[i];
-        }
+      for (int d = 0; d < 2; ++d) {
+        const frag_t<T> pf = to_frag<T>(s, d), df = to_frag<T>(dp, d);
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const frag_t<T> pf = to_frag<T>(s, d), df = to_frag<T>(dp, d);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            dv[t] = mma(L::load_columns(ot, r + 16 * d, t), pf, dv[t]);
-            dk[t] = mma(L::load_columns(qt, r + 16 * d, t), df, dk[t]);
-          }
+        for (int t = 0; t < NT; ++t) {
+          dv[t] = mma(L::load_columns(ot, 16 * d, t), pf, dv[t]);
+          dk[t] = mma(L::load_columns(qt, 16 * d, t), df, dk[t]);
         }
       }
     };
-    while (g < p.group) {
-      step(std::integral_constant<int, 0>{});
-      if (g >= p.group) break;
-      step(std::integral_constant<int, 1>{});
-    }
+    walk_tiles<B::kStages, decltype(copy)::kCalls + 1>(items * p.group, start, use);
   }
   if (j >= p.sk) return;
   const float keep = j < see.nk ? 1.f : 0.f;
@@ -225,10 +220,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dkdv(
 template <typename T, int DP>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(AttnBwdK a) {
   using L = Tile<T, DP>;
-  constexpr int BN = sizeof(T) == 2 ? 64 : 32;
+  constexpr int kStages = 3, kTile = 32 * DP;
   constexpr int NT = DP / 32, NS = DP / 16;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  T* tiles = (T*)lds;  // [2][K, V][BN * DP]
+  T* tiles = (T*)lds;  // [stages][K, V][32 * DP]
 
   const AttnParams& p = a.p;
   const int total = p.batch * p.heads * a.q_tiles;
@@ -244,26 +239,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(At
   const int w0 = row0 + wave * 32, w1 = min(w0 + 31, see.nq - 1);
   const int i = w0 + (lane & 31);
 
-  const int first = row0 < see.nq ? see.lo(row0) & ~(BN - 1) : 0;
+  const int first = row0 < see.nq ? see.lo(row0) & ~31 : 0;
   const int end = row0 < see.nq ? see.hi(last_row) : 0;
   const int wave_lo = see.lo(w0), wave_hi = w0 < see.nq ? see.hi(w1) : 0;
   const int all_lo = see.lo(w1), all_hi = w0 + 31 < see.nq ? see.hi(w0) : 0;
-  const int lo = see.lo(i), hi = see.hi(i);
+  const int lo = see.lo(i);
+  const uint32_t many = max(see.hi(i) - lo, 0);
 
   f32x16 dq[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) dq[t] = zero16();
-  L::template clear_padding<4 * BN>(tiles, p.d, threadIdx.x, 256);
+  L::template clear_padding<kStages * 2 * 32>(tiles, p.d, threadIdx.x, 256);
   if (first < end) {
-    const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
-    const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
-    typename L::template Copier<BN, 4> ck, cv;
-    ck.init(p.k.s, p.d, wave);
-    cv.init(p.v.s, p.d, wave);
-    auto fetch = [&](int key0, T* to) {
-      ck.start(to, kp + key0 * p.k.s, see.nk - 1 - key0, wave);
-      cv.start(to + BN * DP, vp + key0 * p.v.s, see.nk - 1 - key0, wave);
-    };
+    // waves 0 and 1 copy K, waves 2 and 3 V
+    typename L::template Copier<32, 2> copy;
+    const bool second = wave >= 2;
+    const T* src = second ? (const T*)a.v + b * p.v.b + kvh * p.v.h
+                          : (const T*)a.k + b * p.k.b + kvh * p.k.h;
+    const int64_t stride = second ? p.v.s : p.k.s;
+    copy.init(stride, p.d, wave & 1);
     frag_t<T> qf[NS], of[NS];
     const int qi = min(i, see.nq - 1);
     load_operand<T, DP>(qf, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d, p.scale < 0.f);
@@ -271,46 +265,38 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_dq(At
     const int64_t at = ((int64_t)b * p.heads + head) * a.padded;
     const float nlse = i < a.padded ? a.nlse[at + i] : -INFINITY;
     const float ndelta = i < a.padded ? a.ndelta[at + i] : 0.f;
-    __syncthreads();
-    fetch(first, tiles);
-    auto step = [&](int key0, auto N) {
-      tile_barrier();
-      if (key0 + BN < end) fetch(key0 + BN, tiles + (N ^ 1) * 2 * BN * DP);
-      if (key0 >= wave_hi || key0 + BN <= wave_lo) return;
-      const T* kt = tiles + N * 2 * BN * DP;
-      const T* vt = kt + BN * DP;
-      const bool masked = key0 < all_lo || key0 + BN > all_hi;
+    lds_barrier();  // the padding is clear
+    auto start = [&](int tile, auto N) {
+      const int key0 = first + 32 * tile;
+      copy.start(tiles + (2 * N + second) * kTile, src + key0 * stride, see.nk - 1 - key0, wave & 1);
+    };
+    auto use = [&](int tile, auto N) {
+      const int key0 = first + 32 * tile;
+      if (key0 >= wave_hi || key0 + 32 <= wave_lo) return;
+      const T* kt = tiles + 2 * N * kTile;
+      const T* vt = kt + kTile;
+      f32x16 s, dp;
 #pragma unroll
-      for (int r = 0; r < BN; r += 32) {
-        f32x16 s, dp;
+      for (int e = 0; e < 16; ++e) s[e] = nlse, dp[e] = ndelta;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] = nlse, dp[e] = ndelta;
+      for (int d = 0; d < NS; ++d) {
+        s = mma(L::load_rows(kt, 0, d), qf[d], s);
+        dp = mma(L::load_rows(vt, 0, d), of[d], dp);
+      }
+      if (key0 < all_lo || key0 + 32 > all_hi)
 #pragma unroll
-        for (int d = 0; d < NS; ++d) {
-          s = mma(L::load_rows(kt, r, d), qf[d], s);
-          dp = mma(L::load_rows(vt, r, d), of[d], dp);
-        }
-        if (masked)
+        for (int e = 0; e < 16; ++e)
+          if ((uint32_t)(key0 + 4 * h - lo + c_row(e, 0)) >= many) s[e] = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int key = key0 + r + c_row(e, h);
-            if (key < lo || key >= hi) s[e] = -INFINITY;
-          }
+      for (int e = 0; e < 16; ++e) dp[e] *= __builtin_amdgcn_exp2f(s[e] * a.c);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) dp[e] *= __builtin_amdgcn_exp2f(s[e] * a.c);
+      for (int d = 0; d < 2; ++d) {
+        const frag_t<T> df = to_frag<T>(dp, d);
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const frag_t<T> df = to_frag<T>(dp, d);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) dq[t] = mma(L::load_columns(kt, r + 16 * d, t), df, dq[t]);
-        }
+        for (int t = 0; t < NT; ++t) dq[t] = mma(L::load_columns(kt, 16 * d, t), df, dq[t]);
       }
     };
-    for (int key0 = first; key0 < end; key0 += 2 * BN) {
-      step(key0, std::integral_constant<int, 0>{});
-      if (key0 + BN >= end) break;
-      step(key0 + BN, std::integral_constant<int, 1>{});
-    }
+    walk_tiles<kStages, decltype(copy)::kCalls>((end - first + 31) / 32, start, use);
   }
   if (i >= p.sq) return;
   T* out = (T*)a.dq + b * p.dq.b + i * p.dq.s + head * p.dq.h;
@@ -335,8 +321,6 @@ int FC_DP_NAME(attention_backward_)(const AttnPlan& plan, const AttnBwdK& k, hip
   with_type(plan.dtype, [&](auto tag) {
     using T = typename decltype(tag)::type;
     const AttnParams& p = k.p;
-    constexpr int rows = sizeof(T) == 2 ? 64 : 32;
-    constexpr int tile_bytes = 4 * Tile<T, FC_DP>::bytes(rows);
     if (p.sq > 0)
       hipLaunchKernelGGL((k_attention_rows<T>),
                          dim3((unsigned)(((int64_t)p.batch * p.heads * k.padded + 31) / 32)),
@@ -351,10 +335,11 @@ int FC_DP_NAME(attention_backward_)(const AttnPlan& plan, const AttnBwdK& k, hip
     }
     if (p.sq > 0) {
       auto fn = k_attention_dq<T, FC_DP>;
-      rc = set_max_dynamic_lds((const void*)fn, tile_bytes);
+      constexpr int bytes = 3 * 2 * Tile<T, FC_DP>::bytes(32);
+      rc = set_max_dynamic_lds((const void*)fn, bytes);
       if (rc != FUSEDCONV_OK) return;
       hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.heads * k.q_tiles)), dim3(256),
-                         tile_bytes, st, k);
+                         bytes, st, k);
     }
   });
   if (rc != FUSEDCONV_OK) return rc;
