@@ -95,12 +95,11 @@ __device__ __forceinline__ void mask_keys(f32x16 (&s)[KB], int key0, int lo, int
 
 // ------------------------------------------------------------ many queries
 // A block has 128 queries of one head, 32 a wave, and walks the keys in tiles
-// of 32 through a ring of three LDS buffers.
+// of 32 through two LDS buffers.
 template <typename T, int DP>
 struct Many {
-  static constexpr int kStages = 3;
   static constexpr int kTile = 32 * DP;  // values of a tile of K or V
-  static constexpr int kLds = kStages * 2 * kTile * (int)sizeof(T);
+  static constexpr int kLds = 4 * kTile * (int)sizeof(T);
 };
 
 template <typename T, int DP>
@@ -109,7 +108,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
   using M = Many<T, DP>;
   constexpr int NT = DP / 32, NS = DP / 16;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  T* tiles = (T*)lds;  // [stages][K, V][32 * DP]
+  T* tiles = (T*)lds;  // [2 buffers][K, V][32 * DP]
 
   const AttnParams& p = a.p;
   const int total = p.batch * p.heads * a.tiles;
@@ -135,7 +134,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
 
   Running<NT> st;
   st.start();
-  L::template clear_padding<M::kStages * 2 * 32>(tiles, p.d, threadIdx.x, 256);
+  L::template clear_padding<4 * 32>(tiles, p.d, threadIdx.x, 256);
   if (first < end) {
     // waves 0 and 1 copy K, waves 2 and 3 V
     typename L::template Copier<32, 2> copy;
@@ -159,8 +158,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
       const T* kt = tiles + 2 * N * M::kTile;
       const T* vt = kt + M::kTile;
       f32x16 s[1] = {zero16()};
-#pragma unroll
-      for (int d = 0; d < NS; ++d) s[0] = mma(L::load_rows(kt, 0, d), q[d], s[0]);
+      each_step<NS>(p.d, [&](auto d) { s[0] = mma(L::load_rows(kt, 0, d), q[d], s[0]); });
       if (key0 < all_lo || key0 + 32 > all_hi) mask_keys(s, key0, lo, hi, h);
       softmax_step(s, st, a.c);
 #pragma unroll
@@ -171,7 +169,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
           st.o[t] = mma(L::load_columns(vt, 16 * d, t), pf, st.o[t]);
       }
     };
-    walk_tiles<M::kStages, decltype(copy)::kCalls>((end - first + 31) / 32, start, use);
+    walk_tiles((end - first + 31) / 32, start, use);
   }
   if (i >= p.sq) return;
   const float l = half_sum(st.l);
@@ -273,8 +271,7 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
       const T* vt = kt + F::kTile;
       const int key0 = first + 32 * tile;
       f32x16 s[1] = {zero16()};
-#pragma unroll
-      for (int d = 0; d < NS; ++d) s[0] = mma(L::load_rows(kt, 0, d), q[d], s[0]);
+      each_step<NS>(p.d, [&](auto d) { s[0] = mma(L::load_rows(kt, 0, d), q[d], s[0]); });
       if (!all_rows || key0 < all_lo || key0 + 32 > all_hi) mask_keys(s, key0, lo, hi, h);
       softmax_step(s, st, a.c);
 #pragma unroll
