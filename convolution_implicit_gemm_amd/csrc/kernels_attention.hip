@@ -24,10 +24,14 @@ struct AttnK {
   const int32_t *q_lengths, *k_lengths;
   void* o;
   float* lse;
-  float *part_o, *part_lse;  // split form: [units][splits][rows][d], [units][splits][rows]
+  // Partial results where the keys are split over blocks: [units][splits][rows][d]
+  // and (base-2 logs) [units][splits][rows].  Few queries: a unit is a key head of
+  // an entry, its rows query-major.  Many: a unit is a query head.
+  float *part_o, *part_lse;
   float c;                   // |scale| * log2(e), at least kLeastC
   int32_t tiles;             // row tiles of one head (tile form)
   int32_t splits, rows, row_groups;
+  int32_t unit_heads, unit_group;  // heads that units count, and query heads of a unit
 };
 
 namespace {
@@ -111,9 +115,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
   T* tiles = (T*)lds;  // [2 buffers][K, V][32 * DP]
 
   const AttnParams& p = a.p;
-  const int total = p.batch * p.heads * a.tiles;
+  const int total = p.batch * p.heads * a.tiles * a.splits;
   int item = xcd_item(blockIdx.x, total);
   if (item >= total) return;
+  const int split = item % a.splits;
+  item /= a.splits;
   // the last rows first: under a causal window they have the most keys
   const int tile_q = a.tiles - 1 - item % a.tiles;
   item /= a.tiles;
@@ -125,8 +131,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
   const int i = row0 + wave * 32 + (lane & 31);
 
   // keys of the block, of the wave, and those that all rows of the wave see
-  const int first = row0 < see.nq ? see.lo(row0) & ~31 : 0;
-  const int end = row0 < see.nq ? see.hi(last_row) : 0;
+  int first = row0 < see.nq ? see.lo(row0) & ~31 : 0;
+  int end = row0 < see.nq ? see.hi(last_row) : 0;
+  if (a.splits > 1) {  // this block's share of the tiles
+    const int count = max(end - first + 31, 0) >> 5, from = first;
+    first = from + 32 * (int)((int64_t)count * split / a.splits);
+    end = min(end, from + 32 * (int)((int64_t)count * (split + 1) / a.splits));
+  }
   const int w0 = row0 + wave * 32, w1 = min(w0 + 31, see.nq - 1);
   const int wave_lo = see.lo(w0), wave_hi = w0 < see.nq ? see.hi(w1) : 0;
   const int all_lo = see.lo(w1), all_hi = w0 + 31 < see.nq ? see.hi(w0) : 0;
@@ -174,6 +185,22 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
   if (i >= p.sq) return;
   const float l = half_sum(st.l);
   const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;  // no key seen: zeros
+  if (a.splits > 1) {
+    const int64_t part = ((int64_t)(b * p.heads + head) * a.splits + split) * p.sq + i;
+    float* o = a.part_o + part * p.d;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (32 * t + 8 * g >= p.d) continue;
+        Piece<float, 4> po;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) po.v[j] = st.o[t][4 * g + j] * inv;
+        store_piece<float, 4>(o + 32 * t + 8 * g + 4 * h, po);
+      }
+    if (h == 0) a.part_lse[part] = l == 0.f ? -INFINITY : st.m * a.c + log2f(l);
+    return;
+  }
   T* o = (T*)a.o + b * p.o.b + i * p.o.s + head * p.o.h;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -328,36 +355,54 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
   }
 }
 
-// Joins the splits of a row: 64 threads a row, 4 rows a block.
+// Joins the splits of a row: 32 lanes a row, four values each, 8 rows a block.
+// The weights 2^(lse - max) / sum are worked out by one lane a split, 32 at a
+// time (against a running maximum), so a row waits for memory twice and not
+// twice per split.
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_join(AttnK a) {
   const AttnParams& p = a.p;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (at >= (int64_t)p.batch * p.kv_heads * a.rows) return;
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (at >= (int64_t)p.batch * a.unit_heads * a.rows) return;
+  const int lane = threadIdx.x & 31;
   const int64_t unit = at / a.rows;
   const int r = (int)(at - unit * a.rows);
-  const int b = (int)(unit / p.kv_heads), kvh = (int)(unit % p.kv_heads);
-  const int i = r / p.group, head = kvh * p.group + r % p.group;
+  const int b = (int)(unit / a.unit_heads), uh = (int)(unit % a.unit_heads);
+  const int i = r / a.unit_group, head = uh * a.unit_group + r % a.unit_group;
   const float* lse = a.part_lse + unit * a.splits * a.rows + r;
   const float* po = a.part_o + (unit * a.splits * a.rows + r) * p.d;
-  float m = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, lse[(int64_t)s * a.rows]);
-  float sum = 0.f, acc[2] = {0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const float l = lse[(int64_t)s * a.rows];
-    const float f = l == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(l - m);
-    sum += f;
+  const bool live = lane * 4 < p.d;
+  float m = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < a.splits; s0 += 32) {
+    const int n = min(32, a.splits - s0);
+    const float l = lane < n ? lse[(int64_t)(s0 + lane) * a.rows] : -INFINITY;
+    float top = l;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (lane + 64 * e < p.d) acc[e] += f * po[(int64_t)s * a.rows * p.d + lane + 64 * e];
+    for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 32));
+    const float next = fmaxf(m, top);
+    const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
+    const float w = l == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(l - next);
+    sum = sum * keep + lane_sum<1, 32>(w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= keep;
+    m = next;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float f = __shfl(w, s, 32);
+      if (live && f != 0.f) {
+        const Piece<float, 4> x = load_piece<float, 4>(po + (int64_t)(s0 + s) * a.rows * p.d + lane * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += f * x.v[e];
+      }
+    }
   }
   const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+  if (live) {
+    Piece<T, 4> out;
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    if (lane + 64 * e < p.d)
-      ((T*)a.o)[b * p.o.b + i * p.o.s + head * p.o.h + lane + 64 * e] = to_type<T>(acc[e] * inv);
+    for (int e = 0; e < 4; ++e) out.v[e] = to_type<T>(acc[e] * inv);
+    store_piece<T, 4>((T*)a.o + b * p.o.b + i * p.o.s + head * p.o.h + lane * 4, out);
+  }
   if (lane == 0 && a.lse)
     a.lse[((int64_t)b * p.heads + head) * p.sq + i] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
@@ -378,18 +423,18 @@ int FC_DP_NAME(attention_forward_)(const AttnPlan& plan, const AttnK& k, hipStre
       if (rc != FUSEDCONV_OK) return;
       hipLaunchKernelGGL(fn, dim3((unsigned)(p.batch * p.kv_heads * k.row_groups * k.splits)),
                          dim3(64 * Few<T, FC_DP>::kWaves), bytes, st, k);
-      if (k.splits > 1)
-        hipLaunchKernelGGL((k_attention_join<T>),
-                           dim3((unsigned)(((int64_t)p.batch * p.kv_heads * k.rows + 3) / 4)),
-                           dim3(256), 0, st, k);
     } else {
       auto fn = k_attention<T, FC_DP>;
       constexpr int bytes = Many<T, FC_DP>::kLds;
       rc = set_max_dynamic_lds((const void*)fn, bytes);
       if (rc != FUSEDCONV_OK) return;
-      hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.heads * k.tiles)), dim3(256), bytes,
-                         st, k);
+      hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.heads * k.tiles * k.splits)),
+                         dim3(256), bytes, st, k);
     }
+    if (k.splits > 1)
+      hipLaunchKernelGGL((k_attention_join<T>),
+                         dim3((unsigned)(((int64_t)p.batch * k.unit_heads * k.rows + 7) / 8)),
+                         dim3(256), 0, st, k);
   });
   if (rc != FUSEDCONV_OK) return rc;
   return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH;
@@ -400,26 +445,37 @@ int attention_forward_64(const AttnPlan&, const AttnK&, hipStream_t);
 int attention_forward_96(const AttnPlan&, const AttnK&, hipStream_t);
 int attention_forward_128(const AttnPlan&, const AttnK&, hipStream_t);
 
-// Bytes of the split form's partial results.
-static size_t split_bytes(const AttnParams& p, int splits) {
-  const size_t rows = (size_t)p.batch * p.kv_heads * splits * p.sq * p.group;
-  return rows * (p.d + 4) * sizeof(float);
-}
-
 void plan_attention(const AttnParams& p, AttnPlan& plan) {
   plan.dp = p.d <= 32 ? 32 : p.d <= 64 ? 64 : p.d <= 96 ? 96 : 128;
   const int64_t rows = (int64_t)p.sq * p.group;
-  plan.few = rows <= 32;
+  const int64_t units = (int64_t)p.batch * p.kv_heads * ((rows + 31) / 32);
+  const bool wide = plan.dtype == FUSEDCONV_F32;
+  // One wave a row group and the keys split inside the block: always for up to
+  // 32 rows (a wave's columns), and for small float32 calls, whose tiles take
+  // long: 8 heads of 64, 256 queries: 13 us, whole blocks 24; 512: 18 and 21
+  // (split over blocks); but 1024: 42 and 32, and 16 x 128 queries, 512 row
+  // groups: 22 and 15.
+  plan.few = rows <= 32 || (wide && plan.dp <= 64 && units <= 256 && p.sk <= 512);
   plan.splits = 1;
   plan.forward_bytes = 0;
+  int64_t splits = 1, most;  // most: splits that still have enough keys each
   if (plan.few) {
-    // Blocks for every compute unit, of 256 keys (two tiles a wave) at least.
-    const int64_t units = (int64_t)p.batch * p.kv_heads;
-    int64_t splits = units > 0 ? (512 + units - 1) / units : 1;
-    const int64_t most = p.sk / 256;
-    splits = splits > most ? most : splits;
-    plan.splits = splits < 1 ? 1 : (int)splits;
-    if (plan.splits > 1) plan.forward_bytes = split_bytes(p, plan.splits);
+    // 512 blocks, two tiles a wave at least
+    if (units > 0) splits = (512 + units - 1) / units;
+    most = p.sk / 256;
+  } else {
+    // Where at most half the compute units had a block.  The partial results'
+    // way through memory costs about ten 16-bit tiles (128 blocks of 16 tiles,
+    // heads of 128: 19 us whole, 25 in two; of 64 tiles: 55 us whole, 40 in
+    // four), three float32 ones (4 x 512 queries, 8 heads of 64: 43 and 33 us).
+    const int64_t blocks = (int64_t)p.batch * p.heads * ((p.sq + 127) / 128);
+    if (blocks > 0 && blocks <= 128) splits = ((wide ? 256 : 512) + blocks - 1) / blocks;
+    most = p.sk / (32 * (wide ? 4 : 16));
+  }
+  splits = splits > most ? most : splits;
+  if (splits > 1) {
+    plan.splits = (int)splits;
+    plan.forward_bytes = (size_t)p.batch * p.heads * splits * p.sq * (p.d + 4) * sizeof(float);
   }
   // -lse and -rowsum(do * o), rows padded to whole tiles
   plan.backward_bytes = (size_t)p.batch * p.heads * ((p.sq + 63) / 64 * 64) * 2 * sizeof(float);
@@ -434,11 +490,13 @@ int launch_attention_forward(const AttnParams& p, const AttnPlan& plan, const At
   k.c = fmaxf(fabsf(p.scale) * kLog2e, kLeastC);
   k.tiles = (p.sq + 127) / 128;
   k.splits = plan.splits;
-  k.rows = p.sq * p.group;
+  k.unit_heads = plan.few ? p.kv_heads : p.heads;
+  k.unit_group = plan.few ? p.group : 1;
+  k.rows = p.sq * k.unit_group;
   k.row_groups = (k.rows + 31) / 32;
   if (plan.splits > 1) {
     k.part_o = (float*)a.ws;
-    k.part_lse = k.part_o + (size_t)p.batch * p.kv_heads * plan.splits * k.rows * p.d;
+    k.part_lse = k.part_o + (size_t)p.batch * p.heads * plan.splits * p.sq * p.d;
   }
   const hipStream_t st = (hipStream_t)a.stream;
   switch (plan.dp) {

@@ -214,6 +214,11 @@ ATTENTIONS = [  # b, sq, sk, h, hk, d, window, lengths
     (2, 50, 50, 1, 1, 16, (-1, -1), ([-3, 1000], [1000, 7])),   # taken into range
     (1, 33, 0, 2, 2, 64, (-1, -1), None), (1, 140, 63, 9, 3, 24, (-1, -1), None),
 ]
+SPLIT = [  # few blocks and many keys: the keys are split over blocks in tiles
+    (1, 200, 1500, 2, 1, 64, (-1, 0), None), (1, 129, 1100, 1, 1, 128, (300, 0), None),
+    (2, 100, 1300, 3, 3, 72, (-1, -1), ([100, 40], [1300, 5])), (1, 1300, 1300, 1, 1, 40, (-1, 0), None),
+    (1, 33, 4200, 1, 1, 32, (-1, -1), None),
+]
 FEW = [
     (3, 1, 1000, 8, 2, 128, (-1, 0), ([1, 1, 1], [1000, 1, 0])), (1, 1, 33, 1, 1, 64, (-1, -1), None),
     (2, 1, 5000, 32, 1, 64, (-1, 0), ([1, 1], [4999, 31])), (2, 4, 700, 16, 2, 96, (-1, 0), ([4, 2], [700, 3])),
@@ -223,7 +228,7 @@ FEW = [
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("b,sq,sk,h,hk,d,window,lengths", ATTENTIONS + FEW)
+@pytest.mark.parametrize("b,sq,sk,h,hk,d,window,lengths", ATTENTIONS + SPLIT + FEW)
 def test_attention(b, sq, sk, h, hk, d, window, lengths, dtype):
     log(f"CASE attention {dtype} {(b, sq, sk, h, hk, d, window, lengths)}")
     q, k, v, ql, kl = attention_case(b, sq, sk, h, hk, d, dtype, 50, lengths)
@@ -236,7 +241,7 @@ def test_attention(b, sq, sk, h, hk, d, window, lengths, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("b,sq,sk,h,hk,d,window,lengths", ATTENTIONS + FEW)
+@pytest.mark.parametrize("b,sq,sk,h,hk,d,window,lengths", ATTENTIONS + SPLIT + FEW)
 def test_attention_backward(b, sq, sk, h, hk, d, window, lengths, dtype):
     log(f"CASE attention_backward {dtype} {(b, sq, sk, h, hk, d, window, lengths)}")
     q, k, v, ql, kl = attention_case(b, sq, sk, h, hk, d, dtype, 60, lengths)
