@@ -259,6 +259,34 @@ struct Tile {
   }
 };
 
+// Store C, transposed, as the values 0 .. 31 of a lane's row (its column of C):
+// out[8g + 4h + j] = f(c[4g + j]) for the pieces with 8g < d.  16-bit: the halves
+// of the wave, which hold four of every eight values each, trade quads, so that
+// a lane stores 16 bytes and a row's 32 are written together.
+template <typename T, typename F>
+__device__ __forceinline__ void store_row(T* row, const f32x16& c, int d, int h, F&& f) {
+#pragma unroll
+  for (int g = 0; g < 4; g += 2) {
+    Piece<T, 4> a, b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a.v[j] = to_type<T>(f(c[4 * g + j]));
+      b.v[j] = to_type<T>(f(c[4 * g + 4 + j]));
+    }
+    if constexpr (sizeof(T) == 2) {
+      typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+      typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+      const u2 x = __builtin_bit_cast(u2, a), y = __builtin_bit_cast(u2, b);
+      const auto lo = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
+      const auto hi = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
+      if (8 * (g + h) < d) *reinterpret_cast<u4*>(row + 8 * (g + h)) = u4{lo[0], hi[0], lo[1], hi[1]};
+    } else {
+      if (8 * g < d) store_piece<T, 4>(row + 8 * g + 4 * h, a);
+      if (8 * g + 8 < d) store_piece<T, 4>(row + 8 * g + 8 + 4 * h, b);
+    }
+  }
+}
+
 // Waits until this wave's copies are in LDS, then for the block: after it all
 // waves' copies can be read, and what was read before can be overwritten.
 __device__ __forceinline__ void tile_barrier() {
@@ -297,13 +325,16 @@ __device__ __forceinline__ frag_t<T> to_frag(const f32x16& c, int step) {
 // copy one, waves 2 and 3 the other) through two buffers: while a tile is used
 // the next one is on its way.  start(tile, buffer) starts a tile's copies,
 // use(tile, buffer) works on it; the buffer is a constant, part of the
-// addresses.  A third buffer and a wait that leaves the newest copies in flight
+// addresses.  operands() loads what stays in registers, behind the first tile's
+// copies.  A third buffer and a wait that leaves the newest copies in flight
 // was slower: 1091 against 1062 us for the forward pass of 2 x 8192 causal
 // queries, 32 / 8 heads of 128, bf16, and 308 against 300 us for the backward
 // pass of 32 x 577 queries, 16 heads of 72, f16.
-template <typename Start, typename Use>
-__device__ __forceinline__ void walk_tiles(int count, Start&& start, Use&& use) {
+template <typename Start, typename Operands, typename Use>
+__device__ __forceinline__ void walk_tiles(int count, Start&& start, Operands&& operands,
+                                           Use&& use) {
   start(0, int_c<0>{});
+  operands();
   auto step = [&](int tile, auto N) {
     tile_barrier();
     if (tile + 1 < count) start(tile + 1, int_c<N ^ 1>{});

@@ -155,9 +155,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
     const int64_t stride = second ? p.v.s : p.k.s;
     copy.init(stride, p.d, wave & 1);
     frag_t<T> q[NS];
-    const int qi = min(i, see.nq - 1);
-    load_operand<T, DP>(q, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d,
-                        p.scale < 0.f);
+    auto operands = [&] {
+      const int qi = min(i, see.nq - 1);
+      load_operand<T, DP>(q, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d,
+                          p.scale < 0.f);
+    };
     lds_barrier();  // the padding is clear
     auto start = [&](int tile, auto N) {
       const int key0 = first + 32 * tile;
@@ -180,39 +182,24 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
           st.o[t] = mma(L::load_columns(vt, 16 * d, t), pf, st.o[t]);
       }
     };
-    walk_tiles((end - first + 31) / 32, start, use);
+    walk_tiles((end - first + 31) / 32, start, operands, use);
   }
-  if (i >= p.sq) return;
   const float l = half_sum(st.l);
   const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;  // no key seen: zeros
+  if (i >= p.sq) return;  // both lanes of a row or neither: they trade values below
   if (a.splits > 1) {
     const int64_t part = ((int64_t)(b * p.heads + head) * a.splits + split) * p.sq + i;
-    float* o = a.part_o + part * p.d;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (32 * t + 8 * g >= p.d) continue;
-        Piece<float, 4> po;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) po.v[j] = st.o[t][4 * g + j] * inv;
-        store_piece<float, 4>(o + 32 * t + 8 * g + 4 * h, po);
-      }
+      store_row<float>(a.part_o + part * p.d + 32 * t, st.o[t], p.d - 32 * t, h,
+                       [&](float v) { return v * inv; });
     if (h == 0) a.part_lse[part] = l == 0.f ? -INFINITY : st.m * a.c + log2f(l);
     return;
   }
   T* o = (T*)a.o + b * p.o.b + i * p.o.s + head * p.o.h;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int d = 32 * t + 8 * g + 4 * h;
-      if (32 * t + 8 * g >= p.d) continue;
-      Piece<T, 4> po;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) po.v[j] = to_type<T>(st.o[t][4 * g + j] * inv);
-      store_piece<T, 4>(o + d, po);
-    }
+    store_row<T>(o + 32 * t, st.o[t], p.d - 32 * t, h, [&](float v) { return v * inv; });
   if (a.lse && h == 0)
     a.lse[((int64_t)b * p.heads + head) * p.sq + i] =
         l == 0.f ? -INFINITY : st.m * a.c * kLn2 + logf(l);
@@ -386,15 +373,17 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnK a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] *= keep;
     m = next;
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float f = __shfl(w, s, 32);
-      if (live && f != 0.f) {
-        const Piece<float, 4> x = load_piece<float, 4>(po + (int64_t)(s0 + s) * a.rows * p.d + lane * 4);
+    for (int s = 0; s < n; s += 4)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] += f * x.v[e];
+      for (int u = 0; u < 4; ++u) {
+        const float f = __shfl(w, s + u, 32);  // zero from n on
+        if (live && f != 0.f) {
+          const Piece<float, 4> x =
+              load_piece<float, 4>(po + (int64_t)(s0 + s + u) * a.rows * p.d + lane * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += f * x.v[e];
+        }
       }
-    }
   }
   const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
   if (live) {

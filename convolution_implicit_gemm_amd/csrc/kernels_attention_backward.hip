@@ -123,10 +123,12 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
   L::template clear_padding<128 + (B::kVInLds ? 128 : 0)>(tiles, p.d, threadIdx.x, 256);
   if (first < end) {
     frag_t<T> kf[NS], vf[B::kVInLds ? 1 : NS];
-    const int ji = min(j, see.nk - 1);
-    load_operand<T, DP>(kf, (const T*)a.k + b * p.k.b + ji * p.k.s + kvh * p.k.h, p.d, p.scale < 0.f);
     const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
-    if constexpr (!B::kVInLds) load_operand<T, DP>(vf, vp + ji * p.v.s, p.d, false);
+    auto operands = [&] {
+      const int ji = min(j, see.nk - 1);
+      load_operand<T, DP>(kf, (const T*)a.k + b * p.k.b + ji * p.k.s + kvh * p.k.h, p.d, p.scale < 0.f);
+      if constexpr (!B::kVInLds) load_operand<T, DP>(vf, vp + ji * p.v.s, p.d, false);
+    };
 
     // waves 0 and 1 copy Q and nlse, waves 2 and 3 dO and ndelta
     typename L::template Copier<32, 2> copy;
@@ -190,26 +192,18 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
         }
       }
     };
-    walk_tiles(items * p.group, start, use);
+    walk_tiles(items * p.group, start, operands, use);
   }
   if (j >= p.sk) return;
-  const float keep = j < see.nk ? 1.f : 0.f;
+  const bool keep = j < see.nk;
   T* dkp = (T*)a.dk + b * p.dk.b + j * p.dk.s + kvh * p.dk.h;
   T* dvp = (T*)a.dv + b * p.dv.b + j * p.dv.s + kvh * p.dv.h;
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      if (32 * t + 8 * g >= p.d) continue;
-      Piece<T, 4> pk, pv;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        pk.v[e] = to_type<T>(keep != 0.f ? dk[t][4 * g + e] * p.scale : 0.f);
-        pv.v[e] = to_type<T>(keep != 0.f ? dv[t][4 * g + e] : 0.f);
-      }
-      store_piece<T, 4>(dkp + 32 * t + 8 * g + 4 * h, pk);
-      store_piece<T, 4>(dvp + 32 * t + 8 * g + 4 * h, pv);
-    }
+  for (int t = 0; t < NT; ++t) {
+    store_row<T>(dkp + 32 * t, dk[t], p.d - 32 * t, h,
+                 [&](float v) { return keep ? v * p.scale : 0.f; });
+    store_row<T>(dvp + 32 * t, dv[t], p.d - 32 * t, h, [&](float v) { return keep ? v : 0.f; });
+  }
 }
 
 // ---------------------------------------------------------------------- dq
@@ -257,12 +251,15 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
     const int64_t stride = second ? p.v.s : p.k.s;
     copy.init(stride, p.d, wave & 1);
     frag_t<T> qf[NS], of[NS];
-    const int qi = min(i, see.nq - 1);
-    load_operand<T, DP>(qf, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d, p.scale < 0.f);
-    load_operand<T, DP>(of, (const T*)a.dout + b * p.dout.b + qi * p.dout.s + head * p.dout.h, p.d, false);
-    const int64_t at = ((int64_t)b * p.heads + head) * a.padded;
-    const float nlse = i < a.padded ? a.nlse[at + i] : -INFINITY;
-    const float ndelta = i < a.padded ? a.ndelta[at + i] : 0.f;
+    float nlse, ndelta;
+    auto operands = [&] {
+      const int qi = min(i, see.nq - 1);
+      load_operand<T, DP>(qf, (const T*)a.q + b * p.q.b + qi * p.q.s + head * p.q.h, p.d, p.scale < 0.f);
+      load_operand<T, DP>(of, (const T*)a.dout + b * p.dout.b + qi * p.dout.s + head * p.dout.h, p.d, false);
+      const int64_t at = ((int64_t)b * p.heads + head) * a.padded;
+      nlse = i < a.padded ? a.nlse[at + i] : -INFINITY;
+      ndelta = i < a.padded ? a.ndelta[at + i] : 0.f;
+    };
     lds_barrier();  // the padding is clear
     auto start = [&](int tile, auto N) {
       const int key0 = first + 32 * tile;
@@ -293,20 +290,14 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
         for (int t = 0; t < NT; ++t) dq[t] = mma(L::load_columns(kt, 16 * d, t), df, dq[t]);
       }
     };
-    walk_tiles((end - first + 31) / 32, start, use);
+    walk_tiles((end - first + 31) / 32, start, operands, use);
   }
   if (i >= p.sq) return;
   T* out = (T*)a.dq + b * p.dq.b + i * p.dq.s + head * p.dq.h;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      if (32 * t + 8 * g >= p.d) continue;
-      Piece<T, 4> po;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) po.v[e] = to_type<T>(i < see.nq ? dq[t][4 * g + e] * p.scale : 0.f);
-      store_piece<T, 4>(out + 32 * t + 8 * g + 4 * h, po);
-    }
+    store_row<T>(out + 32 * t, dq[t], p.d - 32 * t, h,
+                 [&](float v) { return i < see.nq ? v * p.scale : 0.f; });
 }
 
 // Both kinds of blocks in one launch, those of the keys first: where a causal

@@ -84,6 +84,25 @@ bool strides_ok(const int64_t s[3], int64_t batch, int64_t len, int64_t heads, i
   return len <= 1 || s[1] * esize <= (int64_t(1) << 31) / 256 - 1;
 }
 
+// No two elements of an output at one place: ordered by stride, each axis steps
+// over all that the axes inside it reach.
+bool apart(const int64_t s[3], int64_t batch, int64_t len, int64_t heads, int64_t d) {
+  const int64_t size[3] = {batch, len, heads};
+  if (batch == 0 || len == 0 || heads == 0) return true;
+  bool done[3] = {false, false, false};
+  int64_t reach = d;
+  for (int step = 0; step < 3; ++step) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!done[i] && size[i] > 1 && (at < 0 || s[i] < s[at])) at = i;
+    if (at < 0) break;
+    done[at] = true;
+    if (s[at] < reach) return false;
+    reach += s[at] * (size[at] - 1);
+  }
+  return true;
+}
+
 fc::Strides3 strides_of(const int64_t s[3], int64_t batch, int64_t len, int64_t heads) {
   return {batch > 1 ? s[0] : 0, len > 1 ? s[1] : 0, heads > 1 ? s[2] : 0};
 }
@@ -204,6 +223,9 @@ int fusedconv_rotary_create(const fusedconv_rotary_desc* d, fusedconv_rotary** o
       (d->kv_heads && (!strides_ok(d->k_strides, d->batch, d->len, d->kv_heads, es) ||
                        !strides_ok(d->k_out_strides, d->batch, d->len, d->kv_heads, es))))
     return fail(FUSEDCONV_ERR_ALIGNMENT, "strides must be non-negative, whole 16-byte pieces and within the index limits");
+  if (!apart(d->q_out_strides, d->batch, d->len, d->heads, d->head_dim) ||
+      (d->kv_heads && !apart(d->k_out_strides, d->batch, d->len, d->kv_heads, d->head_dim)))
+    return fail(FUSEDCONV_ERR_ATTR_VALUE, "an output's strides make its elements overlap");
   fusedconv_rotary* h = new (std::nothrow) fusedconv_rotary();
   if (!h) return fail(FUSEDCONV_ERR_ALLOC, "out of host memory");
   h->p.d = *d;
@@ -262,6 +284,11 @@ int fusedconv_attention_create(const fusedconv_attention_desc* d, fusedconv_atte
   for (const int64_t* s : ks)
     if (!strides_ok(s, d->batch, d->k_len, d->kv_heads, es))
       return fail(FUSEDCONV_ERR_ALIGNMENT, "strides must be non-negative, whole 16-byte pieces and within the index limits");
+  if (!apart(d->o_strides, d->batch, d->q_len, d->heads, d->head_dim) ||
+      !apart(d->dq_strides, d->batch, d->q_len, d->heads, d->head_dim) ||
+      !apart(d->dk_strides, d->batch, d->k_len, d->kv_heads, d->head_dim) ||
+      !apart(d->dv_strides, d->batch, d->k_len, d->kv_heads, d->head_dim))
+    return fail(FUSEDCONV_ERR_ATTR_VALUE, "an output's strides make its elements overlap");
   fusedconv_attention* h = new (std::nothrow) fusedconv_attention();
   if (!h) return fail(FUSEDCONV_ERR_ALLOC, "out of host memory");
   const auto limit = [](int64_t w) { return (int32_t)(w > kMaxLen ? -1 : w); };

@@ -332,6 +332,7 @@ def layer_norm(x, weight=None, bias=None, *, axis=-1, eps=1e-5, stats=False, out
     be a view whose rows (images) lie at one stride."""
     if torch is None:
         _setup()
+    eps = float(eps)
     key = ("layer_norm", _meta(x), _meta(weight), _meta(bias), axis, eps, _meta(out))
     op, stat_shape = _calls.get(key) or _remember(
         key, _plan_layer_norm(x, weight, bias, axis, eps, out))
@@ -493,6 +494,12 @@ class Attention(_Plan):
             0 if ws is None else ws.numel(), stream))
 
 
+def _limits(scale, window):
+    """scale and window as plain numbers: they are part of what a call is remembered by."""
+    return (None if scale is None else float(scale),
+            None if window is None else tuple(int(n) for n in window))
+
+
 def _attention_sizes(q, k, v, scale, causal, window, q_lengths, k_lengths):
     """Shapes, limits and strides of a call, checked: the first arguments of Attention."""
     code = _code(q)
@@ -509,7 +516,7 @@ def _attention_sizes(q, k, v, scale, causal, window, q_lengths, k_lengths):
     if window is None:
         left, right = -1, -1
     else:
-        left, right = (int(n) for n in window)
+        left, right = window
     if causal:
         if right > 0:
             raise ValueError("causal=True and a window to the right contradict each other")
@@ -548,8 +555,7 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, q_lengths=None,
     key gets zeros and -inf."""
     if torch is None:
         _setup()
-    if window is not None:
-        window = tuple(window)
+    scale, window = _limits(scale, window)
     key = ("attention", _meta(q), _meta(k), _meta(v), scale, causal, window, _meta(q_lengths),
            _meta(k_lengths), _meta(out))
     op, shape, lse_shape = _calls.get(key) or _remember(
@@ -588,8 +594,7 @@ def attention_backward(do, q, k, v, o, lse, *, scale=None, causal=False, window=
     write (views of one packed gradient, say)."""
     if torch is None:
         _setup()
-    if window is not None:
-        window = tuple(window)
+    scale, window = _limits(scale, window)
     if out is not None:
         out = tuple(out)
     key = ("attention_backward", _meta(do), _meta(q), _meta(k), _meta(v), _meta(o), _meta(lse),

@@ -78,8 +78,9 @@ void fusedconv_layer_norm_destroy(fusedconv_layer_norm* h);
  * negative angle: the gradient of the forward call, and its undoing.  Angles
  * are reduced to a fraction of a turn in 64 bits, so far positions keep their
  * accuracy.  Q is [batch][len][heads][head_dim], K the same with kv_heads (0:
- * no K); strides in elements {batch, len, head}, the last axis contiguous.
- * An output may be its own input (same pointer and strides).
+ * no K); strides in elements {batch, len, head}, the last axis contiguous (0
+ * repeats an input; an output's elements must not overlap).  An output may be
+ * its own input (same pointer and strides).
  */
 typedef struct fusedconv_rotary_desc {
   int32_t dtype;
@@ -133,6 +134,9 @@ void fusedconv_rotary_destroy(fusedconv_rotary* h);
  *
  * head_dim: a multiple of 8, at most 128.  Strides in elements {batch,
  * position, head}; each a multiple of 16 bytes; the last axis is contiguous.
+ * A stride of 0 repeats an input; an output's elements must not overlap, and
+ * outputs overlap no input.  O and its gradient may lie differently: the
+ * backward pass takes O at o_strides and do at do_strides.
  */
 typedef struct fusedconv_attention_desc {
   int32_t dtype;

@@ -90,6 +90,27 @@ def test_attention_stride_refusals(which, bad):
     refused(-15, lambda: fc.Attention(*ATT.values(), *strides))
 
 
+@pytest.mark.parametrize("which,bad", [(3, (1280, 0, 64)), (3, (640, 256, 64)), (5, (1280, 256, 32)), (6, (0, 128, 64)),
+                                       (7, (128, 896, 56))])
+def test_overlapping_outputs(which, bad):
+    strides = list(STRIDES)
+    strides[which] = bad
+    refused(-5, lambda: fc.Attention(*ATT.values(), *strides))
+    if which == 3:
+        refused(-5, lambda: fc.Rotary(**dict(ROT, qos=bad)))
+
+
+def test_output_layouts_that_are_apart():
+    """Packed projections, heads before positions, an unused axis with any stride."""
+    for qs, ks in (((3840, 768, 64), (5376, 768, 64)), ((1280, 64, 320), (896, 64, 448))):
+        fc.Attention(*ATT.values(), qs, ks, ks, qs, qs, qs, ks, ks)
+    fc.Attention(*dict(ATT, batch=1).values(), *[(0,) + s[1:] for s in STRIDES])
+    for n in (0, 1, 2):  # inputs may repeat
+        strides = list(STRIDES)
+        strides[n] = (0, 128, 64)
+        fc.Attention(*ATT.values(), *strides)
+
+
 def test_null_and_workspace_refusals():
     """Pointers are checked before the device is looked at."""
     lib = T._load()
