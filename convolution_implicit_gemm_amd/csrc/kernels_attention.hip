@@ -30,7 +30,7 @@ struct AttnK {
   float *part_o, *part_lse;
   float c;                   // |scale| * log2(e), at least kLeastC
   int32_t tiles;             // row tiles of one head (tile form)
-  int32_t splits, rows, row_groups;
+  int32_t splits, rows, row_groups, few_stages, join_groups;
   int32_t unit_heads, unit_group;  // heads that units count, and query heads of a unit
 };
 
@@ -206,26 +206,29 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
 }
 
 // ------------------------------------------------------------- few queries
-// Up to 32 rows (queries x the heads that share a key head) fill one wave's
-// columns.  The keys an entry really has are split evenly over `splits` blocks
-// and there over the WAVES waves, tile by tile; each wave brings its own tiles
-// of 32 keys to its own LDS, two ahead of none but its own waits, so that no
-// barrier stops the stream from HBM, which bounds this form.  The waves meet in
-// LDS, the blocks in k_attention_join.
+// 32 rows (queries x the heads that share a key head) fill one wave's columns.
+// The keys an entry really has are split evenly over `splits` blocks and there
+// over the waves, tile by tile; each wave brings its own tiles of 32 keys to its
+// own LDS (one buffer, or two where it has more than one tile) and waits for
+// them alone, so that no barrier stops the stream from HBM, which bounds this
+// form.  The waves meet in LDS, the blocks in k_attention_join.
 template <typename T, int DP>
 struct Few {
-  static constexpr int kWaves = sizeof(T) * DP > 256 ? 2 : 4;
-  static constexpr int kTile = 32 * DP;               // values of a tile of 32 keys
-  static constexpr int kStream = kWaves * 4 * kTile * (int)sizeof(T);
-  static constexpr int kMerge = kWaves * (32 * (DP + 1) + 64) * 4;
-  static constexpr int kLds = kStream > kMerge ? kStream : kMerge;
+  static constexpr int kTile = 32 * DP;  // values of a tile of 32 keys
+  static constexpr int kRow = DP + 4;    // floats of a row where the waves meet
+  static constexpr int lds(int waves, int stages) {
+    const int stream = waves * stages * 2 * kTile * (int)sizeof(T);
+    const int merge = waves * (32 * kRow + 64) * 4;
+    return stream > merge ? stream : merge;
+  }
 };
 
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
   using L = Tile<T, DP>;
   using F = Few<T, DP>;
-  constexpr int NT = DP / 32, NS = DP / 16, W = F::kWaves;
+  constexpr int NT = DP / 32, NS = DP / 16;
+  const int W = blockDim.x >> 6;
   extern __shared__ __attribute__((aligned(16))) char lds[];
 
   const AttnParams& p = a.p;
@@ -251,7 +254,7 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
 
   const T* kp = (const T*)a.k + b * p.k.b + kvh * p.k.h;
   const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
-  T* mine = (T*)lds + wave * 4 * F::kTile;
+  T* mine = (T*)lds + wave * a.few_stages * 2 * F::kTile;
   typename L::template Copier<32, 1> ck, cv;
   ck.init(p.k.s, p.d, 0);
   cv.init(p.v.s, p.d, 0);
@@ -264,7 +267,8 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
 
   Running<NT> st;
   st.start();
-  L::template clear_padding<4 * 32>(mine, p.d, lane, 64);
+  L::template clear_padding<2 * 32>(mine, p.d, lane, 64);
+  if (a.few_stages > 1) L::template clear_padding<2 * 32>(mine + 2 * F::kTile, p.d, lane, 64);
   int tile = t0 + wave;
   if (tile < t1) {
     frag_t<T> q[NS];
@@ -300,69 +304,83 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
     }
   }
 
-  // The waves' states, side by side in LDS: [wave][row][DP + 1] outputs, then
-  // [wave][2][32] of (m * c, l).  The odd row length keeps the columns apart.
+  // The waves' states, side by side in LDS: [wave][row][DP + 4] outputs (the rows
+  // four banks apart), then [wave][2][32] of (m * c, l).  Then 32 lanes a row,
+  // four values each.
   const float l = half_sum(st.l);
   __syncthreads();
-  float* so = (float*)lds + wave * 32 * (DP + 1);
-  float* sm = (float*)lds + W * 32 * (DP + 1);
+  float* so = (float*)lds;
+  float* sm = so + W * 32 * F::kRow;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) so[(lane & 31) * (DP + 1) + 32 * t + c_row(j, h)] = st.o[t][j];
+    for (int g = 0; g < 4; ++g) {
+      Piece<float, 4> x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x.v[j] = st.o[t][4 * g + j];
+      store_piece<float, 4>(so + (wave * 32 + (lane & 31)) * F::kRow + 32 * t + 8 * g + 4 * h, x);
+    }
   if (h == 0) {
     sm[wave * 64 + lane] = st.m == -INFINITY ? -INFINITY : st.m * a.c;
     sm[wave * 64 + 32 + lane] = l;
   }
   __syncthreads();
-  for (int at = threadIdx.x; at < rows * p.d; at += W * 64) {
-    const int row = at / p.d, d = at - row * p.d;
+  const int d0 = (threadIdx.x & 31) * 4;
+  for (int row = threadIdx.x >> 5; row < rows; row += 2 * W) {
     float m = -INFINITY;
-#pragma unroll
     for (int w = 0; w < W; ++w) m = fmaxf(m, sm[w * 64 + row]);
-    float sum = 0.f, acc = 0.f;
-#pragma unroll
+    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int w = 0; w < W; ++w) {
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[w * 64 + row] - m);
       sum += f * sm[w * 64 + 32 + row];
-      acc += f * ((const float*)lds)[(w * 32 + row) * (DP + 1) + d];
+      if (d0 < DP) {
+        const Piece<float, 4> x = load_piece<float, 4>(so + (w * 32 + row) * F::kRow + d0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += f * x.v[e];
+      }
     }
-    const float out = sum > 0.f || sum != sum ? acc / sum : 0.f;
+    const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
     const float lse2 = sum == 0.f ? -INFINITY : m + log2f(sum);
     const int rr = group * 32 + row, ri = rr / p.group, rh = kvh * p.group + rr % p.group;
     if (a.splits > 1) {
       const int64_t part = ((int64_t)(b * p.kv_heads + kvh) * a.splits + split) * a.rows + rr;
-      a.part_o[part * p.d + d] = out;
-      if (d == 0) a.part_lse[part] = lse2;
+      if (d0 < p.d)
+        store_piece<float, 4>(a.part_o + part * p.d + d0,
+                              Piece<float, 4>{acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv});
+      if (d0 == 0) a.part_lse[part] = lse2;
     } else {
-      ((T*)a.o)[b * p.o.b + ri * p.o.s + rh * p.o.h + d] = to_type<T>(out);
-      if (d == 0 && a.lse)
-        a.lse[((int64_t)b * p.heads + rh) * p.sq + ri] = lse2 * kLn2;
+      Piece<T, 4> out;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out.v[e] = to_type<T>(acc[e] * inv);
+      if (d0 < p.d) store_piece<T, 4>((T*)a.o + b * p.o.b + ri * p.o.s + rh * p.o.h + d0, out);
+      if (d0 == 0 && a.lse) a.lse[((int64_t)b * p.heads + rh) * p.sq + ri] = lse2 * kLn2;
     }
   }
 }
 
-// Joins the splits of a row: 32 lanes a row, four values each, 8 rows a block.
-// The weights 2^(lse - max) / sum are worked out by one lane a split, 32 at a
-// time (against a running maximum), so a row waits for memory twice and not
-// twice per split.
+// Joins the splits of a row.  32 lanes, four values each, take every
+// join_groups-th split of a row (8 groups a block): 8 of them share a row where
+// there are more than 8 splits.  A split's weight 2^(lse - max) is worked out by
+// one lane, 32 splits at a time, so that a group waits for memory twice, and not
+// twice a split.
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_join(AttnK a) {
+  __shared__ float meet[8][6][32];
   const AttnParams& p = a.p;
-  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (at >= (int64_t)p.batch * a.unit_heads * a.rows) return;
+  const int G = a.join_groups, group = threadIdx.x >> 5, mine = group % G;
+  const int64_t all = (int64_t)p.batch * a.unit_heads * a.rows;
+  const int64_t at = (int64_t)blockIdx.x * (8 / G) + group / G;
+  const bool real = at < all;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = at / a.rows;
-  const int r = (int)(at - unit * a.rows);
-  const int b = (int)(unit / a.unit_heads), uh = (int)(unit % a.unit_heads);
-  const int i = r / a.unit_group, head = uh * a.unit_group + r % a.unit_group;
+  const int64_t unit = real ? at / a.rows : 0;
+  const int r = real ? (int)(at - unit * a.rows) : 0;
   const float* lse = a.part_lse + unit * a.splits * a.rows + r;
-  const float* po = a.part_o + (unit * a.splits * a.rows + r) * p.d;
   const bool live = lane * 4 < p.d;
+  const float* po = a.part_o + (unit * a.splits * a.rows + r) * p.d + (live ? lane * 4 : 0);
   float m = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = 0; s0 < a.splits; s0 += 32) {
-    const int n = min(32, a.splits - s0);
-    const float l = lane < n ? lse[(int64_t)(s0 + lane) * a.rows] : -INFINITY;
+  for (int s0 = mine; s0 < a.splits; s0 += 32 * G) {
+    const int split = s0 + lane * G;
+    const float l = split < a.splits ? lse[(int64_t)split * a.rows] : -INFINITY;
     float top = l;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor(top, off, 32));
@@ -373,18 +391,45 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnK a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] *= keep;
     m = next;
-    for (int s = 0; s < n; s += 4)
+    const int n = min(32, (a.splits - s0 + G - 1) / G);
+    for (int s = 0; s < n; s += 4) {
+      Piece<float, 4> x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)  // past the end: the last one again, with the weight zero
+        x[u] = load_piece<float, 4>(po + (int64_t)min(s0 + (s + u) * G, a.splits - 1) * a.rows * p.d);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float f = __shfl(w, s + u, 32);  // zero from n on
-        if (live && f != 0.f) {
-          const Piece<float, 4> x =
-              load_piece<float, 4>(po + (int64_t)(s0 + s + u) * a.rows * p.d + lane * 4);
+        const float f = __shfl(w, s + u, 32);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] += f * x.v[e];
-        }
+        for (int e = 0; e < 4; ++e) acc[e] += f * x[u].v[e];
       }
+    }
   }
+  if (G > 1) {
+    meet[group][4][lane] = m;
+    meet[group][5][lane] = sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) meet[group][e][lane] = acc[e];
+    __syncthreads();
+    if (mine) return;
+    float all_m = m;
+    for (int g = 1; g < G; ++g) all_m = fmaxf(all_m, meet[group + g][4][lane]);
+    const float own = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - all_m);
+    sum *= own;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= own;
+    for (int g = 1; g < G; ++g) {
+      const float gm = meet[group + g][4][lane];
+      const float f = gm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(gm - all_m);
+      sum += f * meet[group + g][5][lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] += f * meet[group + g][e][lane];
+    }
+    m = all_m;
+  }
+  if (!real) return;
+  const int b = (int)(unit / a.unit_heads), uh = (int)(unit % a.unit_heads);
+  const int i = r / a.unit_group, head = uh * a.unit_group + r % a.unit_group;
   const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
   if (live) {
     Piece<T, 4> out;
@@ -407,11 +452,11 @@ int FC_DP_NAME(attention_forward_)(const AttnPlan& plan, const AttnK& k, hipStre
     const AttnParams& p = k.p;
     if (plan.few) {
       auto fn = k_attention_few<T, FC_DP>;
-      constexpr int bytes = Few<T, FC_DP>::kLds;
+      const int bytes = Few<T, FC_DP>::lds(plan.few_waves, plan.few_stages);
       rc = set_max_dynamic_lds((const void*)fn, bytes);
       if (rc != FUSEDCONV_OK) return;
       hipLaunchKernelGGL(fn, dim3((unsigned)(p.batch * p.kv_heads * k.row_groups * k.splits)),
-                         dim3(64 * Few<T, FC_DP>::kWaves), bytes, st, k);
+                         dim3(64 * plan.few_waves), bytes, st, k);
     } else {
       auto fn = k_attention<T, FC_DP>;
       constexpr int bytes = Many<T, FC_DP>::kLds;
@@ -420,10 +465,12 @@ int FC_DP_NAME(attention_forward_)(const AttnPlan& plan, const AttnK& k, hipStre
       hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.heads * k.tiles * k.splits)),
                          dim3(256), bytes, st, k);
     }
-    if (k.splits > 1)
-      hipLaunchKernelGGL((k_attention_join<T>),
-                         dim3((unsigned)(((int64_t)p.batch * k.unit_heads * k.rows + 7) / 8)),
+    if (k.splits > 1) {
+      const int64_t per_block = 8 / k.join_groups;
+      const int64_t rows = (int64_t)p.batch * k.unit_heads * k.rows;
+      hipLaunchKernelGGL((k_attention_join<T>), dim3((unsigned)((rows + per_block - 1) / per_block)),
                          dim3(256), 0, st, k);
+    }
   });
   if (rc != FUSEDCONV_OK) return rc;
   return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH;
@@ -439,12 +486,14 @@ void plan_attention(const AttnParams& p, AttnPlan& plan) {
   const int64_t rows = (int64_t)p.sq * p.group;
   const int64_t units = (int64_t)p.batch * p.kv_heads * ((rows + 31) / 32);
   const bool wide = plan.dtype == FUSEDCONV_F32;
-  // One wave a row group and the keys split inside the block: always for up to
-  // 32 rows (a wave's columns), and for small float32 calls, whose tiles take
+  // One wave a row group and the keys split inside the block: for up to 32 rows
+  // (a wave's columns) or up to 16 queries, which the other form would leave
+  // alone in a tile of 128 (2 x 5 queries on 30000 keys, 8 heads on one of 128:
+  // FEWT us, there 35); and for small float32 calls, whose tiles take
   // long: 8 heads of 64, 256 queries: 13 us, whole blocks 24; 512: 18 and 21
   // (split over blocks); but 1024: 42 and 32, and 16 x 128 queries, 512 row
   // groups: 22 and 15.
-  plan.few = rows <= 32 || (wide && plan.dp <= 64 && units <= 256 && p.sk <= 512);
+  plan.few = rows <= 32 || p.sq <= 16 || (wide && plan.dp <= 64 && units <= 256 && p.sk <= 512);
   plan.splits = 1;
   plan.forward_bytes = 0;
   int64_t splits = 1, most;  // most: splits that still have enough keys each
@@ -462,6 +511,11 @@ void plan_attention(const AttnParams& p, AttnPlan& plan) {
     most = p.sk / (32 * (wide ? 4 : 16));
   }
   splits = splits > most ? most : splits;
+  // four waves where two buffers each fit in LDS, no more than there are tiles
+  const int64_t tiles = (p.sk + 31) / 32, share = splits > 1 ? (tiles + splits - 1) / splits : tiles;
+  const int most_waves = (wide ? 4 : 2) * plan.dp > 256 ? 2 : 4;
+  plan.few_waves = (int)(share < 1 ? 1 : share < most_waves ? share : most_waves);
+  plan.few_stages = share > plan.few_waves ? 2 : 1;
   if (splits > 1) {
     plan.splits = (int)splits;
     plan.forward_bytes = (size_t)p.batch * p.heads * splits * p.sq * (p.d + 4) * sizeof(float);
@@ -483,6 +537,8 @@ int launch_attention_forward(const AttnParams& p, const AttnPlan& plan, const At
   k.unit_group = plan.few ? p.group : 1;
   k.rows = p.sq * k.unit_group;
   k.row_groups = (k.rows + 31) / 32;
+  k.few_stages = plan.few_stages;
+  k.join_groups = plan.splits > 8 ? 8 : 1;
   if (plan.splits > 1) {
     k.part_o = (float*)a.ws;
     k.part_lse = k.part_o + (size_t)p.batch * p.heads * plan.splits * p.sq * p.d;

@@ -53,8 +53,9 @@ struct AttnParams {
 };
 struct AttnPlan {
   int32_t dtype, dp;    // dp: head_dim rounded up to what the kernels tile (32, 64, 96, 128)
-  int32_t few;          // few query rows: the key axis is split over waves and blocks
-  int32_t splits;       // blocks of one (entry, key head, row group) along the keys
+  int32_t few;          // few query rows: the key axis is split over a block's waves too
+  int32_t splits;       // blocks of one (entry, head, row tile) along the keys
+  int32_t few_waves, few_stages;  // few: waves of a block, tile buffers of a wave
   size_t forward_bytes, backward_bytes;
 };
 struct AttnArgs {
