@@ -248,14 +248,13 @@ struct Tile {
     }
   };
 
+  // Set the chunks past d of ROWS rows to zero.
   template <int ROWS>
   static __device__ __forceinline__ void clear_padding(T* tile, int d, int thread, int threads) {
-    if (d == DP) return;
-    for (int at = thread; at < ROWS * NC; at += threads)
-      if (((at % NC) ^ swizzle(at / NC)) * CE >= d) {
-        typedef float f4 __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<f4*>(tile + at * CE) = f4{0.f, 0.f, 0.f, 0.f};
-      }
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    for (int row = thread; row < ROWS; row += threads)
+      for (int chunk = d / CE; chunk < NC; ++chunk)
+        *reinterpret_cast<f4*>(tile + row * DP + (chunk ^ swizzle(row)) * CE) = f4{0.f, 0.f, 0.f, 0.f};
   }
 };
 

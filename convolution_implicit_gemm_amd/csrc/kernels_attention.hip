@@ -30,7 +30,7 @@ struct AttnK {
   float *part_o, *part_lse;
   float c;                   // |scale| * log2(e), at least kLeastC
   int32_t tiles;             // row tiles of one head (tile form)
-  int32_t splits, rows, row_groups, few_stages, join_groups;
+  int32_t splits, rows, row_groups, few_waves, few_stages, join_groups;
   int32_t unit_heads, unit_group;  // heads that units count, and query heads of a unit
 };
 
@@ -214,6 +214,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
 // form.  The waves meet in LDS, the blocks in k_attention_join.
 template <typename T, int DP>
 struct Few {
+  // where two buffers each fit in LDS
+  static constexpr int kMostWaves = sizeof(T) * DP > 256 ? 2 : 4;
   static constexpr int kTile = 32 * DP;  // values of a tile of 32 keys
   static constexpr int kRow = DP + 4;    // floats of a row where the waves meet
   static constexpr int lds(int waves, int stages) {
@@ -228,7 +230,7 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
   using L = Tile<T, DP>;
   using F = Few<T, DP>;
   constexpr int NT = DP / 32, NS = DP / 16;
-  const int W = blockDim.x >> 6;
+  const int W = a.few_waves;
   extern __shared__ __attribute__((aligned(16))) char lds[];
 
   const AttnParams& p = a.p;
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
   }
 
   // The waves' states, side by side in LDS: [wave][row][DP + 4] outputs (the rows
-  // four banks apart), then [wave][2][32] of (m * c, l).  Then 32 lanes a row,
+  // four banks apart), then [wave][2][32] of (m * c, l).  Then a row's lanes take
   // four values each.
   const float l = half_sum(st.l);
   __syncthreads();
@@ -325,20 +327,25 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
     sm[wave * 64 + 32 + lane] = l;
   }
   __syncthreads();
-  const int d0 = (threadIdx.x & 31) * 4;
-  for (int row = threadIdx.x >> 5; row < rows; row += 2 * W) {
+  constexpr int kLanes = DP <= 32 ? 8 : DP <= 64 ? 16 : 32;  // of a row
+  const int d0 = threadIdx.x % kLanes * 4;
+  for (int row = threadIdx.x / kLanes; row < rows; row += W * 64 / kLanes) {
     float m = -INFINITY;
-    for (int w = 0; w < W; ++w) m = fmaxf(m, sm[w * 64 + row]);
-    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int w = 0; w < W; ++w) {
-      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[w * 64 + row] - m);
-      sum += f * sm[w * 64 + 32 + row];
-      if (d0 < DP) {
-        const Piece<float, 4> x = load_piece<float, 4>(so + (w * 32 + row) * F::kRow + d0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] += f * x.v[e];
+    for (int w = 0; w < F::kMostWaves; ++w)
+      if (w < W) m = fmaxf(m, sm[w * 64 + row]);
+    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < F::kMostWaves; ++w)
+      if (w < W) {
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[w * 64 + row] - m);
+        sum += f * sm[w * 64 + 32 + row];
+        if (d0 < DP) {
+          const Piece<float, 4> x = load_piece<float, 4>(so + (w * 32 + row) * F::kRow + d0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += f * x.v[e];
+        }
       }
-    }
     const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
     const float lse2 = sum == 0.f ? -INFINITY : m + log2f(sum);
     const int rr = group * 32 + row, ri = rr / p.group, rh = kvh * p.group + rr % p.group;
@@ -537,6 +544,7 @@ int launch_attention_forward(const AttnParams& p, const AttnPlan& plan, const At
   k.unit_group = plan.few ? p.group : 1;
   k.rows = p.sq * k.unit_group;
   k.row_groups = (k.rows + 31) / 32;
+  k.few_waves = plan.few_waves;
   k.few_stages = plan.few_stages;
   k.join_groups = plan.splits > 8 ? 8 : 1;
   if (plan.splits > 1) {

@@ -26,15 +26,26 @@ struct AttnBwdK {
   const float* lse;
   void *dq, *dk, *dv;
   float *nlse, *ndelta; // workspace [batch * heads][rows padded to 64]
-  float c;              // |scale| * log2(e), at least kLeastC
+  float c;              // |scale| (float32), |scale| * log2(e), at least kLeastC
   int32_t padded, q_tiles, k_tiles, key_blocks;
 };
 
 namespace {
 
-// nlse = -lse in units of the raw scores, ndelta = -rowsum(do * o): what the
-// products q k^T and do v^T start from, so that the probability is
-// exp2(c * sum) and ds is p times the other sum, with no further operation.
+// 16-bit T: the products q k^T and do v^T start from -lse, in units of the raw
+// scores, and from -rowsum(do * o), so that the probability is exp2(c * sum) and
+// ds is p times the other sum, with no further operation.  float32: they start
+// from zero and the two are added afterwards, which keeps the sums' rounding
+// small (a score next to its lse loses the lse's digits otherwise).
+constexpr bool starts_from_rows(int size) { return size == 2; }
+
+template <typename T>
+__device__ __forceinline__ float probability(float sum, float c, float nlse) {
+  if constexpr (starts_from_rows(sizeof(T))) return __builtin_amdgcn_exp2f(sum * c);
+  else return __builtin_amdgcn_exp2f(fmaf(sum, c, nlse) * kLog2e);
+}
+
+// What those start from: nlse and ndelta = -rowsum(do * o).
 // Rows without a key, behind the entry's queries or in the padding get nlse =
 // -inf: their probabilities are then zero, and need no mask.  8 lanes a row.
 template <typename T>
@@ -60,7 +71,7 @@ __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
 #pragma unroll
   for (int off = 1; off < 8; off <<= 1) s += __shfl_xor(s, off, 64);
   if ((threadIdx.x & 7) == 0) {
-    a.nlse[at] = l == -INFINITY ? l : -l * kLog2e / a.c;
+    a.nlse[at] = l == -INFINITY ? l : starts_from_rows(sizeof(T)) ? -l * kLog2e / a.c : -l;
     a.ndelta[at] = l == -INFINITY ? 0.f : -s;
   }
 }
@@ -165,7 +176,9 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
       const T* qt = tiles + 2 * N * B::kTile;
       const T* ot = qt + B::kTile;
       const float* rt = rows + N * 64;
-      f32x16 s = load_c_rows(rt, h), dp = load_c_rows(rt + 32, h);
+      constexpr bool kFromRows = starts_from_rows(sizeof(T));
+      f32x16 s = kFromRows ? load_c_rows(rt, h) : zero16();
+      f32x16 dp = kFromRows ? load_c_rows(rt + 32, h) : zero16();
       each_step<NS>(p.d, [&](auto d) {
         s = mma(L::load_rows(qt, 0, d), kf[d], s);
         if constexpr (B::kVInLds)
@@ -179,8 +192,8 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
           if ((uint32_t)(row0 + 4 * h - lo + c_row(i, 0)) >= many) s[i] = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[i] = __builtin_amdgcn_exp2f(s[i] * a.c);
-        dp[i] *= s[i];
+        s[i] = probability<T>(s[i], a.c, kFromRows ? 0.f : rt[c_row(i, h)]);
+        dp[i] = (kFromRows ? dp[i] : dp[i] + rt[32 + c_row(i, h)]) * s[i];
       }
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
@@ -270,9 +283,10 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
       if (key0 >= wave_hi || key0 + 32 <= wave_lo) return;
       const T* kt = tiles + 2 * N * kTile;
       const T* vt = kt + kTile;
+      constexpr bool kFromRows = starts_from_rows(sizeof(T));
       f32x16 s, dp;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = nlse, dp[e] = ndelta;
+      for (int e = 0; e < 16; ++e) s[e] = kFromRows ? nlse : 0.f, dp[e] = kFromRows ? ndelta : 0.f;
       each_step<NS>(p.d, [&](auto d) {
         s = mma(L::load_rows(kt, 0, d), qf[d], s);
         dp = mma(L::load_rows(vt, 0, d), of[d], dp);
@@ -282,7 +296,8 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
         for (int e = 0; e < 16; ++e)
           if ((uint32_t)(key0 + 4 * h - lo + c_row(e, 0)) >= many) s[e] = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) dp[e] *= __builtin_amdgcn_exp2f(s[e] * a.c);
+      for (int e = 0; e < 16; ++e)
+        dp[e] = (kFromRows ? dp[e] : dp[e] + ndelta) * probability<T>(s[e], a.c, nlse);
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         const frag_t<T> df = to_frag<T>(dp, d);
@@ -350,7 +365,7 @@ int launch_attention_backward(const AttnParams& p, const AttnPlan& plan, const A
   k.padded = (p.sq + 63) / 64 * 64;
   k.nlse = (float*)a.ws;
   k.ndelta = k.nlse + (size_t)p.batch * p.heads * k.padded;
-  k.c = fmaxf(fabsf(p.scale) * kLog2e, kLeastC);
+  k.c = fmaxf(fabsf(p.scale) * (plan.dtype == FUSEDCONV_F32 ? 1.0f : kLog2e), kLeastC);
   k.q_tiles = (p.sq + 127) / 128;
   k.k_tiles = (p.sk + 127) / 128;
   k.key_blocks = (int32_t)xcd_grid((int64_t)p.batch * p.kv_heads * k.k_tiles);
