@@ -496,7 +496,7 @@ void plan_attention(const AttnParams& p, AttnPlan& plan) {
   // One wave a row group and the keys split inside the block: for up to 32 rows
   // (a wave's columns) or up to 16 queries, which the other form would leave
   // alone in a tile of 128 (2 x 5 queries on 30000 keys, 8 heads on one of 128:
-  // FEWT us, there 35); and for small float32 calls, whose tiles take
+  // 26 us, there 47); and for small float32 calls, whose tiles take
   // long: 8 heads of 64, 256 queries: 13 us, whole blocks 24; 512: 18 and 21
   // (split over blocks); but 1024: 42 and 32, and 16 x 128 queries, 512 row
   // groups: 22 and 15.

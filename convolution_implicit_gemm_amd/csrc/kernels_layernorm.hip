@@ -58,12 +58,28 @@ __device__ __forceinline__ void row_sum(float (&v)[K]) {
   }
 }
 
+// Where a piece of V values of a run of `all` lies.  WHOLE: at its own place.
+// Otherwise the last one of a run that is no whole number of pieces is moved
+// back to end with the run: it is loaded and stored like any other, its first
+// `shift` values are its neighbour's too (both work out the same) and are left
+// out of sums.  A run shorter than a piece is moved value by value.
+struct Place {
+  int at, shift;
+};
+template <bool WHOLE, int V>
+__device__ __forceinline__ Place place_of(int piece, int all) {
+  if (WHOLE) return {piece * V, 0};
+  const int at = max(min(piece * V, all - V), 0);
+  return {at, piece * V - at};
+}
+
 // ------------------------------------------------------------- token rows
 // TPR threads share a row and hold NCH pieces of V values each: thread t has
 // the pieces t, t + TPR, ...  256 threads a block.
 
-template <typename T, int V, int TPR, int NCH>
+template <typename T, bool WHOLE, int TPR, int NCH>
 __global__ __launch_bounds__(256) void k_norm_rows(NormK a) {
+  constexpr int V = 16 / sizeof(T);
   const int t = threadIdx.x % TPR;
   const int row = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
   if (row >= a.n) return;  // whole groups of TPR lanes: those that share a row's sums
@@ -75,23 +91,27 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormK a) {
   Piece<T, V> px[NCH], pw[NCH], pb[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int at = (t + i * TPR) * V;
+    const auto [at, shift] = place_of<WHOLE, V>(t + i * TPR, a.c);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       px[i].v[j] = pb[i].v[j] = (T)0.f;
       pw[i].v[j] = (T)1.f;
     }
-    if (at < a.c) {
-      px[i] = load_piece<T, V>(x + at);
-      if (w) pw[i] = load_piece<T, V>(w + at);
-      if (b) pb[i] = load_piece<T, V>(b + at);
+    if ((t + i * TPR) * V < a.c) {
+      load_run<WHOLE>(px[i], x + at, a.c - at);
+      if (w) load_run<WHOLE>(pw[i], w + at, a.c - at);
+      if (b) load_run<WHOLE>(pb[i], b + at, a.c - at);
     }
   }
   float sum[1] = {0.f};
+  const auto counts = [&](int i, int j) {  // value j of piece i in the sums
+    const auto [at, shift] = place_of<WHOLE, V>(t + i * TPR, a.c);
+    return WHOLE || (j >= shift && at + j < a.c);
+  };
 #pragma unroll
   for (int i = 0; i < NCH; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum[0] += (float)px[i].v[j];
+    for (int j = 0; j < V; ++j) sum[0] += counts(i, j) ? (float)px[i].v[j] : 0.f;
   row_sum<TPR>(sum);
   const float mean = sum[0] / (float)a.c;
   float sq[1] = {0.f};
@@ -101,7 +121,7 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormK a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float d = (float)px[i].v[j] - mean;
-        sq[0] += d * d;
+        sq[0] += counts(i, j) ? d * d : 0.f;
       }
   row_sum<TPR>(sq);
   const float rstd = 1.0f / sqrtf(sq[0] / (float)a.c + a.eps);
@@ -112,21 +132,22 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormK a) {
   T* y = (T*)a.out + (int64_t)row * a.c;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int at = (t + i * TPR) * V;
-    if (at >= a.c) continue;
+    const int at = place_of<WHOLE, V>(t + i * TPR, a.c).at;
+    if ((t + i * TPR) * V >= a.c) continue;
     Piece<T, V> py;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       py.v[j] = to_type<T>(((float)px[i].v[j] - mean) * rstd * (float)pw[i].v[j] + (float)pb[i].v[j]);
-    store_piece<T, V>(y + at, py);
+    store_run<WHOLE>(y + at, py, a.c - at);
   }
 }
 
 // Backward.  A thread keeps its columns' sums of dy and dy * xh over the rows
 // its group visits; the block's groups then meet in LDS, one group after the
 // other, and the block writes one partial row of both.
-template <typename T, int V, int TPR, int NCH>
+template <typename T, bool WHOLE, int TPR, int NCH>
 __global__ __launch_bounds__(256) void k_norm_rows_bwd(NormK a) {
+  constexpr int V = 16 / sizeof(T);
   constexpr int RPB = 256 / TPR;
   const int t = threadIdx.x % TPR;
   const int group = threadIdx.x / TPR;
@@ -137,8 +158,8 @@ __global__ __launch_bounds__(256) void k_norm_rows_bwd(NormK a) {
   for (int i = 0; i < NCH * V; ++i) dw[i] = db[i] = 0.f;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int at = (t + i * TPR) * V;
-    if (w && at < a.c) pw[i] = load_piece<T, V>(w + at);
+    const int at = place_of<WHOLE, V>(t + i * TPR, a.c).at;
+    if (w && (t + i * TPR) * V < a.c) load_run<WHOLE>(pw[i], w + at, a.c - at);
     else
 #pragma unroll
       for (int j = 0; j < V; ++j) pw[i].v[j] = (T)1.f;
@@ -154,10 +175,10 @@ __global__ __launch_bounds__(256) void k_norm_rows_bwd(NormK a) {
     nrstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int at = (t + i * TPR) * V;
-      if (at < a.c) {
-        nx[i] = load_piece<T, V>(x + at);
-        nd[i] = load_piece<T, V>(dy + at);
+      const int at = place_of<WHOLE, V>(t + i * TPR, a.c).at;
+      if ((t + i * TPR) * V < a.c) {
+        load_run<WHOLE>(nx[i], x + at, a.c - at);
+        load_run<WHOLE>(nd[i], dy + at, a.c - at);
       }
     }
   };
@@ -172,24 +193,26 @@ __global__ __launch_bounds__(256) void k_norm_rows_bwd(NormK a) {
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
-      if ((t + i * TPR) * V < a.c)
+      if ((t + i * TPR) * V < a.c) {
+        const auto [at, shift] = place_of<WHOLE, V>(t + i * TPR, a.c);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const float xh = ((float)px[i].v[j] - mean) * rstd;
-          const float d = (float)pd[i].v[j];
+          const float d = WHOLE || (j >= shift && at + j < a.c) ? (float)pd[i].v[j] : 0.f;
           const float g = d * (float)pw[i].v[j];
           s[0] += g;
           s[1] += g * xh;
           dw[i * V + j] += d * xh;
           db[i * V + j] += d;
         }
+      }
     row_sum<TPR>(s);
     const float c1 = s[0] / (float)a.c, c2 = s[1] / (float)a.c;
     T* dx = (T*)a.out + (int64_t)row * a.c;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int at = (t + i * TPR) * V;
-      if (at >= a.c) continue;
+      const int at = place_of<WHOLE, V>(t + i * TPR, a.c).at;
+      if ((t + i * TPR) * V >= a.c) continue;
       Piece<T, V> po;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -197,22 +220,22 @@ __global__ __launch_bounds__(256) void k_norm_rows_bwd(NormK a) {
         const float g = (float)pd[i].v[j] * (float)pw[i].v[j];
         po.v[j] = to_type<T>(rstd * (g - c1 - xh * c2));
       }
-      store_piece<T, V>(dx + at, po);
+      store_run<WHOLE>(dx + at, po, a.c - at);
     }
   }
   if (!a.part) return;
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
   if constexpr (RPB == 1) {
 #pragma unroll
-    for (int i = 0; i < NCH; ++i)
+    for (int i = 0; i < NCH; ++i) {
+      const auto [at, shift] = place_of<WHOLE, V>(t + i * TPR, a.c);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int at = (t + i * TPR) * V + j;
-        if (at < a.c) {
-          out[at] = dw[i * V + j];
-          out[a.c + at] = db[i * V + j];
+      for (int j = 0; j < V; ++j)
+        if ((t + i * TPR) * V < a.c && j >= shift && at + j < a.c) {
+          out[at + j] = dw[i * V + j];
+          out[a.c + at + j] = db[i * V + j];
         }
-      }
+    }
   } else {
     __shared__ float acc[2][NCH * V][TPR];
     for (int g = 0; g < RPB; ++g) {
@@ -225,7 +248,8 @@ __global__ __launch_bounds__(256) void k_norm_rows_bwd(NormK a) {
       __syncthreads();
     }
     for (int at = threadIdx.x; at < a.c; at += 256) {
-      const int piece = at / V, j = (piece / TPR) * V + at % V;
+      const int piece = at / V;
+      const int j = (piece / TPR) * V + at - place_of<WHOLE, V>(piece, a.c).at;
       out[at] = acc[0][j][piece % TPR];
       out[a.c + at] = acc[1][j][piece % TPR];
     }
@@ -309,15 +333,17 @@ __global__ __launch_bounds__(kLoopThreads) void k_norm_columns(NormK a) {
 constexpr int kPlaneThreads = 256;
 constexpr int kPlaneWaves = kPlaneThreads / 64;
 
-// The piece (of V values) `off` bytes behind a block's base pointer: one 32-bit
-// offset a lane for all its channels, whose distances go into the base.
-template <typename T, int V>
-__device__ __forceinline__ Piece<T, V> load_at(const T* base, int64_t step, uint32_t off) {
-  return *reinterpret_cast<const Piece<T, V>*>((const char*)(base + step) + off);
+// The piece `off` bytes behind a block's base pointer: one 32-bit offset a lane
+// for all its channels, whose distances go into the base.
+template <bool WHOLE, typename T, int V>
+__device__ __forceinline__ void load_at(Piece<T, V>& v, const T* base, int64_t step, uint32_t off,
+                                        int n) {
+  load_run<WHOLE>(v, (const T*)((const char*)(base + step) + off), n);
 }
-template <typename T, int V>
-__device__ __forceinline__ void store_at(T* base, int64_t step, uint32_t off, const Piece<T, V>& v) {
-  *reinterpret_cast<Piece<T, V>*>((char*)(base + step) + off) = v;
+template <bool WHOLE, typename T, int V>
+__device__ __forceinline__ void store_at(T* base, int64_t step, uint32_t off,
+                                         const Piece<T, V>& v, int n) {
+  store_run<WHOLE>((T*)((char*)(base + step) + off), v, n);
 }
 
 // Values of the block's waves for every pixel of a tile: [wave][k][lane][j].
@@ -362,15 +388,17 @@ __device__ __forceinline__ void pixel_sum(float (&v)[K][V]) {
 // own channels and the squares about that; the parts' squares about the common
 // mean follow from the distances of the means (exact, nothing cancels).
 // NCH: channels a thread holds; 0: any number, read again for each pass.
-template <typename T, int V, int PL, int NCH>
+template <typename T, bool WHOLE, int PL, int NCH>
 __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
+  constexpr int V = 16 / sizeof(T);
   constexpr int CG = kPlaneThreads / PL;
   constexpr int GW = 64 / PL;  // channel groups of a wave
   const int p = threadIdx.x % PL, g = threadIdx.x / PL;
   const int tile = blockIdx.x;
   const int image = tile / a.tiles;
-  const int pixel = ((tile - image * a.tiles) * PL + p) * V;
-  const bool live = pixel < a.inner;
+  const int piece = (tile - image * a.tiles) * PL + p;
+  const bool live = piece * V < a.inner;
+  const int pixel = place_of<WHOLE, V>(piece, a.inner).at, left = a.inner - pixel;
   const T* x = (const T*)a.x + (int64_t)image * a.x_stride;
   T* y = (T*)a.out + (int64_t)image * a.c * a.inner;
   const uint32_t off = (uint32_t)(g * a.inner + pixel) * sizeof(T);
@@ -387,13 +415,13 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
     } else {
       if (live)
         for (int i = 0; g + i * CG < a.c; ++i) {
-          px[0] = load_at<T, V>(x, i * step, off);
+          load_at<WHOLE>(px[0], x, i * step, off, left);
           f(i, g + i * CG);
         }
     }
   };
   if constexpr (NCH > 0)
-    each([&](int i, int) { px[i] = load_at<T, V>(x, i * step, off); });
+    each([&](int i, int) { load_at<WHOLE>(px[i], x, i * step, off, left); });
   // The parameters wait in LDS for the last pass (32 x 128 channels of 192 x 192:
   // 119 us; read from memory in that pass 126; kept in registers, which costs a
   // third of the waves, 153).  The exchange below is also their barrier.
@@ -452,10 +480,11 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
   if (g == 0 && live && a.mean) {
     const int64_t at = (int64_t)image * a.inner + pixel;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      a.mean[at + j] = mean[j];
-      a.rstd[at + j] = rstd[j];
-    }
+    for (int j = 0; j < V; ++j)
+      if (WHOLE || j < left) {
+        a.mean[at + j] = mean[j];
+        a.rstd[at + j] = rstd[j];
+      }
   }
   each([&](int i, int ch) {
     const int k = HELD > 1 ? i : 0;
@@ -472,14 +501,15 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
       py.v[j] = to_type<T>(((float)px[k].v[j] - mean[j]) * rstd[j] * wc + bc);
-    store_at<T, V>(y, i * step, off, py);
+    store_at<WHOLE>(y, i * step, off, py, left);
   });
 }
 
 // Backward: blocks walk the tiles of all images; a thread keeps the sums of
 // its channels over its own pixels, the PL lanes of a channel meet at the end.
-template <typename T, int V, int PL, int NCH>
+template <typename T, bool WHOLE, int PL, int NCH>
 __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
+  constexpr int V = 16 / sizeof(T);
   constexpr int CG = kPlaneThreads / PL;
   const int p = threadIdx.x % PL, g = threadIdx.x / PL;
   const T* w = (const T*)a.w;
@@ -494,8 +524,10 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
   const int all = a.n * a.tiles;
   for (int tile = blockIdx.x; tile < all; tile += gridDim.x) {
     const int image = tile / a.tiles;
-    const int pixel = ((tile - image * a.tiles) * PL + p) * V;
-    const bool live = pixel < a.inner;
+    const int piece = (tile - image * a.tiles) * PL + p;
+    const bool live = piece * V < a.inner;
+    const auto [pixel, shift] = place_of<WHOLE, V>(piece, a.inner);
+    const int left = a.inner - pixel;
     const T* x = (const T*)a.x + (int64_t)image * a.x_stride;
     const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride;
     T* dx = (T*)a.out + (int64_t)image * a.c * a.inner;
@@ -505,13 +537,13 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
       if (live && g + i * CG < a.c) {
-        px[i] = load_at<T, V>(x, i * step, off);
-        pd[i] = load_at<T, V>(dy, i * step, off);
+        load_at<WHOLE>(px[i], x, i * step, off, left);
+        load_at<WHOLE>(pd[i], dy, i * step, off, left);
       }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      mean[j] = live ? a.mean[(int64_t)image * a.inner + pixel + j] : 0.f;
-      rstd[j] = live ? a.rstd[(int64_t)image * a.inner + pixel + j] : 0.f;
+      mean[j] = live && (WHOLE || j < left) ? a.mean[(int64_t)image * a.inner + pixel + j] : 0.f;
+      rstd[j] = live && (WHOLE || j < left) ? a.rstd[(int64_t)image * a.inner + pixel + j] : 0.f;
       s[0][j] = s[1][j] = 0.f;
     }
 #pragma unroll
@@ -523,8 +555,10 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
           const float d = (float)pd[i].v[j];
           s[0][j] += d * wc[i];
           s[1][j] += d * wc[i] * xh;
-          dw[i] += d * xh;
-          db[i] += d;
+          if (WHOLE || j >= shift) {
+            dw[i] += d * xh;
+            db[i] += d;
+          }
         }
       }
     pixel_sum<PL, V>(s);
@@ -541,7 +575,7 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
           const float xh = ((float)px[i].v[j] - mean[j]) * rstd[j];
           po.v[j] = to_type<T>(rstd[j] * ((float)pd[i].v[j] * wc[i] - s[0][j] - xh * s[1][j]));
         }
-        store_at<T, V>(dx, i * step, off, po);
+        store_at<WHOLE>(dx, i * step, off, po, left);
       }
   }
   if (!a.part) return;
@@ -559,27 +593,30 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd(NormK a) {
 
 // Any number of channels: X and dY read again for the second pass, and dx
 // alone; the weight gradients come from k_norm_plane_sums.
-template <typename T, int V, int PL>
+template <typename T, bool WHOLE, int PL>
 __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd_loop(NormK a) {
+  constexpr int V = 16 / sizeof(T);
   constexpr int CG = kPlaneThreads / PL;
   const int p = threadIdx.x % PL, g = threadIdx.x / PL;
   const T* w = (const T*)a.w;
   const int image = blockIdx.x / a.tiles;
-  const int pixel = ((blockIdx.x - image * a.tiles) * PL + p) * V;
-  const bool live = pixel < a.inner;
+  const int piece = (blockIdx.x - image * a.tiles) * PL + p;
+  const bool live = piece * V < a.inner;
+  const int pixel = place_of<WHOLE, V>(piece, a.inner).at, left = a.inner - pixel;
   const T* x = (const T*)a.x + (int64_t)image * a.x_stride + pixel;
   const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride + pixel;
   T* dx = (T*)a.out + (int64_t)image * a.c * a.inner + pixel;
   float mean[V], rstd[V], s[2][V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    mean[j] = live ? a.mean[(int64_t)image * a.inner + pixel + j] : 0.f;
-    rstd[j] = live ? a.rstd[(int64_t)image * a.inner + pixel + j] : 0.f;
+    mean[j] = live && (WHOLE || j < left) ? a.mean[(int64_t)image * a.inner + pixel + j] : 0.f;
+    rstd[j] = live && (WHOLE || j < left) ? a.rstd[(int64_t)image * a.inner + pixel + j] : 0.f;
     s[0][j] = s[1][j] = 0.f;
   }
   for (int ch = g; live && ch < a.c; ch += CG) {
-    const Piece<T, V> px = load_piece<T, V>(x + (int64_t)ch * a.inner);
-    const Piece<T, V> pd = load_piece<T, V>(dy + (int64_t)ch * a.inner);
+    Piece<T, V> px, pd;
+    load_run<WHOLE>(px, x + (int64_t)ch * a.inner, left);
+    load_run<WHOLE>(pd, dy + (int64_t)ch * a.inner, left);
     const float wc = w ? (float)w[ch] : 1.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -590,8 +627,9 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd_loop(NormK a)
   }
   pixel_sum<PL, V>(s);
   for (int ch = g; live && ch < a.c; ch += CG) {
-    const Piece<T, V> px = load_piece<T, V>(x + (int64_t)ch * a.inner);
-    const Piece<T, V> pd = load_piece<T, V>(dy + (int64_t)ch * a.inner);
+    Piece<T, V> px, pd;
+    load_run<WHOLE>(px, x + (int64_t)ch * a.inner, left);
+    load_run<WHOLE>(pd, dy + (int64_t)ch * a.inner, left);
     const float wc = w ? (float)w[ch] : 1.f;
     Piece<T, V> po;
 #pragma unroll
@@ -600,7 +638,7 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd_loop(NormK a)
       po.v[j] = to_type<T>(rstd[j] * ((float)pd.v[j] * wc - s[0][j] / (float)a.c -
                                       xh * (s[1][j] / (float)a.c)));
     }
-    store_piece<T, V>(dx + (int64_t)ch * a.inner, po);
+    store_run<WHOLE>(dx + (int64_t)ch * a.inner, po, left);
   }
 }
 
@@ -665,7 +703,7 @@ __global__ void k_norm_zero(float* dw, float* db, int c) {
 // ------------------------------------------------------------- variants
 struct NormPlan {
   bool planes, loop;
-  int v;        // values an access moves
+  bool whole;   // every row (plane) is whole aligned pieces
   int tpr;      // rows: threads a row; planes: pixel lanes
   int nch;      // pieces (planes: channels) a thread holds
   int blocks;   // backward: blocks that leave a partial
@@ -674,26 +712,28 @@ struct NormPlan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The wide form needs every row (plane) to start on a 16-byte border and to
-// be whole pieces; otherwise single values are moved.
+// Rows (planes) that start on 16-byte borders and are whole pieces are moved as
+// such.  Others are moved in pieces too, at their own alignment (single values
+// instead: 256 x 768 f16 planes of 7 x 7 39 us, so 22; 16000 x 513 rows, backward,
+// 83 and 64; rows of 4099 73 and 47).
 NormPlan plan_norm(const NormProblem& p, bool backward) {
   NormPlan q{};
-  const int es = p.dtype == FUSEDCONV_F32 ? 4 : 2;
   q.planes = p.inner > 1;
-  const int wide = 16 / es;
+  const int wide = p.dtype == FUSEDCONV_F32 ? 4 : 8;
   const int64_t run = q.planes ? p.inner : p.c;
-  const bool strided = p.x_stride % wide || (backward && p.dy_stride % wide);
-  q.v = run % wide == 0 && !strided ? wide : 1;
+  q.whole = run % wide == 0 && p.x_stride % wide == 0 && (!backward || p.dy_stride % wide == 0);
   if (!q.planes) {
-    const int64_t pieces = ceil_div(p.c, q.v);
+    const int64_t pieces = ceil_div(p.c, wide);
     // Up to 64 pieces a row: the smallest power of two of lanes, one piece
     // each.  Up to four pieces a lane, one wave a row (no barrier); then one
-    // block a row.
+    // block a row.  Backward, rows that are no whole pieces go over to a block
+    // above two pieces a lane: with four the registers leave two waves a SIMD
+    // (25700 rows of 1275 f16: 69 us, so 61).
     q.tpr = 8;
     while (q.tpr < 64 && q.tpr < pieces) q.tpr *= 2;
     q.nch = 1;
     if (pieces > 64) {
-      q.tpr = pieces <= 256 ? 64 : 256;
+      q.tpr = pieces <= (backward && !q.whole ? 128 : 256) ? 64 : 256;
       while (q.nch * q.tpr < pieces) q.nch *= 2;
     }
     q.loop = q.nch > 8;
@@ -704,23 +744,20 @@ NormPlan plan_norm(const NormProblem& p, bool backward) {
     if (q.loop && q.blocks > 64) q.blocks = 64;
     return q;
   }
-  if (q.v == 1 && p.inner % (wide / 2) == 0 && p.x_stride % (wide / 2) == 0 &&
-      (!backward || p.dy_stride % (wide / 2) == 0))
-    q.v = wide / 2;
   // Pixel lanes: as many as leave a thread 16 channels or fewer.  Long runs of a
   // plane and many values in flight per thread both count (f16, 128 channels of
   // 192 x 192, forward: 8 / 16 / 32 lanes 157 / 123 / 122 us; 384 of 56 x 56: 71 /
   // 80 / 105, the last two with 24 and 48 channels a thread), but not where the
   // planes are shorter than the lanes or the tiles too few for the chip.
   q.tpr = 32;
-  while (q.tpr > 8 && (p.c * q.tpr > 16 * kPlaneThreads || q.tpr / 2 * q.v >= p.inner ||
-                       p.n * ceil_div(p.inner, (int64_t)q.tpr * q.v) < 512))
+  while (q.tpr > 8 && (p.c * q.tpr > 16 * kPlaneThreads || q.tpr / 2 * wide >= p.inner ||
+                       p.n * ceil_div(p.inner, (int64_t)q.tpr * wide) < 512))
     q.tpr /= 2;
   const int cg = kPlaneThreads / q.tpr;
   q.nch = 2;
   while (q.nch * cg < p.c && q.nch <= 32) q.nch = q.nch < 4 ? 4 : q.nch < 16 ? q.nch + 4 : q.nch + 8;
   q.loop = q.nch > (backward ? 16 : 32);
-  q.tiles = (int)ceil_div(p.inner, (int64_t)q.tpr * q.v);
+  q.tiles = (int)ceil_div(p.inner, (int64_t)q.tpr * wide);
   const int64_t all = p.n * q.tiles;
   const int64_t most = q.nch <= 8 ? 768 : 512;  // blocks that fit the chip's registers at once
   q.blocks = (int)(all < most ? all : most);
@@ -744,8 +781,8 @@ NormK kernel_args(const NormProblem& p, const NormArgs& a, const NormPlan& q) {
 template <int I>
 using int_c = std::integral_constant<int, I>;
 
-// f(V, TPR, NCH) as compile-time constants for a register-held row plan.
-template <typename T, typename F>
+// f(WHOLE, TPR, NCH) as compile-time constants for a register-held row plan.
+template <typename F>
 void with_rows(const NormPlan& q, F&& f) {
   auto pick = [&](auto v) {
     if (q.tpr == 8) f(v, int_c<8>{}, int_c<1>{});
@@ -754,16 +791,17 @@ void with_rows(const NormPlan& q, F&& f) {
     else if (q.tpr == 64 && q.nch == 1) f(v, int_c<64>{}, int_c<1>{});
     else if (q.tpr == 64 && q.nch == 2) f(v, int_c<64>{}, int_c<2>{});
     else if (q.tpr == 64) f(v, int_c<64>{}, int_c<4>{});
+    else if (q.nch == 1) f(v, int_c<256>{}, int_c<1>{});
     else if (q.nch == 2) f(v, int_c<256>{}, int_c<2>{});
     else if (q.nch == 4) f(v, int_c<256>{}, int_c<4>{});
     else f(v, int_c<256>{}, int_c<8>{});
   };
-  if (q.v == 1) pick(int_c<1>{});
-  else pick(int_c<16 / sizeof(T)>{});
+  if (q.whole) pick(std::true_type{});
+  else pick(std::false_type{});
 }
 
-// f(V, PL, NCH) for a plane plan; NCH = 0: the looped form.
-template <typename T, bool BACKWARD, typename F>
+// f(WHOLE, PL, NCH) for a plane plan; NCH = 0: the looped form.
+template <bool BACKWARD, typename F>
 void with_planes(const NormPlan& q, F&& f) {
   auto pick = [&](auto v, auto pl) {
     if (q.loop) f(v, pl, int_c<0>{});
@@ -782,10 +820,8 @@ void with_planes(const NormPlan& q, F&& f) {
     else if (q.tpr == 16) pick(v, int_c<16>{});
     else pick(v, int_c<32>{});
   };
-  constexpr int wide = 16 / sizeof(T);
-  if (q.v == 1) lanes(int_c<1>{});
-  else if (q.v == wide) lanes(int_c<wide>{});
-  else lanes(int_c<wide / 2>{});
+  if (q.whole) lanes(std::true_type{});
+  else lanes(std::false_type{});
 }
 
 int status() { return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH; }
@@ -804,14 +840,14 @@ int launch_norm_forward(const NormProblem& p, const NormArgs& a) {
   with_type(p.dtype, [&](auto tag) {
     using T = typename decltype(tag)::type;
     if (q.planes)
-      with_planes<T, false>(q, [&](auto v, auto pl, auto nch) {
+      with_planes<false>(q, [&](auto v, auto pl, auto nch) {
         hipLaunchKernelGGL((k_norm_planes<T, v, pl, nch>), dim3((unsigned)(p.n * q.tiles)),
                            dim3(kPlaneThreads), 0, st, k);
       });
     else if (q.loop)
       hipLaunchKernelGGL((k_norm_rows_loop<T>), dim3((unsigned)p.n), dim3(kLoopThreads), 0, st, k);
     else
-      with_rows<T>(q, [&](auto v, auto tpr, auto nch) {
+      with_rows(q, [&](auto v, auto tpr, auto nch) {
         hipLaunchKernelGGL((k_norm_rows<T, v, tpr, nch>),
                            dim3((unsigned)ceil_div(p.n, 256 / tpr)), dim3(256), 0, st, k);
       });
@@ -832,7 +868,7 @@ int launch_norm_backward(const NormProblem& p, const NormArgs& a) {
   with_type(p.dtype, [&](auto tag) {
     using T = typename decltype(tag)::type;
     if (q.planes) {
-      with_planes<T, true>(q, [&](auto v, auto pl, auto nch) {
+      with_planes<true>(q, [&](auto v, auto pl, auto nch) {
         if constexpr (nch == 0) {
           hipLaunchKernelGGL((k_norm_planes_bwd_loop<T, v, pl>), dim3((unsigned)(p.n * q.tiles)),
                              dim3(kPlaneThreads), 0, st, k);
@@ -851,7 +887,7 @@ int launch_norm_backward(const NormProblem& p, const NormArgs& a) {
                            dim3(q.blocks, (unsigned)ceil_div(p.c, kLoopThreads)),
                            dim3(kLoopThreads), 0, st, k);
     } else {
-      with_rows<T>(q, [&](auto v, auto tpr, auto nch) {
+      with_rows(q, [&](auto v, auto tpr, auto nch) {
         hipLaunchKernelGGL((k_norm_rows_bwd<T, v, tpr, nch>), dim3(q.blocks), dim3(256), 0, st, k);
       });
     }

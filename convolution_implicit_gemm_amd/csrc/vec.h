@@ -74,6 +74,34 @@ __device__ __forceinline__ int xcd_item(int block, int total) {
 }
 inline unsigned xcd_grid(int64_t total) { return (unsigned)((total + 7) / 8 * 8); }
 
+// The V values at p, or the first n of them where the rest lies behind a row's
+// end (zeros then).  WHOLE: p is aligned to the piece and all V are there.
+// Otherwise p has any alignment: the hardware takes wide accesses at every
+// element's address.
+template <bool WHOLE, typename T, int V>
+__device__ __forceinline__ void load_run(Piece<T, V>& v, const T* p, int n) {
+  if (WHOLE) {
+    v = load_piece<T, V>(p);
+  } else if (n >= V) {
+    __builtin_memcpy(&v, p, sizeof(v));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v.v[j] = j < n ? p[j] : (T)0.f;
+  }
+}
+template <bool WHOLE, typename T, int V>
+__device__ __forceinline__ void store_run(T* p, const Piece<T, V>& v, int n) {
+  if (WHOLE) {
+    store_piece<T, V>(p, v);
+  } else if (n >= V) {
+    __builtin_memcpy(p, &v, sizeof(v));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < n) p[j] = v.v[j];
+  }
+}
+
 // Run f(tag<T>) for the element type of a FUSEDCONV_* code.
 template <typename T>
 struct type_tag {
