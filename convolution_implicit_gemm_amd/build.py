@@ -19,16 +19,13 @@ BUILD = os.path.join(PKG, "_build")
 SOURCES = ["resolver.cpp", "planner.cpp", "capi.cpp", "kernels_direct.hip", "kernels_igemm.hip",
            "kernels_transposed.hip", "kernels_im2col.hip", "noalloc.hip", "backward.cpp",
            "kernels_backward.hip", "kernels_halo32.hip", "transformer.cpp",
-           "kernels_layernorm.hip", "kernels_rotary.hip"]
+           "kernels_layernorm.hip", "kernels_rotary.hip", "kernels_attention_d128.hip",
+           "kernels_attention_d96.hip", "kernels_attention_d64.hip", "kernels_attention_d32.hip"]
 # Kernels specialised per activation: compiled once per activation id
 # (-DFC_ACT=k, k = 0 .. ACT_COUNT-1); unit 0 also holds the route entry points.
 ACT_SOURCES = ["kernels_depthwise.hip", "kernels_dwmfma.hip", "kernels_halo.hip",
                "kernels_smallc.hip", "kernels_pointwise.hip"]
 ACT_COUNT = 15
-# Attention kernels, compiled once per head size their tiles are made for
-# (-DFC_DP=k); unit 32 also holds the planner and the launchers.
-DP_SOURCES = ["kernels_attention.hip", "kernels_attention_backward.hip"]
-DP_SIZES = [128, 96, 64, 32]
 ARCH = "gfx950"
 # Packed fp32 ops stay off (the compiler is not allowed to form v_pk_*_f32).
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-unused-function",
@@ -36,11 +33,11 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-
 
 
 def _compile(job) -> str:
-    src, key, val = job
-    stem = os.path.splitext(src)[0] + (f"_{key[3].lower()}{val}" if key else "")
+    src, act = job
+    stem = os.path.splitext(src)[0] + ("" if act is None else f"_a{act}")
     obj = os.path.join(BUILD, stem + ".o")
     lang = ["-x", "hip"] if src.endswith(".hip") else []
-    defs = [f"-D{key}={val}"] if key else []
+    defs = [] if act is None else [f"-DFC_ACT={act}"]
     cmd = ["hipcc", *FLAGS, *defs, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     out = "\n".join(ln for ln in (r.stdout + r.stderr).splitlines()
@@ -54,9 +51,7 @@ def _compile(job) -> str:
 
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    jobs = [(f, "FC_DP", k) for f in DP_SOURCES for k in DP_SIZES]
-    jobs += [(f, "FC_ACT", k) for f in ACT_SOURCES for k in range(ACT_COUNT)]
-    jobs += [(f, None, None) for f in SOURCES]
+    jobs = [(f, k) for f in ACT_SOURCES for k in range(ACT_COUNT)] + [(f, None) for f in SOURCES]
     workers = max(1, min(16, os.cpu_count() or 1))
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
         objs = list(ex.map(_compile, jobs))

@@ -7,7 +7,9 @@
 // 4 * q_len * head_dim bytes that every key block would otherwise add to dq in
 // memory, in an order that changes.
 //
-// Compiled once per head size the tiles are made for (FC_DP).
+// Compiled once per head size the tiles are made for, as the forward pass is.
+#pragma once
+
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -324,8 +326,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_backw
   if ((int)blockIdx.x < a.key_blocks) keys_block<T, DP>(a, blockIdx.x);
   else queries_block<T, DP>(a, blockIdx.x - a.key_blocks);
 }
-
-#define FC_DP_NAME(name) FC_CAT(name, FC_DP)
 
 }  // namespace
 

@@ -1,12 +1,14 @@
 // Attention, forward (include/fusedconv_transformer.h): one pass over the keys
 // with the running maximum and sum of the softmax.
 //
-// Compiled once per head size the tiles are made for (FC_DP = 32, 64, 96, 128);
-// unit 32 also holds the plan and the launcher.
+// Compiled once per head size the tiles are made for (FC_DP = 32, 64, 96, 128,
+// kernels_attention_d*.hip); unit 32 also holds the plan and the launcher.
 //
 // Scores are computed transposed, S^T = K Q^T: a lane then holds one query
 // (C's column) and half of a tile's keys, the softmax needs one exchange per
 // tile, and the probabilities are the B operand of O^T = V^T P^T as they stand.
+#pragma once
+
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -447,8 +449,6 @@ __global__ __launch_bounds__(256) void k_attention_join(AttnK a) {
   if (lane == 0 && a.lse)
     a.lse[((int64_t)b * p.heads + head) * p.sq + i] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
-
-#define FC_DP_NAME(name) FC_CAT(name, FC_DP)
 
 }  // namespace
 

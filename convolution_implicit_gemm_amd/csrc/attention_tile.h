@@ -375,4 +375,7 @@ constexpr float kLeastC = 1e-20f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// A function of the unit for one head size (FC_DP).
+#define FC_DP_NAME(name) FC_CAT(name, FC_DP)
+
 }  // namespace fc
