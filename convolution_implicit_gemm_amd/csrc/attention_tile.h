@@ -117,18 +117,29 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // every transposing read; here the kernels wait (tile_barrier, vmcnt) where a
 // tile is needed.  The instruction has no output register, and its address is
 // read when it is issued.
+#ifdef __OPTIMIZE__
+#define FC_WAVE_POINTER(p) (p)
+#else
+// An unoptimized build keeps even values that are the same for the whole wave in
+// vector registers; the operand has to be scalar.
+#define FC_WAVE_POINTER(p)                                                                       \
+  ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)(p) >> 32)) << 32 |   \
+   (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uint64_t)(p)))
+#endif
 template <int BYTES>
 __device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t off, const void* base) {
-  to = __builtin_amdgcn_readfirstlane(to);
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to),
-                 "v"(off), "s"(base)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+                     __builtin_amdgcn_readfirstlane(to)),
+                 "v"(off), "s"(FC_WAVE_POINTER(base))
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(to),
-                 "v"(off), "s"(base)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
+                     __builtin_amdgcn_readfirstlane(to)),
+                 "v"(off), "s"(FC_WAVE_POINTER(base))
                  : "memory");
 }
+#undef FC_WAVE_POINTER
 
 // A tile of ROWS rows of DP values in LDS, in 16-byte chunks.  Chunk c of row r
 // lies at chunk c ^ swizzle(r) of the row, so that both ways of reading a tile
