@@ -4,7 +4,9 @@
 // the cosines and sines of its tokens' pairs, once for all heads of Q and K,
 // then turns the heads: each item is one 16-byte piece of one half of a head
 // and its partner in the other half (interleaved: one piece), so every value
-// is read once and written once; the call is bound by HBM.
+// is read once and written once; the call is bound by HBM: 256 x 196 tokens, 12
+// heads of 64 in Q and K, bf16, 309 MB in 60 us.  Loading the next item before
+// the present one is stored gained nothing (58 to 60).
 //
 // The angle pos * inv_freq is taken in 64 bits and reduced there to a fraction
 // of a turn in [-1/2, 1/2]: at position 10^6 an angle in 32 bits would be off
