@@ -12,6 +12,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attention_tile.h"
@@ -29,7 +30,11 @@ struct AttnBwdK {
   void *dq, *dk, *dv;
   float *nlse, *ndelta; // workspace [batch * heads][rows padded to 64]
   float c;              // |scale| (float32), |scale| * log2(e), at least kLeastC
-  int32_t padded, q_tiles, k_tiles, key_blocks;
+  // Partial gradients where the queries of a key block are split over k_splits
+  // blocks, the keys of a query block over q_splits: [k_splits][dk, dv][batch]
+  // [kv_heads][sk][d], [q_splits][batch][heads][sq][d].
+  float *part_k, *part_q;
+  int32_t padded, q_tiles, k_tiles, key_blocks, k_splits, q_splits;
 };
 
 namespace {
@@ -107,7 +112,7 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
   float* rows = (float*)(lds + B::kLds) - 128;           // [2 buffers][nlse, ndelta][32]
 
   const AttnParams& p = a.p;
-  const int total = p.batch * p.kv_heads * a.k_tiles;
+  const int total = p.batch * p.kv_heads * a.k_splits * a.k_tiles;
   int item = xcd_item(block, total);
   if (item >= total) return;
   // The first keys first: a causal window shows them to most queries.  Where
@@ -116,6 +121,8 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
   const int turn = total <= 512 ? item / a.k_tiles & 1 : 0;
   const int tile_k = turn ? a.k_tiles - 1 - item % a.k_tiles : item % a.k_tiles;
   item /= a.k_tiles;
+  int split = 0;
+  if (a.k_splits > 1) split = item % a.k_splits, item /= a.k_splits;
   const int kvh = item % p.kv_heads, b = item / p.kv_heads;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, h = lane >> 5;
@@ -130,13 +137,20 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
   const int all_lo = see.qlo(w1), all_hi = see.qhi(w0);
   const int lo = see.qlo(j);
   const uint32_t many = max(see.qhi(j) - lo, 0);
+  // Tiles are numbered through the heads of the group; this block's are t0 .. t1 - 1.
+  const int items = first < end ? (end - first + 31) / 32 : 0;
+  int t0 = 0, t1 = items * p.group;
+  if (a.k_splits > 1) {
+    t0 = share(t1, split, a.k_splits);
+    t1 = share(t1, split + 1, a.k_splits);
+  }
 
   f32x16 dk[NT], dv[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) dk[t] = dv[t] = zero16();
 
   L::template clear_padding<128 + (B::kVInLds ? 128 : 0)>(tiles, p.d, threadIdx.x, 256);
-  if (first < end) {
+  if (t0 < t1) {
     frag_t<T> kf[NS], vf[B::kVInLds ? 1 : NS];
     const T* vp = (const T*)a.v + b * p.v.b + kvh * p.v.h;
     auto operands = [&] {
@@ -159,10 +173,10 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
       cv.init(p.v.s, p.d, wave);
       cv.start(vt, vp + key0 * p.v.s, see.nk - 1 - key0, wave);
     }
-    const int items = (end - first + 31) / 32;
-    // Tiles are numbered through the heads of the group: where the next one to
-    // copy and the next one to use are.
-    int start_g = 0, start_row = first, use_row = first;
+    // where the next tile to copy and the next one to use are
+    int start_g = 0, start_row = first;
+    if (t0 > 0) start_g = t0 / items, start_row += 32 * (t0 - start_g * items);
+    int use_row = start_row;
     auto start = [&](int, auto N) {
       copy.start(tiles + (2 * N + second) * B::kTile,
                  src + start_g * st.h + start_row * st.s, see.nq - 1 - start_row, wave & 1);
@@ -209,10 +223,22 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
         }
       }
     };
-    walk_tiles(items * p.group, start, operands, use);
+    walk_tiles(t1 - t0, start, operands, use);
   }
   if (j >= p.sk) return;
   const bool keep = j < see.nk;
+  if (a.k_splits > 1) {
+    const int64_t one = (int64_t)p.batch * p.kv_heads * p.sk * p.d;
+    float* pk = a.part_k + 2 * split * one + (((int64_t)b * p.kv_heads + kvh) * p.sk + j) * p.d;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      store_row<float>(pk + 32 * t, dk[t], p.d - 32 * t, h,
+                       [&](float v) { return keep ? v * p.scale : 0.f; });
+      store_row<float>(pk + one + 32 * t, dv[t], p.d - 32 * t, h,
+                       [&](float v) { return keep ? v : 0.f; });
+    }
+    return;
+  }
   T* dkp = (T*)a.dk + b * p.dk.b + j * p.dk.s + kvh * p.dk.h;
   T* dvp = (T*)a.dv + b * p.dv.b + j * p.dv.s + kvh * p.dv.h;
 #pragma unroll
@@ -235,11 +261,13 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
   T* tiles = (T*)lds;  // [2 buffers][K, V][32 * DP]
 
   const AttnParams& p = a.p;
-  const int total = p.batch * p.heads * a.q_tiles;
+  const int total = p.batch * p.heads * a.q_splits * a.q_tiles;
   int item = xcd_item(block, total);
   if (item >= total) return;
   const int tile_q = a.q_tiles - 1 - item % a.q_tiles;
   item /= a.q_tiles;
+  int split = 0;
+  if (a.q_splits > 1) split = item % a.q_splits, item /= a.q_splits;
   const int head = item % p.heads, b = item / p.heads, kvh = head / p.group;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, h = lane >> 5;
@@ -248,8 +276,15 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
   const int w0 = row0 + wave * 32, w1 = min(w0 + 31, see.nq - 1);
   const int i = w0 + (lane & 31);
 
-  const int first = row0 < see.nq ? see.lo(row0) & ~31 : 0;
+  int first = row0 < see.nq ? see.lo(row0) & ~31 : 0;
   const int end = row0 < see.nq ? see.hi(last_row) : 0;
+  const int items = first < end ? (end - first + 31) / 32 : 0;
+  int count = items;
+  if (a.q_splits > 1) {
+    const int t0 = share(items, split, a.q_splits);
+    count = share(items, split + 1, a.q_splits) - t0;
+    first += 32 * t0;
+  }
   const int wave_lo = see.lo(w0), wave_hi = w0 < see.nq ? see.hi(w1) : 0;
   const int all_lo = see.lo(w1), all_hi = w0 + 31 < see.nq ? see.hi(w0) : 0;
   const int lo = see.lo(i);
@@ -259,7 +294,7 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) dq[t] = zero16();
   L::template clear_padding<4 * 32>(tiles, p.d, threadIdx.x, 256);
-  if (first < end) {
+  if (count > 0) {
     // waves 0 and 1 copy K, waves 2 and 3 V
     typename L::template Copier<32, 2> copy;
     const bool second = wave >= 2;
@@ -309,9 +344,17 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
         for (int t = 0; t < NT; ++t) dq[t] = mma(L::load_columns(kt, 16 * d, t), df, dq[t]);
       }
     };
-    walk_tiles((end - first + 31) / 32, start, operands, use);
+    walk_tiles(count, start, operands, use);
   }
   if (i >= p.sq) return;
+  if (a.q_splits > 1) {
+    const int64_t row = (((int64_t)split * p.batch + b) * p.heads + head) * p.sq + i;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      store_row<float>(a.part_q + row * p.d + 32 * t, dq[t], p.d - 32 * t, h,
+                       [&](float v) { return i < see.nq ? v * p.scale : 0.f; });
+    return;
+  }
   T* out = (T*)a.dq + b * p.dq.b + i * p.dq.s + head * p.dq.h;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -334,6 +377,45 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_backw
   else queries_block<T, DP>(a, blockIdx.x - a.key_blocks);
 }
 
+// The partial gradients' sums, in the splits' order: a thread has eight values.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attention_sums(AttnBwdK a, uint32_t key_items,
+                                                        uint32_t items) {
+  const AttnParams& p = a.p;
+  uint32_t at = blockIdx.x * 256 + threadIdx.x;
+  if (at >= items) return;
+  const bool keys = at < key_items;
+  if (!keys) at -= key_items;
+  const uint32_t pieces = p.d / 8, len = keys ? p.sk : p.sq, heads = keys ? p.kv_heads : p.heads;
+  const int splits = keys ? a.k_splits : a.q_splits;
+  const int64_t step = (int64_t)(keys ? 2 : 1) * p.batch * heads * len * p.d;
+  const float* part = (keys ? a.part_k : a.part_q) + (int64_t)at * 8;
+  float acc[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s, part += step) {
+    const Piece<float, 4> x = load_piece<float, 4>(part), y = load_piece<float, 4>(part + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += x.v[e], acc[4 + e] += y.v[e];
+  }
+  uint32_t row = at / pieces;
+  const int d0 = (int)(at - row * pieces) * 8;
+  const int i = (int)(row % len);
+  row /= len;
+  const int head = (int)(row % heads);
+  row /= heads;
+  const int b = (int)(row % (uint32_t)p.batch);
+  const bool dv = keys && row >= (uint32_t)p.batch;
+  const Strides3 st = dv ? p.dv : keys ? p.dk : p.dq;
+  T* out = (T*)(dv ? a.dv : keys ? a.dk : a.dq) + b * st.b + i * st.s + head * st.h + d0;
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    Piece<T, 4> y;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y.v[u] = to_type<T>(acc[e + u]);
+    store_piece<T, 4>(out + e, y);
+  }
+}
+
 }  // namespace
 
 int FC_DP_NAME(attention_backward_)(const AttnPlan& plan, const AttnBwdK& k, hipStream_t st) {
@@ -350,8 +432,14 @@ int FC_DP_NAME(attention_backward_)(const AttnPlan& plan, const AttnBwdK& k, hip
     static_assert(bytes >= 4 * Tile<T, FC_DP>::bytes(32));
     rc = set_max_dynamic_lds((const void*)fn, bytes);
     if (rc != FUSEDCONV_OK) return;
-    const unsigned queries = xcd_grid((int64_t)p.batch * p.heads * k.q_tiles);
+    const unsigned queries = xcd_grid((int64_t)p.batch * p.heads * k.q_splits * k.q_tiles);
     hipLaunchKernelGGL(fn, dim3(k.key_blocks + queries), dim3(256), bytes, st, k);
+    const int64_t key_items = k.k_splits > 1 ? 2 * (int64_t)p.batch * p.kv_heads * p.sk * p.d / 8 : 0;
+    const int64_t items =
+        key_items + (k.q_splits > 1 ? (int64_t)p.batch * p.heads * p.sq * p.d / 8 : 0);
+    if (items > 0)
+      hipLaunchKernelGGL((k_attention_sums<T>), dim3((unsigned)((items + 255) / 256)), dim3(256), 0,
+                         st, k, (uint32_t)key_items, (uint32_t)items);
   });
   if (rc != FUSEDCONV_OK) return rc;
   return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH;
@@ -361,6 +449,44 @@ int FC_DP_NAME(attention_backward_)(const AttnPlan& plan, const AttnBwdK& k, hip
 int attention_backward_64(const AttnPlan&, const AttnBwdK&, hipStream_t);
 int attention_backward_96(const AttnPlan&, const AttnBwdK&, hipStream_t);
 int attention_backward_128(const AttnPlan&, const AttnBwdK&, hipStream_t);
+
+// A tile's walk is shared by several blocks where one block would work for more
+// than twice the time that all of them take on a full chip (a tile counts four
+// products in a key block, three in a query block), in as many shares as that
+// time goes into it, rounded down, so that no few blocks are left for a second
+// round (one head of 8192 x 8192, 128, bf16: 138 us, rounded up 172).  Shares
+// have at least 4 float32 tiles or 32 16-bit ones, less is lost to the partial
+// gradients (2 x 1024 queries, 8 heads of 64, f16: 31 us whole, 40 in shares of
+// 16).  64 queries on 32768 keys, 8 / 2 heads of 128, bf16: 990 us whole, 67
+// shared; 3669 on 192, 28 / 14 of 112, f32: 1706 and 385; 4096 causal ones, 16 / 4
+// of 128, bf16: 578 and 291.
+void plan_attention_backward(const AttnParams& p, AttnPlan& plan) {
+  const bool wide = plan.dtype == FUSEDCONV_F32;
+  // what a block of 128 sees at most
+  const auto span = [&](int64_t len, int64_t other, int32_t limit) {
+    if (p.left >= 0 && p.right >= 0) len = std::min<int64_t>(len, (int64_t)p.left + p.right + 128);
+    return limit >= 0 ? std::min<int64_t>(len, other + limit) : len;
+  };
+  const int64_t k_tiles = (span(p.sq, p.sk, p.right) + 31) / 32 * p.group;
+  const int64_t q_tiles = (span(p.sk, p.sq, p.left) + 31) / 32;
+  const int64_t key_blocks = (int64_t)p.batch * p.kv_heads * ((p.sk + 127) / 128);
+  const int64_t query_blocks = (int64_t)p.batch * p.heads * ((p.sq + 127) / 128);
+  int64_t work = key_blocks * k_tiles * 4 + query_blocks * q_tiles * 3;
+  if ((p.left < 0) != (p.right < 0)) work /= 2;
+  const int64_t full = std::max<int64_t>(work / (wide ? 256 : 512), 1);
+  const auto splits = [&](int64_t blocks, int64_t tiles, int64_t cost) {
+    if (blocks > 512 || cost <= 2 * full) return 1;
+    const int64_t most = std::min<int64_t>(tiles / (wide ? 4 : 32), 64);
+    return (int)std::max<int64_t>(std::min(cost / full, most), 1);
+  };
+  plan.k_splits = splits(key_blocks, k_tiles, k_tiles * 4);
+  plan.q_splits = splits(query_blocks, q_tiles, q_tiles * 3);
+  // -lse and -rowsum(do * o), rows padded to whole tiles; the partial gradients
+  size_t floats = (size_t)p.batch * p.heads * ((p.sq + 63) / 64 * 64) * 2;
+  if (plan.k_splits > 1) floats += 2 * (size_t)plan.k_splits * p.batch * p.kv_heads * p.sk * p.d;
+  if (plan.q_splits > 1) floats += (size_t)plan.q_splits * p.batch * p.heads * p.sq * p.d;
+  plan.backward_bytes = floats * sizeof(float);
+}
 
 int launch_attention_backward(const AttnParams& p, const AttnPlan& plan, const AttnArgs& a) {
   AttnBwdK k{};
@@ -375,7 +501,11 @@ int launch_attention_backward(const AttnParams& p, const AttnPlan& plan, const A
   k.c = fmaxf(fabsf(p.scale) * (plan.dtype == FUSEDCONV_F32 ? 1.0f : kLog2e), kLeastC);
   k.q_tiles = (p.sq + 127) / 128;
   k.k_tiles = (p.sk + 127) / 128;
-  k.key_blocks = (int32_t)xcd_grid((int64_t)p.batch * p.kv_heads * k.k_tiles);
+  k.k_splits = plan.k_splits;
+  k.q_splits = plan.q_splits;
+  k.part_k = k.ndelta + (size_t)p.batch * p.heads * k.padded;
+  k.part_q = k.part_k + (k.k_splits > 1 ? 2 * (size_t)k.k_splits * p.batch * p.kv_heads * p.sk * p.d : 0);
+  k.key_blocks = (int32_t)xcd_grid((int64_t)p.batch * p.kv_heads * k.k_splits * k.k_tiles);
   const hipStream_t st = (hipStream_t)a.stream;
   switch (plan.dp) {
     case 32: return attention_backward_32(plan, k, st);

@@ -535,8 +535,7 @@ void plan_attention(const AttnParams& p, AttnPlan& plan) {
     plan.splits = (int)splits;
     plan.forward_bytes = (size_t)p.batch * p.heads * splits * p.sq * (p.d + 4) * sizeof(float);
   }
-  // -lse and -rowsum(do * o), rows padded to whole tiles
-  plan.backward_bytes = (size_t)p.batch * p.heads * ((p.sq + 63) / 64 * 64) * 2 * sizeof(float);
+  plan_attention_backward(p, plan);
 }
 
 int launch_attention_forward(const AttnParams& p, const AttnPlan& plan, const AttnArgs& a) {

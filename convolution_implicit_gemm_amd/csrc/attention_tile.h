@@ -375,6 +375,10 @@ struct Sight {
     return left < 0 ? nq : min(nq, j + left - nk + nq + 1);
   }
 };
+// The first of n tiles that block `split` of `splits` takes.
+__device__ __forceinline__ int share(int n, int split, int splits) {
+  return (int)((int64_t)n * split / splits);
+}
 __device__ __forceinline__ int length_of(const int32_t* lengths, int b, int most) {
   return lengths ? min(max(lengths[b], 0), most) : most;
 }

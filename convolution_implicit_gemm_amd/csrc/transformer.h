@@ -56,6 +56,7 @@ struct AttnPlan {
   int32_t few;          // few query rows: the key axis is split over a block's waves too
   int32_t splits;       // blocks of one (entry, head, row tile) along the keys
   int32_t few_waves, few_stages;  // few: waves of a block, tile buffers of a wave
+  int32_t k_splits, q_splits;  // backward: blocks that share a tile's queries, its keys
   size_t forward_bytes, backward_bytes;
 };
 struct AttnArgs {

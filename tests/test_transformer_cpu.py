@@ -193,6 +193,21 @@ def test_plans_by_size():
     assert plan(100, 64, 2, 2).backward_bytes == 2 * 128 * 2 * 4
 
 
+def test_backward_plans_by_size():
+    """Few key blocks with long walks, or few query blocks, keep partial gradients in the workspace."""
+    def parts(sq, sk, h, hk, b=1, dtype=1):
+        q, k = (sq * h * 64, h * 64, 64), (sk * hk * 64, hk * 64, 64)
+        op = fc.Attention(dtype, b, sq, sk, h, hk, 64, 0.1, -1, -1, q, k, k, q, q, q, k, k)
+        return op.backward_bytes - 2 * 4 * b * h * ((sq + 63) // 64 * 64)
+    assert parts(4096, 4096, 16, 16) == 0
+    assert parts(577, 577, 16, 16, b=32) == 0
+    one = 2 * 128 * 2 * 64 * 4                      # dk and dv of one share
+    assert parts(1 << 15, 128, 2, 2) % one == 0 and parts(1 << 15, 128, 2, 2) // one > 8
+    one = 64 * 2 * 64 * 4                           # dq of one share
+    assert parts(64, 1 << 15, 2, 2) % one == 0 and parts(64, 1 << 15, 2, 2) // one > 8
+    assert 0 < parts(1 << 20, 1, 1, 1, dtype=0) <= 64 * 2 * 64 * 4
+
+
 def test_oracle_gradients_against_differences():
     g = torch.Generator().manual_seed(0)
     new = lambda *s: torch.randn(s, generator=g, dtype=torch.float64)  # noqa: E731

@@ -264,6 +264,35 @@ def test_attention_backward(b, sq, sk, h, hk, d, window, lengths, dtype):
         assert torch.equal(got[n], again[n]), f"{name} differs from call to call"
 
 
+SHARED = [  # few blocks with long walks: their tiles are shared by several blocks, whose gradients are summed
+    (1, 2100, 100, 4, 2, 64, (-1, -1), None), (1, 1500, 40, 6, 1, 128, (-1, -1), None),
+    (2, 1100, 130, 2, 2, 40, (-1, -1), ([1100, 700], [130, 33])), (1, 1290, 1290, 2, 1, 72, (-1, 0), None),
+    (3, 1025, 70, 2, 1, 120, (-1, 40), ([1025, 0, 31], [70, 70, 1])), (1, 60, 2500, 2, 1, 32, (-1, 0), None),
+    (1, 1400, 1400, 1, 1, 96, (-1, 800), None), (1, 1200, 1800, 1, 1, 8, (700, -1), None),
+]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("b,sq,sk,h,hk,d,window,lengths", SHARED)
+def test_attention_backward_shared(b, sq, sk, h, hk, d, window, lengths, dtype):
+    test_attention_backward(b, sq, sk, h, hk, d, window, lengths, dtype)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_attention_backward_shared_out(dtype):
+    """Shared tiles into a packed gradient: the bits of separate ones; the rest of it unchanged."""
+    q, k, v, _, _ = attention_case(2, 1100, 1100, 2, 2, 64, dtype, 90)
+    q, k, v, do = (dev(x) for x in (q, k, v, randn(91, 2, 1100, 2, 64, dtype=TYPES[dtype])))
+    o, lse = fc.attention(q, k, v, causal=True, lse=True)
+    want = fc.attention_backward(do, q, k, v, o, lse, causal=True)
+    grads = torch.full((2, 1100, 4, 2, 64), 7.0, device="cuda", dtype=TYPES[dtype])
+    fc.attention_backward(do, q, k, v, o, lse, causal=True, out=grads.unbind(2)[:3])
+    torch.cuda.synchronize()
+    for n in range(3):
+        assert torch.equal(grads[:, :, n], want[n])
+    assert (grads[:, :, 3] == 7).all()
+
+
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 2.5])
 def test_attention_scales(scale):
     q, k, v, _, _ = attention_case(1, 70, 70, 2, 1, 64, "f32", 70)
