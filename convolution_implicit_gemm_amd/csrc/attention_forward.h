@@ -11,6 +11,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attention_tile.h"
@@ -511,19 +512,30 @@ void plan_attention(const AttnParams& p, AttnPlan& plan) {
   plan.few = rows <= 32 || p.sq <= 16 || (wide && plan.dp <= 64 && units <= 256 && p.sk <= 512);
   plan.splits = 1;
   plan.forward_bytes = 0;
+  // keys that a block's queries see at most
+  int64_t reach = p.left >= 0 ? std::min<int64_t>(p.sk, (int64_t)p.sq + p.left) : p.sk;
+  if (p.left >= 0 && p.right >= 0)
+    reach = std::min<int64_t>(reach, std::min(p.sq, 128) + (int64_t)p.left + p.right);
   int64_t splits = 1, most;  // most: splits that still have enough keys each
   if (plan.few) {
     // 512 blocks, two tiles a wave at least
     if (units > 0) splits = (512 + units - 1) / units;
-    most = p.sk / 256;
+    most = reach / 256;
   } else {
     // Where at most half the compute units had a block.  The partial results'
     // way through memory costs about ten 16-bit tiles (128 blocks of 16 tiles,
     // heads of 128: 19 us whole, 25 in two; of 64 tiles: 55 us whole, 40 in
     // four), three float32 ones (4 x 512 queries, 8 heads of 64: 43 and 33 us).
+    // 16-bit: also where a compute unit, which has room for two, had one block, or
+    // where a causal window leaves them uneven and there is hardly a second one,
+    // but with 64 tiles at least (4096 queries, heads of 128: 8 heads 103 us
+    // whole, 88 in two; 12 causal ones 119 and 95; 2048 causal queries, 12 heads:
+    // 54 and 39 in three; 1024 queries, 24 heads, 32 tiles: 30 and 37 in two).
     const int64_t blocks = (int64_t)p.batch * p.heads * ((p.sq + 127) / 128);
-    if (blocks > 0 && blocks <= 128) splits = ((wide ? 256 : 512) + blocks - 1) / blocks;
-    most = p.sk / (32 * (wide ? 4 : 16));
+    const bool half = blocks <= 128, uneven = p.left < 0 && p.right >= 0;
+    if (blocks > 0 && (half || (!wide && reach >= 2048 && blocks <= (uneven ? 384 : 256))))
+      splits = ((wide ? 256 : 512) + blocks - 1) / blocks;
+    most = reach / (32 * (wide ? 4 : 16));
   }
   splits = splits > most ? most : splits;
   // four waves where two buffers each fit in LDS, no more than there are tiles

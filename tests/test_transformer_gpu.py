@@ -264,6 +264,19 @@ def test_attention_backward(b, sq, sk, h, hk, d, window, lengths, dtype):
         assert torch.equal(got[n], again[n]), f"{name} differs from call to call"
 
 
+UNEVEN = [  # many blocks, long keys: two or three shares of the keys; windows that leave few of them
+    (1, 700, 2100, 24, 24, 16, (-1, -1), None), (1, 700, 2100, 48, 12, 8, (-1, 0), None),
+    (3, 257, 2050, 20, 4, 40, (-1, 0), ([257, 3, 130], [2050, 2049, 40])), (1, 300, 4100, 4, 2, 64, (200, 0), None),
+    (2, 1, 3000, 8, 2, 64, (256, 0), ([1, 1], [3000, 100])), (1, 3, 3000, 2, 1, 96, (900, 5), None),
+]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("b,sq,sk,h,hk,d,window,lengths", UNEVEN)
+def test_attention_uneven(b, sq, sk, h, hk, d, window, lengths, dtype):
+    test_attention(b, sq, sk, h, hk, d, window, lengths, dtype)
+
+
 SHARED = [  # few blocks with long walks: their tiles are shared by several blocks, whose gradients are summed
     (1, 2100, 100, 4, 2, 64, (-1, -1), None), (1, 1500, 40, 6, 1, 128, (-1, -1), None),
     (2, 1100, 130, 2, 2, 40, (-1, -1), ([1100, 700], [130, 33])), (1, 1290, 1290, 2, 1, 72, (-1, 0), None),
