@@ -329,7 +329,7 @@ __global__ __launch_bounds__(kLoopThreads) void k_norm_columns(NormK a) {
 // A block has a tile of PL * V consecutive pixels of one image, all channels:
 // lane p of PL holds V pixels, channel group g of CG the channels g, g + CG,
 // ... (NCH of them).  A wave's accesses are 64 / PL channels of PL * V *
-// sizeof(T) bytes (128 or more for the vector forms) each.
+// sizeof(T) bytes (128 or more, with four lanes 64) each.
 
 constexpr int kPlaneThreads = 256;
 constexpr int kPlaneWaves = kPlaneThreads / 64;
@@ -757,6 +757,12 @@ NormPlan plan_norm(const NormProblem& p, bool backward) {
   while (q.tpr > 8 && (p.c * q.tpr > 16 * kPlaneThreads || q.tpr / 2 * wide >= p.inner ||
                        p.n * ceil_div(p.inner, (int64_t)q.tpr * wide) < 512))
     q.tpr /= 2;
+  // Four lanes' runs are half a line; they take as much memory time as eight only
+  // where the chip is not full anyway (8 x 384 channels of 14 x 14, f16, backward:
+  // 23 us with eight, 15 with four; 18 x 709, forward: 22 and 13; but 256 x 768,
+  // forward: 69 and 74), and are better than the second reading of the looped form
+  // (256 x 768 of 14 x 14, backward: 181 us looped, 118 with four).
+  if (q.tpr == 8 && (p.n * ceil_div(p.inner, 8 * wide) < 256 || (backward && p.c > 512))) q.tpr = 4;
   const int cg = kPlaneThreads / q.tpr;
   q.nch = 2;
   while (q.nch * cg < p.c && q.nch <= 32) q.nch = q.nch < 4 ? 4 : q.nch < 16 ? q.nch + 4 : q.nch + 8;
@@ -820,7 +826,8 @@ void with_planes(const NormPlan& q, F&& f) {
     }
   };
   auto lanes = [&](auto v) {
-    if (q.tpr == 8) pick(v, int_c<8>{});
+    if (q.tpr == 4) pick(v, int_c<4>{});
+    else if (q.tpr == 8) pick(v, int_c<8>{});
     else if (q.tpr == 16) pick(v, int_c<16>{});
     else pick(v, int_c<32>{});
   };

@@ -41,14 +41,16 @@ __device__ __forceinline__ void stay_packed(Piece<T, V>& p) {
   }
 }
 
-// v plus the value of the lane OFF away (lane ^ OFF), without LDS.  OFF = 4 and
-// 8 read a mirrored lane: the same value once the offsets below have been
-// added, so sums over 8 or more lanes add 1, 2, 4, ... in this order.
-template <int OFF>
+// v plus the value of the lane OFF away (lane ^ OFF), without LDS.  OFF = 4 reads
+// the mirrored lane (lane ^ 7), which has the same value once the offsets 1 and 2
+// have been added; where they have not (FIRST), the quads are mirrored as well.
+template <int OFF, bool FIRST>
 __device__ __forceinline__ float add_lane(float v) {
   if constexpr (OFF <= 8) {
     constexpr int ctrl = OFF == 1 ? 0xB1 : OFF == 2 ? 0x4E : OFF == 4 ? 0x141 : 0x128;
-    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
+    int other = __builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true);
+    if constexpr (OFF == 4 && FIRST) other = __builtin_amdgcn_update_dpp(0, other, 0x1B, 0xf, 0xf, true);
+    return v + __int_as_float(other);
   } else if constexpr (OFF == 16) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
@@ -58,9 +60,9 @@ __device__ __forceinline__ float add_lane(float v) {
   }
 }
 // Sum over the lanes that differ in the bits FROM, 2 * FROM, ... below TO.
-template <int FROM, int TO>
+template <int FROM, int TO, bool FIRST = true>
 __device__ __forceinline__ float lane_sum(float v) {
-  if constexpr (FROM < TO) return lane_sum<2 * FROM, TO>(add_lane<FROM>(v));
+  if constexpr (FROM < TO) return lane_sum<2 * FROM, TO, false>(add_lane<FROM, FIRST>(v));
   else return v;
 }
 

@@ -80,6 +80,20 @@ def test_layer_norm_backward(shape, axis, dtype):
         assert torch.equal(g, a), f"{name} differs from call to call"
 
 
+
+PLANES = [  # many channels, few and many tiles, short and odd planes; channels that no block holds
+    (2, 700, 5, 9), (300, 640, 3, 3), (2, 1024, 16, 16), (1, 513, 31, 33), (1, 1500, 4, 4), (1, 2100, 3, 5),
+    (3, 40, 6, 6), (70, 513, 20, 20), (1, 257, 2, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", PLANES)
+def test_layer_norm_planes(shape, dtype):
+    test_layer_norm(shape, 1, dtype)
+    test_layer_norm_backward(shape, 1, dtype)
+
+
 @pytest.mark.parametrize("axis", [-1, 1])
 def test_layer_norm_options(axis):
     """Without parameters, with one of the gradients only, views at a stride, no rows."""
