@@ -191,7 +191,7 @@ def test_plans_by_size():
     assert one.forward_bytes == 2 * 128 * 4 * (64 + 4) * 4  # 128 splits of 256 keys, four rows a key head
     assert plan(4096, 4096, 16, 16).forward_bytes == 0
     assert plan(4096, 4096, 8, 8).forward_bytes > 0  # one block to a compute unit, causal
-    assert plan(1024, 1024, 8, 8, b=3).forward_bytes == 0
+    assert plan(1024, 1024, 24, 24).forward_bytes == 0
     assert plan(100, 64, 2, 2).backward_bytes == 2 * 128 * 2 * 4
 
 
