@@ -78,7 +78,7 @@ bool strides_ok(const int64_t s[3], int64_t batch, int64_t len, int64_t heads, i
   const int64_t size[3] = {batch, len, heads};
   for (int i = 0; i < 3; ++i) {
     if (size[i] <= 1) continue;
-    if (s[i] < 0 || s[i] * esize % 16 != 0) return false;
+    if (s[i] < 0 || s[i] % (16 / esize) != 0) return false;  // their bytes may pass 64 bits
     if (s[i] > kMaxElements / size[i]) return false;
   }
   return len <= 1 || s[1] * esize <= (int64_t(1) << 31) / 256 - 1;
@@ -205,9 +205,9 @@ int fusedconv_rotary_create(const fusedconv_rotary_desc* d, fusedconv_rotary** o
   if (d->batch < 0 || d->len < 0 || d->heads < 1 || d->kv_heads < 0)
     return fail(FUSEDCONV_ERR_OUTPUT_SHAPE, "batch, len, kv_heads must be >= 0, heads >= 1");
   const int64_t es = elem_size(d->dtype);
-  if (d->head_dim < 1 || d->head_dim * es % 16 != 0)
+  if (d->head_dim < 1 || d->head_dim % (16 / es) != 0)
     return fail(FUSEDCONV_ERR_OUTPUT_SHAPE, "a head must be whole 16-byte pieces");
-  if (d->pairs < 1 || 2 * d->pairs > d->head_dim)
+  if (d->pairs < 1 || d->pairs > d->head_dim / 2)
     return fail(FUSEDCONV_ERR_ATTR_VALUE, "pairs must be in [1, head_dim / 2]");
   if (d->num_axes < 1 || d->num_axes > 8)
     return fail(FUSEDCONV_ERR_ATTR_VALUE, "num_axes must be in [1, 8]");
