@@ -28,6 +28,7 @@ struct NormK {
   int64_t x_stride, dy_stride;
   int32_t n, c, inner;
   int32_t tiles;  // NCHW: pixel tiles of one image
+  int32_t in_place;  // NCHW, forward: out is x
   float eps;
 };
 
@@ -389,6 +390,9 @@ __device__ __forceinline__ void pixel_sum(float (&v)[K][V]) {
 // own channels and the squares about that; the parts' squares about the common
 // mean follow from the distances of the means (exact, nothing cancels).
 // NCH: channels a thread holds; 0: any number, read again for each pass.
+// In place a moved-back piece may find its first `shift` pixels, which another
+// thread, or another block, owns, already overwritten.  No pixel's values meet
+// another's, so it only has to keep what came of them: it stores its own pixels.
 template <typename T, bool WHOLE, int PL, int NCH>
 __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
   constexpr int V = 16 / sizeof(T);
@@ -399,7 +403,9 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
   const int image = tile / a.tiles;
   const int piece = (tile - image * a.tiles) * PL + p;
   const bool live = piece * V < a.inner;
-  const int pixel = place_of<WHOLE, V>(piece, a.inner).at, left = a.inner - pixel;
+  const auto [pixel, shift] = place_of<WHOLE, V>(piece, a.inner);
+  const int left = a.inner - pixel;
+  const int kept = WHOLE || !a.in_place ? 0 : shift;  // pixels that are another thread's to store
   const T* x = (const T*)a.x + (int64_t)image * a.x_stride;
   T* y = (T*)a.out + (int64_t)image * a.c * a.inner;
   const uint32_t off = (uint32_t)(g * a.inner + pixel) * sizeof(T);
@@ -482,7 +488,7 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
     const int64_t at = (int64_t)image * a.inner + pixel;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (WHOLE || j < left) {
+      if (WHOLE || (j >= shift && j < left)) {
         a.mean[at + j] = mean[j];
         a.rstd[at + j] = rstd[j];
       }
@@ -502,7 +508,11 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes(NormK a) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
       py.v[j] = to_type<T>(((float)px[k].v[j] - mean[j]) * rstd[j] * wc + bc);
-    store_at<WHOLE>(y, i * step, off, py, left);
+    if (WHOLE || kept == 0) store_at<WHOLE>(y, i * step, off, py, left);
+    else
+#pragma unroll
+      for (int j = 1; j < V; ++j)
+        if (j >= kept) *((T*)((char*)(y + i * step) + off) + j) = py.v[j];
   });
 }
 
@@ -784,6 +794,7 @@ NormK kernel_args(const NormProblem& p, const NormArgs& a, const NormPlan& q) {
   k.x_stride = p.x_stride; k.dy_stride = p.dy_stride;
   k.n = (int32_t)p.n; k.c = (int32_t)p.c; k.inner = (int32_t)p.inner;
   k.tiles = q.tiles;
+  k.in_place = a.in_place;
   k.eps = p.eps;
   return k;
 }

@@ -103,6 +103,15 @@ bool apart(const int64_t s[3], int64_t batch, int64_t len, int64_t heads, int64_
   return true;
 }
 
+// Whether any of n rows of `row` bytes, `step` bytes apart from a, lies in the
+// `bytes` bytes from b on.
+bool rows_meet(const void* a, int64_t n, int64_t row, int64_t step, const void* b, int64_t bytes) {
+  const int64_t to_b = (int64_t)((intptr_t)b - (intptr_t)a);  // from the first row to b
+  // the first row that ends behind b's start
+  const int64_t i = to_b < row ? 0 : (to_b - row) / step + 1;
+  return i < n && i * step < to_b + bytes;
+}
+
 fc::Strides3 strides_of(const int64_t s[3], int64_t batch, int64_t len, int64_t heads) {
   return {batch > 1 ? s[0] : 0, len > 1 ? s[1] : 0, heads > 1 ? s[2] : 0};
 }
@@ -160,10 +169,15 @@ int fusedconv_layer_norm_forward(const fusedconv_layer_norm* h, const void* x, c
   if (!aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned16(bias) ||
       !aligned16(mean) || !aligned16(rstd))
     return fail(FUSEDCONV_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+  const int64_t es = elem_size(h->p.dtype), row = h->p.c * h->p.inner * es;
+  const bool in_place = x == y && h->p.x_stride * es == row;
+  if (!in_place && rows_meet(x, h->p.n, row, h->p.x_stride * es, y, h->p.n * row))
+    return fail(FUSEDCONV_ERR_ATTR_VALUE, "y is x, both contiguous, or overlaps it nowhere");
   const int rc = ready(stream);
   if (rc != FUSEDCONV_OK) return rc;
   fc::NormArgs a{};
   a.x = x; a.w = weight; a.b = bias; a.out = y; a.mean = mean; a.rstd = rstd; a.stream = stream;
+  a.in_place = in_place;
   return launched(fc::launch_norm_forward(h->p, a));
 }
 
@@ -183,6 +197,10 @@ int fusedconv_layer_norm_backward(const fusedconv_layer_norm* h, const void* dy,
   if (h->workspace > 0 && (dweight || dbias) && (!workspace || workspace_bytes < h->workspace))
     return fail(FUSEDCONV_ERR_WORKSPACE,
                 "workspace smaller than fusedconv_layer_norm_workspace_size() reports");
+  const int64_t es = elem_size(h->p.dtype), row = h->p.c * h->p.inner * es;
+  if (h->p.n > 0 && (rows_meet(x, h->p.n, row, h->p.x_stride * es, dx, h->p.n * row) ||
+                     rows_meet(dy, h->p.n, row, h->p.dy_stride * es, dx, h->p.n * row)))
+    return fail(FUSEDCONV_ERR_ATTR_VALUE, "dx must not overlap x or dy");
   const int rc = ready(stream);
   if (rc != FUSEDCONV_OK) return rc;
   fc::NormArgs a{};

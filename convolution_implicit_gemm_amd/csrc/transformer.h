@@ -23,6 +23,7 @@ struct NormArgs {
   float *dw, *db;     // float [c]
   float* part;        // workspace: [blocks][2][c]
   void* stream;
+  bool in_place;      // forward: out is x
 };
 size_t norm_workspace(const NormProblem& p);
 int launch_norm_forward(const NormProblem& p, const NormArgs& a);

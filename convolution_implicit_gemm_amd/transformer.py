@@ -329,7 +329,8 @@ def layer_norm(x, weight=None, bias=None, *, axis=-1, eps=1e-5, stats=False, out
     """y = (x - mean) * rstd * weight + bias over `axis` (-1: token rows, 1: the channels of an
     NCHW tensor); (y, mean, rstd) with stats=True, the statistics in float32 with x's shape
     without `axis`, as layer_norm_backward takes them.  weight and bias: [c], x's dtype.  x may
-    be a view whose rows (images) lie at one stride."""
+    be a view whose rows (images) lie at one stride.  out: where to write, contiguous; x itself is
+    allowed, tensors that overlap x otherwise are not."""
     if torch is None:
         _setup()
     eps = float(eps)

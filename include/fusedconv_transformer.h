@@ -35,7 +35,9 @@ extern "C" {
  * with the biased variance taken about the mean.  inner = 1: n token rows of c
  * values.  inner > 1: NCHW images, inner = H * W, as the convolutions write
  * them.  x_stride / dy_stride: elements from one n to the next (>= c * inner);
- * within an n the values are contiguous.  Y and DX are contiguous.
+ * within an n the values are contiguous.  Y and DX are contiguous.  Y may be X
+ * itself (same pointer, X contiguous); any other overlap of Y with X, and one of
+ * DX with X or DY, is refused (FUSEDCONV_ERR_ATTR_VALUE).
  *
  * Backward, with g = dy * weight, xh = (x - mean) * rstd:
  *     dx = rstd * (g - mean_c(g) - xh * mean_c(g * xh))
