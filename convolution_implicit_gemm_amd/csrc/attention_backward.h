@@ -41,7 +41,8 @@ namespace {
 
 // 16-bit T: the products q k^T and do v^T start from -lse, in units of the raw
 // scores, and from -rowsum(do * o), so that the probability is exp2(c * sum) and
-// ds is p times the other sum, with no further operation.  float32: they start
+// ds is p times the other sum, with no further operation.  f16: from up - lse, so
+// that both come 2^up times (kBackwardUp).  float32: they start
 // from zero and the two are added afterwards, which keeps the sums' rounding
 // small (a score next to its lse loses the lse's digits otherwise).
 constexpr bool starts_from_rows(int size) { return size == 2; }
@@ -51,6 +52,44 @@ __device__ __forceinline__ float probability(float sum, float c, float nlse) {
   if constexpr (starts_from_rows(sizeof(T))) return __builtin_amdgcn_exp2f(sum * c);
   else return __builtin_amdgcn_exp2f(fmaf(sum, c, nlse) * kLog2e);
 }
+
+// f16: 2^up ds may pass 65504 where do v^T is large.  A wave then takes its ds
+// down by a power of two, for good, and what it has summed of them with it, as
+// the running maximum of a softmax does: gradients of any size keep their bits.
+// The comparisons of every tile cost 3 to 4 % (2 x 4096 causal queries, 32 / 8 heads
+// of 128, f16: 968 us without, 997 with them).  A bound on ds from the norms of do
+// and v would need none, but lies 2^7 above the usual ds, and its factor would
+// be another product a value.
+struct Down {
+  float by = 1.f;           // the same in all lanes
+  float limit = 32768.f;    // what may pass unchanged; below zero once `by` is less than 1
+  // The tile's ds, and the sums of the products with them.
+  template <int NT>
+  __device__ __forceinline__ void operator()(f32x16& ds, f32x16 (&sums)[NT]) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(ds[i]));
+    if (!__any(most > limit)) return;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ds[i] *= by;
+    // infinite inputs keep their infinite results
+    most = most < INFINITY ? most * by : 0.f;
+    if (!__any(most > 32768.f)) return;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+    const int top = __builtin_amdgcn_readfirstlane(__float_as_int(most)) >> 23;  // exponent + 127
+    // 2^-n with 2^-n * most in [2^13, 2^14): a while until the next time
+    const float down = __int_as_float((127 + 13 + 127 - top) << 23);
+    by = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(by * down)));
+    limit = -1.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ds[i] *= down;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sums[t][i] *= down;
+  }
+};
 
 // What those start from: nlse and ndelta = -rowsum(do * o).
 // Rows without a key, behind the entry's queries or in the padding get nlse =
@@ -80,7 +119,9 @@ __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
 #pragma unroll
   for (int off = 1; off < 8; off <<= 1) s += __shfl_xor(s, off, 64);
   if ((threadIdx.x & 7) == 0) {
-    a.nlse[at] = l == -INFINITY ? l : starts_from_rows(sizeof(T)) ? -l * kLog2e / a.c : -l;
+    a.nlse[at] = l == -INFINITY                  ? l
+                 : starts_from_rows(sizeof(T)) ? ((float)kBackwardUp<T> - l * kLog2e) / a.c
+                                               : -l;
     a.ndelta[at] = l == -INFINITY ? 0.f : -s;
   }
 }
@@ -146,6 +187,7 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
   }
 
   f32x16 dk[NT], dv[NT];
+  Down down;
 #pragma unroll
   for (int t = 0; t < NT; ++t) dk[t] = dv[t] = zero16();
 
@@ -213,6 +255,7 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
         s[i] = probability<T>(s[i], a.c, kFromRows ? 0.f : rt[c_row(i, h)]);
         dp[i] = (kFromRows ? dp[i] : dp[i] + rt[32 + c_row(i, h)]) * s[i];
       }
+      if constexpr (kBackwardUp<T> > 0) down(dp, dk);
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         const frag_t<T> pf = to_frag<T>(s, d), df = to_frag<T>(dp, d);
@@ -227,15 +270,17 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
   }
   if (j >= p.sk) return;
   const bool keep = j < see.nk;
+  constexpr float kBack = 1.f / (1 << kBackwardUp<T>);
+  const float back = p.scale * (kBack / down.by);
   if (a.k_splits > 1) {
     const int64_t one = (int64_t)p.batch * p.kv_heads * p.sk * p.d;
     float* pk = a.part_k + 2 * split * one + (((int64_t)b * p.kv_heads + kvh) * p.sk + j) * p.d;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       store_row<float>(pk + 32 * t, dk[t], p.d - 32 * t, h,
-                       [&](float v) { return keep ? v * p.scale : 0.f; });
+                       [&](float v) { return keep ? v * back : 0.f; });
       store_row<float>(pk + one + 32 * t, dv[t], p.d - 32 * t, h,
-                       [&](float v) { return keep ? v : 0.f; });
+                       [&](float v) { return keep ? v * kBack : 0.f; });
     }
     return;
   }
@@ -244,8 +289,8 @@ __device__ __forceinline__ void keys_block(const AttnBwdK& a, int block) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     store_row<T>(dkp + 32 * t, dk[t], p.d - 32 * t, h,
-                 [&](float v) { return keep ? v * p.scale : 0.f; });
-    store_row<T>(dvp + 32 * t, dv[t], p.d - 32 * t, h, [&](float v) { return keep ? v : 0.f; });
+                 [&](float v) { return keep ? v * back : 0.f; });
+    store_row<T>(dvp + 32 * t, dv[t], p.d - 32 * t, h, [&](float v) { return keep ? v * kBack : 0.f; });
   }
 }
 
@@ -291,6 +336,7 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
   const uint32_t many = max(see.hi(i) - lo, 0);
 
   f32x16 dq[NT];
+  Down down;
 #pragma unroll
   for (int t = 0; t < NT; ++t) dq[t] = zero16();
   L::template clear_padding<4 * 32>(tiles, p.d, threadIdx.x, 256);
@@ -337,6 +383,7 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         dp[e] = (kFromRows ? dp[e] : dp[e] + ndelta) * probability<T>(s[e], a.c, nlse);
+      if constexpr (kBackwardUp<T> > 0) down(dp, dq);
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         const frag_t<T> df = to_frag<T>(dp, d);
@@ -347,19 +394,20 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
     walk_tiles(count, start, operands, use);
   }
   if (i >= p.sq) return;
+  const float back = p.scale * (1.f / (1 << kBackwardUp<T>) / down.by);
   if (a.q_splits > 1) {
     const int64_t row = (((int64_t)split * p.batch + b) * p.heads + head) * p.sq + i;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
       store_row<float>(a.part_q + row * p.d + 32 * t, dq[t], p.d - 32 * t, h,
-                       [&](float v) { return i < see.nq ? v * p.scale : 0.f; });
+                       [&](float v) { return i < see.nq ? v * back : 0.f; });
     return;
   }
   T* out = (T*)a.dq + b * p.dq.b + i * p.dq.s + head * p.dq.h;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
     store_row<T>(out + 32 * t, dq[t], p.d - 32 * t, h,
-                 [&](float v) { return i < see.nq ? v * p.scale : 0.f; });
+                 [&](float v) { return i < see.nq ? v * back : 0.f; });
 }
 
 // Bound by the matrix cores at the clock that the chip's power allows under

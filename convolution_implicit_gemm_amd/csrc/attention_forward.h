@@ -54,10 +54,11 @@ struct Running {
 };
 
 // One block of 32 * KB keys: scores s (masked entries -inf) -> probabilities in
-// s, state updated.  The reference m follows the maximum only when that exceeds
-// it by 8 octaves, or is the first: factors up to 2^8 are exact in every T, the
-// sums are fp32, and the output is rescaled a few times instead of every tile.
-template <int KB, int NT>
+// s, 2^UP times, state updated.  The reference m follows the maximum only when
+// that exceeds it by 8 octaves, or is the first: factors up to 2^(8 + UP) fit
+// every T, the sums are fp32, and the output is rescaled a few times instead of
+// every tile.
+template <int UP, int KB, int NT>
 __device__ __forceinline__ void softmax_step(f32x16 (&s)[KB], Running<NT>& st, float c) {
   float mx = s[0][0];
 #pragma unroll
@@ -75,7 +76,7 @@ __device__ __forceinline__ void softmax_step(f32x16 (&s)[KB], Running<NT>& st, f
 #pragma unroll
       for (int i = 0; i < 16; ++i) st.o[t][i] *= a;
   }
-  const float mc = st.m == -INFINITY ? 0.f : st.m * c;
+  const float mc = (st.m == -INFINITY ? 0.f : st.m * c) - (float)UP;
   float l = 0.f;
 #pragma unroll
   for (int k = 0; k < KB; ++k)
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
       f32x16 s[1] = {zero16()};
       each_step<NS>(p.d, [&](auto d) { s[0] = mma(L::load_rows(kt, 0, d), q[d], s[0]); });
       if (key0 < all_lo || key0 + 32 > all_hi) mask_keys(s, key0, lo, hi, h);
-      softmax_step(s, st, a.c);
+      softmax_step<kForwardUp<T>>(s, st, a.c);
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         const frag_t<T> pf = to_frag<T>(s[0], d);
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
     for (int t = 0; t < NT; ++t)
       store_row<float>(a.part_o + part * p.d + 32 * t, st.o[t], p.d - 32 * t, h,
                        [&](float v) { return v * inv; });
-    if (h == 0) a.part_lse[part] = l == 0.f ? -INFINITY : st.m * a.c + log2f(l);
+    if (h == 0) a.part_lse[part] = l == 0.f ? -INFINITY : st.m * a.c + (log2f(l) - kForwardUp<T>);
     return;
   }
   T* o = (T*)a.o + b * p.o.b + i * p.o.s + head * p.o.h;
@@ -211,7 +212,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
     store_row<T>(o + 32 * t, st.o[t], p.d - 32 * t, h, [&](float v) { return v * inv; });
   if (a.lse && h == 0)
     a.lse[((int64_t)b * p.heads + head) * p.sq + i] =
-        l == 0.f ? -INFINITY : st.m * a.c * kLn2 + logf(l);
+        l == 0.f ? -INFINITY : st.m * a.c * kLn2 + (logf(l) - kForwardUp<T> * kLn2);
 }
 
 // ------------------------------------------------------------- few queries
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
       f32x16 s[1] = {zero16()};
       each_step<NS>(p.d, [&](auto d) { s[0] = mma(L::load_rows(kt, 0, d), q[d], s[0]); });
       if (!all_rows || key0 < all_lo || key0 + 32 > all_hi) mask_keys(s, key0, lo, hi, h);
-      softmax_step(s, st, a.c);
+      softmax_step<kForwardUp<T>>(s, st, a.c);
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         const frag_t<T> pf = to_frag<T>(s[0], d);
@@ -358,7 +359,7 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
         }
       }
     const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
-    const float lse2 = sum == 0.f ? -INFINITY : m + log2f(sum);
+    const float lse2 = sum == 0.f ? -INFINITY : m + (log2f(sum) - kForwardUp<T>);
     const int rr = group * 32 + row, ri = rr / p.group, rh = kvh * p.group + rr % p.group;
     if (a.splits > 1) {
       const int64_t part = ((int64_t)(b * p.kv_heads + kvh) * a.splits + split) * a.rows + rr;

@@ -390,6 +390,18 @@ constexpr float kLeastC = 1e-20f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// f16's normal values lie between 2^-14 and 65504, and below that range a rounding
+// is no longer half a step of the value.  The factors of the second products, P
+// and ds, are therefore rounded as 2^up P and 2^up ds; their sums in fp32 are
+// scaled back where they are stored.  Forward, P is relative to a reference that
+// the row's maximum exceeds by 8 octaves at most: 2^7 P stays below 2^15, and
+// factors down to 2^-21 of the maximum keep all their bits.  Backward, P <= 1: 2^15
+// P, down to 2^-29.  bf16 has float's range, float32 rounds nothing: no scaling.
+template <typename T>
+constexpr int kForwardUp = std::is_same<T, _Float16>::value ? 7 : 0;
+template <typename T>
+constexpr int kBackwardUp = std::is_same<T, _Float16>::value ? 15 : 0;
+
 // A function of the unit for one head size (FC_DP).
 #define FC_DP_NAME(name) FC_CAT(name, FC_DP)
 

@@ -131,8 +131,13 @@ void fusedconv_rotary_destroy(fusedconv_rotary* h);
  *     dq = scale * ds k;  dk = scale * ds^T q
  * with dk, dv summed over the query heads that share a key head; no atomics,
  * so the same call gives the same bits.  For 16-bit T the factors P and ds of
- * these products are rounded to T (relative error of half a step of T each,
- * as the inputs they meet have); all sums are fp32.
+ * the second products, forward and backward, are rounded to T (relative error
+ * of half a step of T each, as the inputs they meet have); all sums are fp32.
+ * f16 has few octaves below 1: its factors are rounded after scaling by powers
+ * of two that the sums lose again.  They keep their relative error down to 2^-21
+ * of a row's largest probability (forward), to a probability or a ds of 2^-29
+ * (backward), and a larger ds than f16 holds lowers that scale instead of
+ * becoming infinite.
  *
  * head_dim: a multiple of 8, at most 128.  Strides in elements {batch,
  * position, head}; each a multiple of 16 bytes; the last axis is contiguous.

@@ -218,7 +218,7 @@ class AttentionCase:
 
 
 def _tiny(dtype):
-    """Results below the normal range are rounded to an absolute step, and 16-bit factors too."""
+    """Results below the normal range are rounded to an absolute step."""
     return 2.0 ** -24 if dtype == torch.float16 else 2.0 ** -120
 
 
