@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 
 from . import _binding
 from ._binding import FusedConvError
@@ -101,19 +102,24 @@ def _check(rc):
 torch = None      # imported on first use, as the package itself does not need it
 _DTYPES = {}
 _current_handle = None
+_first_use = threading.Lock()
 
 
 def _setup():
-    """First use: torch and the library."""
+    """First use: torch and the library.  `torch` is what calls look at, so it is set last."""
     global torch, _current_handle
-    import torch
-    _load()
-    # the current stream's raw handle without a Stream object, where torch offers it: a third
-    # of what a small call costs on the host
-    _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _DTYPES.update({torch.float32: _binding.F32, torch.float16: _binding.F16,
-                    torch.bfloat16: BF16})
+    import torch as module
+    with _first_use:
+        if torch is not None:
+            return
+        _load()
+        # the current stream's raw handle without a Stream object, where torch offers it: a third
+        # of what a small call costs on the host
+        _current_handle = getattr(module._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: module.cuda.current_stream(index).cuda_stream)
+        _DTYPES.update({module.float32: _binding.F32, module.float16: _binding.F16,
+                        module.bfloat16: BF16})
+        torch = module
 
 
 def _code(t):
