@@ -71,6 +71,11 @@ int ready(void* stream) noexcept {
   }
 }
 
+// Arrays that the kernels read and write value by value need their type's alignment only.
+bool aligned_to(const void* p, size_t bytes) { return (uintptr_t)p % bytes == 0; }
+constexpr char kAlignment[] =
+    "tensors must be 16-byte aligned; statistics, lengths, positions and the like to their type";
+
 // Strides of a [batch][len][heads][d] tensor: not negative, whole 16-byte
 // pieces, and an extent within the index limits; a tile's 256 rows have to fit
 // 31-bit byte offsets.
@@ -167,8 +172,8 @@ int fusedconv_layer_norm_forward(const fusedconv_layer_norm* h, const void* x, c
   if (h->p.n == 0) return FUSEDCONV_OK;
   if (!x || !y) return fail(FUSEDCONV_ERR_NULL_ARG, "x and y are required");
   if (!aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned16(bias) ||
-      !aligned16(mean) || !aligned16(rstd))
-    return fail(FUSEDCONV_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return fail(FUSEDCONV_ERR_ALIGNMENT, kAlignment);
   const int64_t es = elem_size(h->p.dtype), row = h->p.c * h->p.inner * es;
   const bool in_place = x == y && h->p.x_stride * es == row;
   if (!in_place && rows_meet(x, h->p.n, row, h->p.x_stride * es, y, h->p.n * row))
@@ -190,10 +195,10 @@ int fusedconv_layer_norm_backward(const fusedconv_layer_norm* h, const void* dy,
     return fail(FUSEDCONV_ERR_NULL_ARG, "weight is given iff it was declared");
   if (h->p.n > 0 && (!dy || !x || !mean || !rstd || !dx))
     return fail(FUSEDCONV_ERR_NULL_ARG, "dy, x, mean, rstd and dx are required");
-  if (!aligned16(dy) || !aligned16(x) || !aligned16(weight) || !aligned16(mean) ||
-      !aligned16(rstd) || !aligned16(dx) || !aligned16(dweight) || !aligned16(dbias) ||
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(weight) || !aligned_to(mean, 4) ||
+      !aligned_to(rstd, 4) || !aligned16(dx) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4) ||
       !aligned16(workspace))
-    return fail(FUSEDCONV_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    return fail(FUSEDCONV_ERR_ALIGNMENT, kAlignment);
   if (h->workspace > 0 && (dweight || dbias) && (!workspace || workspace_bytes < h->workspace))
     return fail(FUSEDCONV_ERR_WORKSPACE,
                 "workspace smaller than fusedconv_layer_norm_workspace_size() reports");
@@ -261,8 +266,9 @@ int fusedconv_rotary_run(const fusedconv_rotary* h, const void* q, const void* k
   if (!q || !q_out || !positions || !inv_freq || !axes || (d.kv_heads && (!k || !k_out)))
     return fail(FUSEDCONV_ERR_NULL_ARG, "a required pointer is NULL");
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) ||
-      !aligned16(positions) || !aligned16(inv_freq) || !aligned16(axes))
-    return fail(FUSEDCONV_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+      !aligned_to(positions, d.position_dtype == FUSEDCONV_POS_I64 ? 8 : 4) ||
+      !aligned_to(inv_freq, 4) || !aligned_to(axes, 4))
+    return fail(FUSEDCONV_ERR_ALIGNMENT, kAlignment);
   const int rc = ready(stream);
   if (rc != FUSEDCONV_OK) return rc;
   fc::RotaryArgs a{q, k, positions, inv_freq, axes, q_out, k_out, stream};
@@ -348,9 +354,9 @@ int fusedconv_attention_forward(const fusedconv_attention* h, const void* q, con
   if (h->p.batch == 0 || h->p.sq == 0) return FUSEDCONV_OK;
   if (!q || !o || (h->p.sk > 0 && (!k || !v)))
     return fail(FUSEDCONV_ERR_NULL_ARG, "q, k, v and o are required");
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
-      !aligned16(q_lengths) || !aligned16(k_lengths) || !aligned16(workspace))
-    return fail(FUSEDCONV_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned_to(lse, 4) ||
+      !aligned_to(q_lengths, 4) || !aligned_to(k_lengths, 4) || !aligned16(workspace))
+    return fail(FUSEDCONV_ERR_ALIGNMENT, kAlignment);
   if (h->plan.forward_bytes > 0 && (!workspace || workspace_bytes < h->plan.forward_bytes))
     return fail(FUSEDCONV_ERR_WORKSPACE,
                 "workspace smaller than fusedconv_attention_workspace_size() reports");
@@ -373,9 +379,9 @@ int fusedconv_attention_backward(const fusedconv_attention* h, const void* dout,
   if ((p.sq > 0 && (!dout || !q || !o || !lse || !dq)) || (p.sk > 0 && (!k || !v || !dk || !dv)))
     return fail(FUSEDCONV_ERR_NULL_ARG, "a required pointer is NULL");
   if (!aligned16(dout) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
-      !aligned16(lse) || !aligned16(q_lengths) || !aligned16(k_lengths) || !aligned16(dq) ||
+      !aligned_to(lse, 4) || !aligned_to(q_lengths, 4) || !aligned_to(k_lengths, 4) || !aligned16(dq) ||
       !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
-    return fail(FUSEDCONV_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    return fail(FUSEDCONV_ERR_ALIGNMENT, kAlignment);
   if (h->plan.backward_bytes > 0 && (!workspace || workspace_bytes < h->plan.backward_bytes))
     return fail(FUSEDCONV_ERR_WORKSPACE,
                 "workspace smaller than fusedconv_attention_workspace_size() reports");

@@ -13,8 +13,10 @@
  * Types: FUSEDCONV_F32, FUSEDCONV_F16 and FUSEDCONV_BF16, one type T for all
  * tensors of a call except where stated.  Sums, statistics, probabilities and
  * products are held in fp32; results are rounded once when stored (to nearest
- * even).  Device pointers are 16-byte aligned; a tensor without elements may
- * have a NULL pointer.
+ * even).  Pointers to tensors of T and to the workspace are 16-byte aligned;
+ * statistics, weight gradients, lse, lengths, positions, frequencies and axes,
+ * which are read and written value by value, are aligned to their own type.  A
+ * tensor without elements may have a NULL pointer.
  */
 #ifndef FUSEDCONV_TRANSFORMER_H
 #define FUSEDCONV_TRANSFORMER_H
