@@ -99,7 +99,7 @@ struct Down {
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
   const AttnParams& p = a.p;
-  const int64_t at = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int64_t at = (int64_t)block_number() * 32 + (threadIdx.x >> 3);
   if (at >= (int64_t)p.batch * p.heads * a.padded) return;
   const int i = (int)(at % a.padded);
   const int head = (int)(at / a.padded % p.heads), b = (int)(at / a.padded / p.heads);
@@ -421,8 +421,9 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
 // queries' blocks first 1176).
 template <typename T, int DP>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention_backward(AttnBwdK a) {
-  if ((int)blockIdx.x < a.key_blocks) keys_block<T, DP>(a, blockIdx.x);
-  else queries_block<T, DP>(a, blockIdx.x - a.key_blocks);
+  const int block = block_number();
+  if (block < a.key_blocks) keys_block<T, DP>(a, block);
+  else queries_block<T, DP>(a, block - a.key_blocks);
 }
 
 // The partial gradients' sums, in the splits' order: a thread has eight values.
@@ -473,15 +474,15 @@ int FC_DP_NAME(attention_backward_)(const AttnPlan& plan, const AttnBwdK& k, hip
     const AttnParams& p = k.p;
     if (p.sq > 0)
       hipLaunchKernelGGL((k_attention_rows<T>),
-                         dim3((unsigned)(((int64_t)p.batch * p.heads * k.padded + 31) / 32)),
-                         dim3(256), 0, st, k);
+                         grid_of(((int64_t)p.batch * p.heads * k.padded + 31) / 32), dim3(256), 0, st,
+                         k);
     auto fn = k_attention_backward<T, FC_DP>;
     constexpr int bytes = KeyBlock<T, FC_DP>::kLds;  // the larger of the two
     static_assert(bytes >= 4 * Tile<T, FC_DP>::bytes(32));
     rc = set_max_dynamic_lds((const void*)fn, bytes);
     if (rc != FUSEDCONV_OK) return;
-    const unsigned queries = xcd_grid((int64_t)p.batch * p.heads * k.q_splits * k.q_tiles);
-    hipLaunchKernelGGL(fn, dim3(k.key_blocks + queries), dim3(256), bytes, st, k);
+    const int64_t queries = xcd_grid((int64_t)p.batch * p.heads * k.q_splits * k.q_tiles);
+    hipLaunchKernelGGL(fn, grid_of(k.key_blocks + queries), dim3(256), bytes, st, k);
     const int64_t key_items = k.k_splits > 1 ? 2 * (int64_t)p.batch * p.kv_heads * p.sk * p.d / 8 : 0;
     const int64_t items =
         key_items + (k.q_splits > 1 ? (int64_t)p.batch * p.heads * p.sq * p.d / 8 : 0);

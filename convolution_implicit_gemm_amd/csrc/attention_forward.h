@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attention(AttnK
 
   const AttnParams& p = a.p;
   const int total = p.batch * p.heads * a.tiles * a.splits;
-  int item = xcd_item(blockIdx.x, total);
+  int item = xcd_item(block_number(), total);
   if (item >= total) return;
   const int split = item % a.splits;
   item /= a.splits;
@@ -246,8 +246,9 @@ __global__ __launch_bounds__(256) void k_attention_few(AttnK a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
 
   const AttnParams& p = a.p;
-  const int split = blockIdx.x % a.splits;
-  const int unit = blockIdx.x / a.splits;
+  const int split = block_number() % a.splits;
+  const int unit = block_number() / a.splits;
+  if (unit >= p.batch * p.kv_heads * a.row_groups) return;
   const int group = unit % a.row_groups;
   const int kvh = unit / a.row_groups % p.kv_heads, b = unit / a.row_groups / p.kv_heads;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -472,14 +473,14 @@ int FC_DP_NAME(attention_forward_)(const AttnPlan& plan, const AttnK& k, hipStre
       const int bytes = Few<T, FC_DP>::lds(plan.few_waves, plan.few_stages);
       rc = set_max_dynamic_lds((const void*)fn, bytes);
       if (rc != FUSEDCONV_OK) return;
-      hipLaunchKernelGGL(fn, dim3((unsigned)(p.batch * p.kv_heads * k.row_groups * k.splits)),
+      hipLaunchKernelGGL(fn, grid_of((int64_t)p.batch * p.kv_heads * k.row_groups * k.splits),
                          dim3(64 * plan.few_waves), bytes, st, k);
     } else {
       auto fn = k_attention<T, FC_DP>;
       constexpr int bytes = Many<T, FC_DP>::kLds;
       rc = set_max_dynamic_lds((const void*)fn, bytes);
       if (rc != FUSEDCONV_OK) return;
-      hipLaunchKernelGGL(fn, dim3(xcd_grid((int64_t)p.batch * p.heads * k.tiles * k.splits)),
+      hipLaunchKernelGGL(fn, grid_of(xcd_grid((int64_t)p.batch * p.heads * k.tiles * k.splits)),
                          dim3(256), bytes, st, k);
     }
     if (k.splits > 1) {

@@ -11,6 +11,7 @@
 // X again for each pass (from the caches, as a row is short next to them).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "fusedconv.h"
@@ -309,21 +310,23 @@ __global__ __launch_bounds__(kLoopThreads) void k_norm_rows_bwd_loop(NormK a) {
   }
 }
 
-// Column sums for the loop form: block (x: row range, y: 256 columns).
+// Column sums for the loop form: block (x: row range, y: columns 256 * y + thread,
+// and every 256 * gridDim.y on).
 template <typename T>
 __global__ __launch_bounds__(kLoopThreads) void k_norm_columns(NormK a) {
-  const int col = blockIdx.y * kLoopThreads + threadIdx.x;
-  if (col >= a.c) return;
-  float dw = 0.f, db = 0.f;
-  for (int row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const float d = (float)((const T*)a.dy)[(int64_t)row * a.dy_stride + col];
-    const float x = (float)((const T*)a.x)[(int64_t)row * a.x_stride + col];
-    dw += d * ((x - a.mean[row]) * a.rstd[row]);
-    db += d;
-  }
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
-  out[col] = dw;
-  out[a.c + col] = db;
+  for (int col = blockIdx.y * kLoopThreads + threadIdx.x; col < a.c;
+       col += gridDim.y * kLoopThreads) {
+    float dw = 0.f, db = 0.f;
+    for (int row = blockIdx.x; row < a.n; row += gridDim.x) {
+      const float d = (float)((const T*)a.dy)[(int64_t)row * a.dy_stride + col];
+      const float x = (float)((const T*)a.x)[(int64_t)row * a.x_stride + col];
+      dw += d * ((x - a.mean[row]) * a.rstd[row]);
+      db += d;
+    }
+    out[col] = dw;
+    out[a.c + col] = db;
+  }
 }
 
 // ------------------------------------------------------------- NCHW images
@@ -656,27 +659,29 @@ __global__ __launch_bounds__(kPlaneThreads) void k_norm_planes_bwd_loop(NormK a)
   }
 }
 
-// One channel (blockIdx.y) over the images blockIdx.x, + gridDim.x, ...
+// A channel (blockIdx.y, and every gridDim.y on) over the images blockIdx.x, +
+// gridDim.x, ...
 template <typename T>
 __global__ __launch_bounds__(kLoopThreads) void k_norm_plane_sums(NormK a) {
-  const int ch = blockIdx.y;
-  float s[2] = {0.f, 0.f};
-  for (int image = blockIdx.x; image < a.n; image += gridDim.x) {
-    const T* x = (const T*)a.x + (int64_t)image * a.x_stride + (int64_t)ch * a.inner;
-    const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride + (int64_t)ch * a.inner;
-    const float* mean = a.mean + (int64_t)image * a.inner;
-    const float* rstd = a.rstd + (int64_t)image * a.inner;
-    for (int i = threadIdx.x; i < a.inner; i += kLoopThreads) {
-      const float d = (float)dy[i];
-      s[0] += d * (((float)x[i] - mean[i]) * rstd[i]);
-      s[1] += d;
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
+  for (int ch = blockIdx.y; ch < a.c; ch += gridDim.y) {
+    float s[2] = {0.f, 0.f};
+    for (int image = blockIdx.x; image < a.n; image += gridDim.x) {
+      const T* x = (const T*)a.x + (int64_t)image * a.x_stride + (int64_t)ch * a.inner;
+      const T* dy = (const T*)a.dy + (int64_t)image * a.dy_stride + (int64_t)ch * a.inner;
+      const float* mean = a.mean + (int64_t)image * a.inner;
+      const float* rstd = a.rstd + (int64_t)image * a.inner;
+      for (int i = threadIdx.x; i < a.inner; i += kLoopThreads) {
+        const float d = (float)dy[i];
+        s[0] += d * (((float)x[i] - mean[i]) * rstd[i]);
+        s[1] += d;
+      }
     }
-  }
-  row_sum<kLoopThreads>(s);
-  if (threadIdx.x == 0) {
-    float* out = a.part + (int64_t)blockIdx.x * 2 * a.c;
-    out[ch] = s[0];
-    out[a.c + ch] = s[1];
+    row_sum<kLoopThreads>(s);
+    if (threadIdx.x == 0) {
+      out[ch] = s[0];
+      out[a.c + ch] = s[1];
+    }
   }
 }
 
@@ -725,6 +730,8 @@ struct NormPlan {
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kMostY = 32768;  // of a launch's second axis (65535 are allowed)
 
 // Rows (planes) that start on 16-byte borders and are whole pieces are moved as
 // such.  Others are moved in pieces too, at their own alignment (single values
@@ -846,6 +853,26 @@ void with_planes(const NormPlan& q, F&& f) {
   else lanes(std::false_type{});
 }
 
+// One axis of a launch holds fewer than 2^32 threads: calls of more blocks are
+// launched in parts of whole rows (images), `per` of them.
+constexpr int64_t kMostBlocks = 1 << 23;
+template <typename F>
+void in_parts(const NormProblem& p, const NormK& k, int64_t per, F&& launch) {
+  const int64_t es = p.dtype == FUSEDCONV_F32 ? 4 : 2;
+  for (int64_t first = 0; first < p.n; first += per) {
+    NormK part = k;
+    part.n = (int32_t)std::min(per, p.n - first);
+    part.x = (const char*)k.x + first * p.x_stride * es;
+    if (k.dy) part.dy = (const char*)k.dy + first * p.dy_stride * es;
+    part.out = (char*)k.out + first * p.c * p.inner * es;
+    if (k.mean) part.mean = k.mean + first * p.inner;
+    if (k.rstd) part.rstd = k.rstd + first * p.inner;
+    launch(part);
+  }
+}
+// Blocks of the kernels that step from row to row: any number of them will do.
+unsigned loop_blocks(int64_t rows) { return (unsigned)std::min<int64_t>(rows, 1 << 22); }
+
 int status() { return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH; }
 
 }  // namespace
@@ -863,15 +890,19 @@ int launch_norm_forward(const NormProblem& p, const NormArgs& a) {
     using T = typename decltype(tag)::type;
     if (q.planes)
       with_planes<false>(q, [&](auto v, auto pl, auto nch) {
-        hipLaunchKernelGGL((k_norm_planes<T, v, pl, nch>), dim3((unsigned)(p.n * q.tiles)),
-                           dim3(kPlaneThreads), 0, st, k);
+        in_parts(p, k, kMostBlocks / q.tiles, [&](const NormK& part) {
+          hipLaunchKernelGGL((k_norm_planes<T, v, pl, nch>), dim3((unsigned)part.n * q.tiles),
+                             dim3(kPlaneThreads), 0, st, part);
+        });
       });
     else if (q.loop)
-      hipLaunchKernelGGL((k_norm_rows_loop<T>), dim3((unsigned)p.n), dim3(kLoopThreads), 0, st, k);
+      hipLaunchKernelGGL((k_norm_rows_loop<T>), dim3(loop_blocks(p.n)), dim3(kLoopThreads), 0, st, k);
     else
       with_rows(q, [&](auto v, auto tpr, auto nch) {
-        hipLaunchKernelGGL((k_norm_rows<T, v, tpr, nch>),
-                           dim3((unsigned)ceil_div(p.n, 256 / tpr)), dim3(256), 0, st, k);
+        in_parts(p, k, kMostBlocks * (256 / tpr), [&](const NormK& part) {
+          hipLaunchKernelGGL((k_norm_rows<T, v, tpr, nch>),
+                             dim3((unsigned)ceil_div(part.n, 256 / tpr)), dim3(256), 0, st, part);
+        });
       });
   });
   return status();
@@ -892,10 +923,12 @@ int launch_norm_backward(const NormProblem& p, const NormArgs& a) {
     if (q.planes) {
       with_planes<true>(q, [&](auto v, auto pl, auto nch) {
         if constexpr (nch == 0) {
-          hipLaunchKernelGGL((k_norm_planes_bwd_loop<T, v, pl>), dim3((unsigned)(p.n * q.tiles)),
-                             dim3(kPlaneThreads), 0, st, k);
+          in_parts(p, k, kMostBlocks / q.tiles, [&](const NormK& part) {
+            hipLaunchKernelGGL((k_norm_planes_bwd_loop<T, v, pl>),
+                               dim3((unsigned)part.n * q.tiles), dim3(kPlaneThreads), 0, st, part);
+          });
           if (k.part)
-            hipLaunchKernelGGL((k_norm_plane_sums<T>), dim3(q.blocks, (unsigned)p.c),
+            hipLaunchKernelGGL((k_norm_plane_sums<T>), dim3(q.blocks, (unsigned)std::min(p.c, kMostY)),
                                dim3(kLoopThreads), 0, st, k);
         } else {
           hipLaunchKernelGGL((k_norm_planes_bwd<T, v, pl, nch>), dim3(q.blocks),
@@ -903,10 +936,11 @@ int launch_norm_backward(const NormProblem& p, const NormArgs& a) {
         }
       });
     } else if (q.loop) {
-      hipLaunchKernelGGL((k_norm_rows_bwd_loop<T>), dim3((unsigned)p.n), dim3(kLoopThreads), 0, st, k);
+      hipLaunchKernelGGL((k_norm_rows_bwd_loop<T>), dim3(loop_blocks(p.n)), dim3(kLoopThreads), 0,
+                         st, k);
       if (k.part)
         hipLaunchKernelGGL((k_norm_columns<T>),
-                           dim3(q.blocks, (unsigned)ceil_div(p.c, kLoopThreads)),
+                           dim3(q.blocks, (unsigned)std::min(ceil_div(p.c, kLoopThreads), kMostY)),
                            dim3(kLoopThreads), 0, st, k);
     } else {
       with_rows(q, [&](auto v, auto tpr, auto nch) {

@@ -48,6 +48,7 @@ struct RotaryK {
   int64_t qs[3], ks[3], qos[3], kos[3];
   int64_t pos_batch;
   int32_t tokens, heads, all_heads, pairs, num_axes, pos_type, tok;
+  int32_t first;                   // the launch's first token
   float sign;                      // -1: inverse
   FastDiv len, turn_items, turns, copies, copy_items;  // per token and per head
   int32_t copy_from;               // first copied value of a head
@@ -56,7 +57,7 @@ struct RotaryK {
 template <typename T, int W, bool INTER>
 __global__ __launch_bounds__(256) void k_rotary(RotaryK a) {
   extern __shared__ float2 table[];  // [tok][pairs]
-  const int t0 = blockIdx.x * a.tok;
+  const int t0 = a.first + blockIdx.x * a.tok;
   const int tok = min(a.tok, a.tokens - t0);
   for (int i = threadIdx.x; i < tok * a.pairs; i += 256) {
     const int t = i / a.pairs, p = i - t * a.pairs;
@@ -185,20 +186,26 @@ int launch_rotary(const RotaryProblem& p, const RotaryArgs& a) {
   int tok = 512 / k.pairs < 1 ? 1 : 512 / k.pairs > 32 ? 32 : 512 / k.pairs;
   while (tok > 1 && (k.tokens + tok - 1) / tok < 2048) tok /= 2;
   k.tok = tok;
-  const unsigned blocks = (unsigned)((k.tokens + tok - 1) / tok);
   const size_t lds = (size_t)tok * k.pairs * sizeof(float2);
   const hipStream_t st = (hipStream_t)a.stream;
-  with_type(d.dtype, [&](auto tag) {
-    using T = typename decltype(tag)::type;
-    constexpr int P = 16 / sizeof(T);
-    if (d.interleaved) {
-      if (wide) hipLaunchKernelGGL((k_rotary<T, P, true>), dim3(blocks), dim3(256), lds, st, k);
-      else hipLaunchKernelGGL((k_rotary<T, 1, true>), dim3(blocks), dim3(256), lds, st, k);
-    } else {
-      if (wide) hipLaunchKernelGGL((k_rotary<T, P, false>), dim3(blocks), dim3(256), lds, st, k);
-      else hipLaunchKernelGGL((k_rotary<T, 1, false>), dim3(blocks), dim3(256), lds, st, k);
-    }
-  });
+  // One axis of a launch holds fewer than 2^32 threads: more tokens go in parts.
+  constexpr int64_t kMostBlocks = 1 << 23;
+  for (int64_t first = 0; first < k.tokens; first += kMostBlocks * tok) {
+    const int64_t rest = (k.tokens - first + tok - 1) / tok;
+    const dim3 blocks((unsigned)(rest < kMostBlocks ? rest : kMostBlocks));
+    k.first = (int32_t)first;
+    with_type(d.dtype, [&](auto tag) {
+      using T = typename decltype(tag)::type;
+      constexpr int P = 16 / sizeof(T);
+      if (d.interleaved) {
+        if (wide) hipLaunchKernelGGL((k_rotary<T, P, true>), blocks, dim3(256), lds, st, k);
+        else hipLaunchKernelGGL((k_rotary<T, 1, true>), blocks, dim3(256), lds, st, k);
+      } else {
+        if (wide) hipLaunchKernelGGL((k_rotary<T, P, false>), blocks, dim3(256), lds, st, k);
+        else hipLaunchKernelGGL((k_rotary<T, 1, false>), blocks, dim3(256), lds, st, k);
+      }
+    });
+  }
   return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH;
 }
 

@@ -66,15 +66,24 @@ __device__ __forceinline__ float lane_sum(float v) {
   else return v;
 }
 
+// Blocks by number: one axis of a launch holds fewer than 2^32 threads, so that
+// large launches have a second one.  There are at least `blocks` of them; those
+// from `blocks` on have no work.
+inline dim3 grid_of(int64_t blocks) {
+  const int64_t rows = (blocks + (1 << 22) - 1) >> 22;
+  return dim3((unsigned)((blocks + rows - 1) / rows), (unsigned)rows);
+}
+__device__ __forceinline__ int block_number() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Blocks go round the 8 XCDs in launch order; this deals each XCD a run of
 // consecutive work items, so that neighbours (which read the same keys, or the
-// same queries) share its L2.  The grid is 8 * ceil(total / 8); an item >= total
-// has no work.
+// same queries) share its L2.  The grid is 8 * ceil(total / 8) or more; an item >=
+// total has no work.
 __device__ __forceinline__ int xcd_item(int block, int total) {
   const int run = (total + 7) >> 3;
-  return (block & 7) * run + (block >> 3);
+  return (block >> 3) < run ? (block & 7) * run + (block >> 3) : total;
 }
-inline unsigned xcd_grid(int64_t total) { return (unsigned)((total + 7) / 8 * 8); }
+inline int64_t xcd_grid(int64_t total) { return (total + 7) / 8 * 8; }
 
 // The V values at p, or the first n of them where the rest lies behind a row's
 // end (zeros then).  WHOLE: p is aligned to the piece and all V are there.
