@@ -235,6 +235,7 @@ struct Few {
     const int merge = waves * (32 * kRow + 64) * 4;
     return stream > merge ? stream : merge;
   }
+  static constexpr int kMostLds = lds(kMostWaves, 2);
 };
 
 template <typename T, int DP>
@@ -471,7 +472,8 @@ int FC_DP_NAME(attention_forward_)(const AttnPlan& plan, const AttnK& k, hipStre
     if (plan.few) {
       auto fn = k_attention_few<T, FC_DP>;
       const int bytes = Few<T, FC_DP>::lds(plan.few_waves, plan.few_stages);
-      rc = set_max_dynamic_lds((const void*)fn, bytes);
+      // the limit is the kernel's, for all its calls
+      rc = set_max_dynamic_lds((const void*)fn, Few<T, FC_DP>::kMostLds);
       if (rc != FUSEDCONV_OK) return;
       hipLaunchKernelGGL(fn, grid_of((int64_t)p.batch * p.kv_heads * k.row_groups * k.splits),
                          dim3(64 * plan.few_waves), bytes, st, k);

@@ -1,7 +1,7 @@
 """The host code of layer norm, rotary and attention under AddressSanitizer and
 UndefinedBehaviorSanitizer (CPU): transformer_sanitizer_driver.cpp sweeps descriptions, with values
-from the ends of their ranges among them, through create, workspace size and destroy.  Both
-sanitizers apply to the host pass only; the device pass, at -O0, just gives the objects their code.
+from the ends of their ranges among them, through create, workspace size and destroy, and checks that
+each attention kernel's LDS limit is set to one size.  Both sanitizers apply to the host pass only; the device pass, at -O0, just gives the objects their code.
 """
 import concurrent.futures
 import os
@@ -50,5 +50,6 @@ def test_host_code_under_asan_and_ubsan(tmp_path):
     report = r.stdout + r.stderr
     assert r.returncode == 0, report[-4000:]
     assert "runtime error" not in report and "AddressSanitizer" not in report, report[-4000:]
-    created, rejected = (int(r.stdout.split()[n]) for n in (1, 3))
+    created, rejected, kernels = (int(r.stdout.split()[n]) for n in (1, 3, 5))
     assert created > 80000 and rejected > 30000, r.stdout
+    assert kernels == 24, r.stdout  # two forms, three types, four head sizes

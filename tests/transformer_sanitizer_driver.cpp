@@ -2,13 +2,16 @@
 // AddressSanitizer and UndefinedBehaviorSanitizer (built by
 // tests/test_transformer_sanitizers_cpu.py): seeded descriptions, most of them
 // valid, some with one field set to a value from the ends of its range, through
-// create, workspace size and destroy.  No GPU call is made; what the entry points
+// create, workspace size and destroy.  Attention's forward pass is also run up to the
+// point where it asks for a kernel's LDS, which has to be one size a kernel: the limit
+// is a kernel's, whatever its calls need.  No kernel is launched; what the entry points
 // need of the rest of the library stands below.  Prints one line and exits 0; a
 // sanitizer finding aborts.
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
 
+#include <map>
 #include <string>
 
 #include "fusedconv_transformer.h"
@@ -16,9 +19,18 @@
 
 namespace fc {
 int set_last_error(int code, const std::string&) { return code; }
-int check_device(void*) { return FUSEDCONV_ERR_DEVICE; }
+int check_device(void*) { return FUSEDCONV_OK; }
 void clear_last_error() {}
-int set_max_dynamic_lds(const void*, int) { return FUSEDCONV_ERR_LAUNCH; }
+std::map<const void*, int> g_lds;
+int set_max_dynamic_lds(const void* kernel, int bytes) {
+  const int before = g_lds.emplace(kernel, bytes).first->second;
+  if (bytes != before) {
+    printf("a kernel's LDS limit is set to %d and to %d bytes\n", before, bytes);
+    fflush(stdout);
+    abort();
+  }
+  return FUSEDCONV_ERR_LAUNCH;  // and so nothing is launched
+}
 }  // namespace fc
 
 namespace {
@@ -151,6 +163,8 @@ void attention(bool mess) {
   ++g_created;
   size_t forward = 0, backward = 0;
   if (fusedconv_attention_workspace_size(h, &forward, &backward) != FUSEDCONV_OK) abort();
+  void* const p = (void*)4096;  // never read
+  (void)fusedconv_attention_forward(h, p, p, p, nullptr, nullptr, p, nullptr, p, forward, nullptr);
   fusedconv_attention_destroy(h);
 }
 
@@ -163,6 +177,6 @@ int main(int argc, char** argv) {
     rotary(i & 1);
     attention(i & 1);
   }
-  printf("handles: %d created, %d rejected\n", g_created, g_rejected);
+  printf("handles: %d created, %d rejected, %d kernels\n", g_created, g_rejected, (int)fc::g_lds.size());
   return 0;
 }
