@@ -115,7 +115,8 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // and base are the same for the whole wave.  In assembly because the compiler,
 // which cannot tell which LDS reads such a copy concerns, waits for it before
 // every transposing read; here the kernels wait (tile_barrier, vmcnt) where a
-// tile is needed.  The instruction has no output register, and its address is
+// tile is needed.  The instruction has no output register, and its addresses (m0
+// holds the one in LDS; a wait state lies between its writing and its use) are
 // read when it is issued.
 #ifdef __OPTIMIZE__
 #define FC_WAVE_POINTER(p) (p)
@@ -129,12 +130,12 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 template <int BYTES>
 __device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t off, const void* base) {
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(
                      __builtin_amdgcn_readfirstlane(to)),
                  "v"(off), "s"(FC_WAVE_POINTER(base))
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(
                      __builtin_amdgcn_readfirstlane(to)),
                  "v"(off), "s"(FC_WAVE_POINTER(base))
                  : "memory");
