@@ -502,9 +502,10 @@ class Attention(_Plan):
 
 
 def _limits(scale, window):
-    """scale and window as plain numbers: they are part of what a call is remembered by."""
+    """scale and window as plain numbers: they are part of what a call is remembered by.  The
+    window within 64 bits, which the descriptor would cut off."""
     return (None if scale is None else float(scale),
-            None if window is None else tuple(int(n) for n in window))
+            None if window is None else tuple(max(-2, min(int(n), 1 << 62)) for n in window))
 
 
 def _attention_sizes(q, k, v, scale, causal, window, q_lengths, k_lengths):
