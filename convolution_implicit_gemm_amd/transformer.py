@@ -560,7 +560,7 @@ def attention(q, k, v, *, scale=None, causal=False, window=None, q_lengths=None,
     q_lengths, k_lengths: int32 [batch] on the device, what is filled of each entry; query i
     stands at k_length - q_length + i.  window=(left, right): the keys a query sees around its
     position, -1 without limit; causal=True is a window of 0 to the right.  A query that sees no
-    key gets zeros and -inf."""
+    key gets zeros and -inf.  out: where to write; it must not overlap an input."""
     if torch is None:
         _setup()
     scale, window = _limits(scale, window)
@@ -599,12 +599,14 @@ def attention_backward(do, q, k, v, o, lse, *, scale=None, causal=False, window=
                        q_lengths=None, k_lengths=None, out=None, stream=None):
     """(dq, dk, dv) of attention, from its output o and log-sum-exps; the other arguments as
     there.  dk and dv sum over the query heads that share a key head.  out: the three tensors to
-    write (views of one packed gradient, say)."""
+    write (views of one packed gradient, say), which overlap neither each other nor an input."""
     if torch is None:
         _setup()
     scale, window = _limits(scale, window)
     if out is not None:
         out = tuple(out)
+        if len(out) != 3 or any(t is None for t in out):
+            raise ValueError("out has to be the three tensors dq, dk and dv")
     key = ("attention_backward", _meta(do), _meta(q), _meta(k), _meta(v), _meta(o), _meta(lse),
            scale, causal, window, _meta(q_lengths), _meta(k_lengths),
            None if out is None else tuple(_meta(t) for t in out))
