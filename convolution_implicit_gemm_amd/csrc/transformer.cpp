@@ -51,9 +51,14 @@ int64_t product(int64_t a, int64_t b, int64_t c, int64_t limit) {
 }
 constexpr int64_t kMaxElements = int64_t(1) << 40;
 
-int launched(int rc) noexcept {
-  if (rc == FUSEDCONV_OK) return rc;
+// Launch by f() and report what came of it; the bookkeeping of a launch may run out
+// of host memory.
+template <typename F>
+int launched(F&& f) noexcept {
+  int rc = FUSEDCONV_ERR_ALLOC;
   try {
+    rc = f();
+    if (rc == FUSEDCONV_OK) return rc;
     return fc::set_last_error(
         rc, std::string("kernel launch failed: ") + hipGetErrorString(hipGetLastError()));
   } catch (...) {
@@ -183,7 +188,7 @@ int fusedconv_layer_norm_forward(const fusedconv_layer_norm* h, const void* x, c
   fc::NormArgs a{};
   a.x = x; a.w = weight; a.b = bias; a.out = y; a.mean = mean; a.rstd = rstd; a.stream = stream;
   a.in_place = in_place;
-  return launched(fc::launch_norm_forward(h->p, a));
+  return launched([&] { return fc::launch_norm_forward(h->p, a); });
 }
 
 int fusedconv_layer_norm_backward(const fusedconv_layer_norm* h, const void* dy, const void* x,
@@ -212,7 +217,7 @@ int fusedconv_layer_norm_backward(const fusedconv_layer_norm* h, const void* dy,
   a.x = x; a.dy = dy; a.w = weight; a.out = dx;
   a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
   a.dw = dweight; a.db = dbias; a.part = (float*)workspace; a.stream = stream;
-  return launched(fc::launch_norm_backward(h->p, a));
+  return launched([&] { return fc::launch_norm_backward(h->p, a); });
 }
 
 void fusedconv_layer_norm_destroy(fusedconv_layer_norm* h) { delete h; }
@@ -272,7 +277,7 @@ int fusedconv_rotary_run(const fusedconv_rotary* h, const void* q, const void* k
   const int rc = ready(stream);
   if (rc != FUSEDCONV_OK) return rc;
   fc::RotaryArgs a{q, k, positions, inv_freq, axes, q_out, k_out, stream};
-  return launched(fc::launch_rotary(h->p, a));
+  return launched([&] { return fc::launch_rotary(h->p, a); });
 }
 
 void fusedconv_rotary_destroy(fusedconv_rotary* h) { delete h; }
@@ -365,7 +370,7 @@ int fusedconv_attention_forward(const fusedconv_attention* h, const void* q, con
   fc::AttnArgs a{};
   a.q = q; a.k = k; a.v = v; a.q_lengths = q_lengths; a.k_lengths = k_lengths;
   a.o = o; a.lse = lse; a.ws = workspace; a.stream = stream;
-  return launched(fc::launch_attention_forward(h->p, h->plan, a));
+  return launched([&] { return fc::launch_attention_forward(h->p, h->plan, a); });
 }
 
 int fusedconv_attention_backward(const fusedconv_attention* h, const void* dout, const void* q,
@@ -391,7 +396,7 @@ int fusedconv_attention_backward(const fusedconv_attention* h, const void* dout,
   a.q = q; a.k = k; a.v = v; a.o_in = o; a.dout = dout; a.lse_in = lse;
   a.q_lengths = q_lengths; a.k_lengths = k_lengths;
   a.dq = dq; a.dk = dk; a.dv = dv; a.ws = workspace; a.stream = stream;
-  return launched(fc::launch_attention_backward(p, h->plan, a));
+  return launched([&] { return fc::launch_attention_backward(p, h->plan, a); });
 }
 
 void fusedconv_attention_destroy(fusedconv_attention* h) { delete h; }

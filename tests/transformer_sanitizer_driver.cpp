@@ -12,10 +12,21 @@
 #include <stdlib.h>
 
 #include <map>
+#include <new>
 #include <string>
 
 #include "fusedconv_transformer.h"
 #include "internal.h"
+
+namespace {
+uint64_t g_state = 0x9e3779b97f4a7c15ull;
+uint64_t rnd() {  // xorshift64*
+  g_state ^= g_state >> 12;
+  g_state ^= g_state << 25;
+  g_state ^= g_state >> 27;
+  return g_state * 0x2545f4914f6cdd1dull;
+}
+}  // namespace
 
 namespace fc {
 int set_last_error(int code, const std::string&) { return code; }
@@ -29,19 +40,14 @@ int set_max_dynamic_lds(const void* kernel, int bytes) {
     fflush(stdout);
     abort();
   }
-  return FUSEDCONV_ERR_LAUNCH;  // and so nothing is launched
+  // nothing is launched after either; what is thrown must not leave a C function
+  if (rnd() % 16 == 0) throw std::bad_alloc();
+  return FUSEDCONV_ERR_LAUNCH;
 }
 }  // namespace fc
 
 namespace {
 
-uint64_t g_state = 0x9e3779b97f4a7c15ull;
-uint64_t rnd() {  // xorshift64*
-  g_state ^= g_state >> 12;
-  g_state ^= g_state << 25;
-  g_state ^= g_state >> 27;
-  return g_state * 0x2545f4914f6cdd1dull;
-}
 int64_t pick(int64_t lo, int64_t hi) { return lo + (int64_t)((rnd() >> 20) % (uint64_t)(hi - lo + 1)); }
 
 // A value from the ends of the range: near a power of two, near the limits, or negative.
@@ -164,7 +170,9 @@ void attention(bool mess) {
   size_t forward = 0, backward = 0;
   if (fusedconv_attention_workspace_size(h, &forward, &backward) != FUSEDCONV_OK) abort();
   void* const p = (void*)4096;  // never read
-  (void)fusedconv_attention_forward(h, p, p, p, nullptr, nullptr, p, nullptr, p, forward, nullptr);
+  const int rc =
+      fusedconv_attention_forward(h, p, p, p, nullptr, nullptr, p, nullptr, p, forward, nullptr);
+  if (rc != FUSEDCONV_OK && rc != FUSEDCONV_ERR_LAUNCH && rc != FUSEDCONV_ERR_ALLOC) abort();
   fusedconv_attention_destroy(h);
 }
 
