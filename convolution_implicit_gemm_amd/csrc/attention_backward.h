@@ -94,8 +94,8 @@ struct Down {
 // What those start from: nlse and ndelta = -rowsum(do * o).
 // Rows without a key, behind the entry's queries or in the padding get nlse =
 // -inf: their probabilities are then zero, and need no mask.  8 lanes a row;
-// bound by reading o and do (2 x 4096 queries, 32 heads of 128, bf16: 134 MB in
-// 30 us).
+// bound by reading o and do (2 x 4096 queries, 32 heads of 128, bf16: 134 MB in 24
+// to 30 us).
 template <typename T>
 __global__ __launch_bounds__(256) void k_attention_rows(AttnBwdK a) {
   const AttnParams& p = a.p;
@@ -410,11 +410,14 @@ __device__ __forceinline__ void queries_block(const AttnBwdK& a, int block) {
                  [&](float v) { return i < see.nq ? v * back : 0.f; });
 }
 
-// Bound by the matrix cores at the clock that the chip's power allows under
-// them: 2 x 4096 causal queries, 32 / 8 heads of 128, bf16, is 962 GFLOP in seven
-// products, 885 us for this kernel, the matrix cores busy for 53 % of the active
-// cycles; 32 x 577 queries, 16 heads of 72, f16, works on 80 of 72 values and on
-// 19 tiles for 18 and a row, 260 us, 37 %.
+// Long walks are bound by the matrix cores at the clock that the chip's power
+// allows under them: 2 x 4096 causal queries, 32 / 8 heads of 128, bf16, is 962
+// GFLOP in seven products, 885 to 940 us for this kernel on different cards, the
+// matrix cores busy for 53 % of the active cycles.  Short ones are not: 32 x 577
+// queries, 16 heads of 72, f16, take 280 us, the matrix cores busy for 36 %.  Of
+// their 230 GFLOP 123 are the formula's, 49 the two products taken twice, 58 padding
+// (80 and 96 columns for 72 values, 19 tiles for 18 and a row); and a block clears
+// padding, loads operands and waits for its first tile every 19 tiles.
 // Both kinds of blocks in one launch, those of the keys first: where a causal
 // window leaves them uneven, or too few for the chip, the others fill in (2 x
 // 4096 causal queries, 32 / 8 heads of 128, bf16: 915 us, two launches 1037, the

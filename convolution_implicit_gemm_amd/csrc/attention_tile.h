@@ -324,6 +324,11 @@ __device__ __forceinline__ void load_operand(frag_t<T> (&f)[DP / 16], const T* r
   }
 }
 
+// The factors P and ds of a second product as its operand.  Rounding them to T is
+// what 16-bit matrix products take; with both halves of a float kept, as two
+// operands, those products would be twice as many.  Against 64 bits it moves the
+// error of a result, which is rounded to T itself, from 2.1e-4 to 2.9e-4 (f16,
+// forward and backward) and from 1.5e-3 to 2.1e-3 (bf16; backward 1.7e-3 to 2.4e-3).
 template <typename T>
 __device__ __forceinline__ frag_t<T> to_frag(const f32x16& c, int step) {
   frag_t<T> f;

@@ -1,9 +1,14 @@
 // Layer norm, forward and backward (include/fusedconv_transformer.h), over
 // token rows and over the channels of NCHW images.
 //
-// All four kernels are bound by HBM: they hold a row's values (NCHW: a pixel
-// tile's) in registers between the statistics and the result, so every value
-// is read once and written once.  The variance is the mean of squares about
+// All four kernels hold a row's values (NCHW: a pixel tile's) in registers between
+// the statistics and the result, so every value is read once and written once.
+// Rows, and planes of many tiles, run at a copy's rate; planes of few lines do not:
+// a tile takes a run of pixels from every channel, runs that in such planes begin and
+// end inside lines that a neighbour reads too, and the last tile is mostly empty
+// (f16, 256 x 768 channels of 14 x 14: 61 us forward for 30 of bytes, backward 120
+// for 45; of 7 x 7: 20 for 8, 32 for 11).  Rows that are no whole pieces: 16000 x
+// 513, f16, 14 for 7 and 24 for 10; 25700 x 1275, backward, 61 for 39.  The variance is the mean of squares about
 // the mean (a second pass over registers), not a difference of two sums, so a
 // large common offset costs no digits.
 //
@@ -734,9 +739,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kMostY = 32768;  // of a launch's second axis (65535 are allowed)
 
 // Rows (planes) that start on 16-byte borders and are whole pieces are moved as
-// such.  Others are moved in pieces too, at their own alignment (single values
-// instead: 256 x 768 f16 planes of 7 x 7 39 us, so 22; 16000 x 513 rows, backward,
-// 83 and 64; rows of 4099 73 and 47).
+// such.  Others are moved in pieces too, at their own alignment (256 x 768 f16
+// planes of 7 x 7: 20 us, with single values 39).
 NormPlan plan_norm(const NormProblem& p, bool backward) {
   NormPlan q{};
   q.planes = p.inner > 1;
@@ -776,9 +780,9 @@ NormPlan plan_norm(const NormProblem& p, bool backward) {
     q.tpr /= 2;
   // Four lanes' runs are half a line; they take as much memory time as eight only
   // where the chip is not full anyway (8 x 384 channels of 14 x 14, f16, backward:
-  // 23 us with eight, 15 with four; 18 x 709, forward: 22 and 13; but 256 x 768,
-  // forward: 69 and 74), and are better than the second reading of the looped form
-  // (256 x 768 of 14 x 14, backward: 181 us looped, 118 with four).
+  // 23 us with eight, 11 with four; 18 x 709, forward: 22 and 12; but 256 x 768,
+  // forward: 62 and 72), and are better than the second reading of the looped form
+  // (256 x 768 of 14 x 14, backward: 186 us looped, 120 with four).
   if (q.tpr == 8 && (p.n * ceil_div(p.inner, 8 * wide) < 256 || (backward && p.c > 512))) q.tpr = 4;
   const int cg = kPlaneThreads / q.tpr;
   q.nch = 2;

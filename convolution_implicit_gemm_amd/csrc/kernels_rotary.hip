@@ -5,7 +5,11 @@
 // then turns the heads: each item is one 16-byte piece of one half of a head
 // and its partner in the other half (interleaved: one piece), so every value
 // is read once and written once; the call is bound by HBM: 256 x 196 tokens, 12
-// heads of 64 in Q and K, bf16, 309 MB in 60 us.  Loading the next item before
+// heads of 64 in Q and K, bf16, 309 MB in 60 us.  Pairs that do not fill whole
+// pieces move as single values, copied tail and all, and are bound by their
+// accesses: f16, heads of 72, halves of 36 pairs, 125 us for 68 of bytes (interleaved,
+// where the 72 values are whole pieces, 75); heads of 88 with 18 pairs 235 for 83.
+// Loading the next item before
 // the present one is stored gained nothing (58 to 60).
 //
 // The angle pos * inv_freq is taken in 64 bits and reduced there to a fraction
