@@ -53,6 +53,13 @@ def both(b, sq, sk, h, hk, d, window, lengths, dtype, seed=1):
         ref.within(name, got[n], grads[n], grads[n + 3])
 
 
+@pytest.fixture(autouse=True)
+def give_back():
+    """The large tensors' memory, for the tests that follow."""
+    yield
+    torch.cuda.empty_cache()
+
+
 WINDOWS = [  # b, sq, sk, h, hk, d, window, lengths
     (3, 150, 210, 2, 1, 64, (33, 7), ([150, 64, 1], [210, 100, 40])),
     (4, 140, 140, 2, 2, 72, (20, 0), ([140, 3, 0, 77], [140, 140, 60, 0])),

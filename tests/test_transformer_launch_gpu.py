@@ -15,6 +15,13 @@ def case(name):
     sys.__stderr__.flush()
 
 
+@pytest.fixture(autouse=True)
+def give_back():
+    """The large tensors' memory, for the tests that follow."""
+    yield
+    torch.cuda.empty_cache()
+
+
 def places(n, width):
     """Runs of entries at the start, around the middle and at the end."""
     return [slice(a, a + width) for a in (0, n // 2 - width // 2, n - width)]
