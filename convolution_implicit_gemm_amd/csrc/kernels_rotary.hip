@@ -12,37 +12,18 @@
 // Loading the next item before
 // the present one is stored gained nothing (58 to 60).
 //
-// The angle pos * inv_freq is taken in 64 bits and reduced there to a fraction
-// of a turn in [-1/2, 1/2]: at position 10^6 an angle in 32 bits would be off
-// by 0.03 radians.  The sine and cosine of the fraction are 32-bit.
+// turns.h has the angles.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
 
 #include "fusedconv.h"
 #include "transformer.h"
+#include "turns.h"
 #include "vec.h"
 
 namespace fc {
 namespace {
-
-// Quotients by a divisor known at launch: floor(n / d) = (n * mul) >> (32 + shift)
-// for 0 <= n < 2^31 (mul rounded up, shift = ceil(log2 d) - 1).
-struct FastDiv {
-  uint32_t d, mul, shift;
-};
-FastDiv fast_div(uint32_t d) {
-  FastDiv f{d, 0, 0};
-  if (d == 1) return f;
-  uint32_t s = 0;
-  while ((uint64_t(1) << s) < d) ++s;
-  f.shift = s - 1;
-  f.mul = (uint32_t)(((uint64_t(1) << (32 + f.shift)) + d - 1) / d);
-  return f;
-}
-__device__ __forceinline__ uint32_t quotient(uint32_t n, const FastDiv& f) {
-  return f.d == 1 ? n : __umulhi(n, f.mul) >> f.shift;
-}
 
 struct RotaryK {
   const void *q, *k, *pos;
@@ -66,16 +47,9 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryK a) {
   for (int i = threadIdx.x; i < tok * a.pairs; i += 256) {
     const int t = i / a.pairs, p = i - t * a.pairs;
     const int b = quotient(t0 + t, a.len), s = t0 + t - b * (int)a.len.d;
-    const int axis = min(max(a.axes[p], 0), a.num_axes - 1);
-    const int64_t at = b * a.pos_batch + (int64_t)s * a.num_axes + axis;
-    const double pos = a.pos_type == FUSEDCONV_POS_I64   ? (double)((const int64_t*)a.pos)[at]
-                       : a.pos_type == FUSEDCONV_POS_I32 ? (double)((const int32_t*)a.pos)[at]
-                                                         : (double)((const float*)a.pos)[at];
-    const double turns = pos * (double)a.inv_freq[p] * 0.15915494309189533577;  // 1 / (2 pi)
-    const float frac = (float)(turns - rint(turns));
-    float sn, cs;
-    sincospif(2.0f * frac, &sn, &cs);
-    table[i] = make_float2(cs, a.sign * sn);
+    const float2 turn = turn_of(a.pos, a.pos_type, b * a.pos_batch + (int64_t)s * a.num_axes,
+                                a.num_axes, a.inv_freq, a.axes, p);
+    table[i] = make_float2(turn.x, a.sign * turn.y);
   }
   __syncthreads();
 
