@@ -8,7 +8,8 @@ FusedConv README ("Description", "Inputs", "Outputs", "Attributes").
 from __future__ import annotations
 
 from ._binding import EXPORTS, FusedConvError, Handle, LIB_PATH, load
-from .block import QkNormRotary, qk_norm_rotary, qk_norm_rotary_backward
+from .block import (GatedFfn, QkNormRotary, gated_ffn, gated_ffn_backward, qk_norm_rotary,
+                    qk_norm_rotary_backward)
 from .transformer import (Attention, LayerNorm, Rotary, attention, attention_backward, layer_norm,
                           layer_norm_backward, rotary)
 
@@ -16,7 +17,7 @@ __all__ = ["fused_conv", "FusedConv", "Handle", "FusedConvError", "load", "LIB_P
            "ConvBackwardData", "ConvBackwardWeight", "conv_backward_data", "conv_backward_weight",
            "LayerNorm", "Rotary", "Attention", "layer_norm", "layer_norm_backward", "rotary",
            "attention", "attention_backward", "QkNormRotary", "qk_norm_rotary",
-           "qk_norm_rotary_backward"]
+           "qk_norm_rotary_backward", "GatedFfn", "gated_ffn", "gated_ffn_backward"]
 
 _cache: dict = {}
 

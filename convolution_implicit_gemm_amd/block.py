@@ -1,9 +1,10 @@
 """What a whole transformer block needs beside layer norm, rotary positions and attention, on torch
-tensors: norms of queries and keys with their rotation, and their gradients.
+tensors: norms of queries and keys with their rotation, the gated feed-forward block, and their
+gradients.
 
 include/fusedconv_block.h, in the same libfusedconv.so and the manner of transformer.py: a planned
-object for fixed shapes (QkNormRotary) and functions that keep such plans by shape (qk_norm_rotary
-and its backward function).  Only arguments are marshalled here.
+object for fixed shapes (QkNormRotary, GatedFfn) and functions that keep such plans by shape
+(qk_norm_rotary, gated_ffn and the backward functions).  Only arguments are marshalled here.
 
 Types: float32, float16, bfloat16.  Everything runs on the current stream of the tensors' device, or
 on `stream` (a torch stream or a raw handle), on which the results and the workspace are then
@@ -22,7 +23,9 @@ from .transformer import _I64x3, _check, _dense, _heads_tensor, _meta, _on, _Pla
 # Every symbol include/fusedconv_block.h declares.
 EXPORTS = ["fusedconv_qk_norm_rotary_create", "fusedconv_qk_norm_rotary_workspace_size",
            "fusedconv_qk_norm_rotary_forward", "fusedconv_qk_norm_rotary_backward",
-           "fusedconv_qk_norm_rotary_destroy"]
+           "fusedconv_qk_norm_rotary_destroy", "fusedconv_gated_ffn_create",
+           "fusedconv_gated_ffn_workspace_size", "fusedconv_gated_ffn_forward",
+           "fusedconv_gated_ffn_backward", "fusedconv_gated_ffn_destroy"]
 
 
 class QkNormRotaryDesc(ctypes.Structure):
@@ -36,6 +39,14 @@ class QkNormRotaryDesc(ctypes.Structure):
                 ("q_strides", _I64x3), ("k_strides", _I64x3),
                 ("q_out_strides", _I64x3), ("k_out_strides", _I64x3),
                 ("dq_strides", _I64x3), ("dk_strides", _I64x3)]
+
+
+class GatedFfnDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("in", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("out", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("dy_stride", ctypes.c_int64), ("activation", ctypes.c_char_p),
+                ("alpha", ctypes.c_float)]
 
 
 _lib = None
@@ -55,6 +66,11 @@ def _load():
             "fusedconv_qk_norm_rotary_forward": [vp] * 11,
             "fusedconv_qk_norm_rotary_backward": [vp] * 15 + [sz, vp],
             "fusedconv_qk_norm_rotary_destroy": [vp],
+            "fusedconv_gated_ffn_create": [ctypes.POINTER(GatedFfnDesc), ctypes.POINTER(vp)],
+            "fusedconv_gated_ffn_workspace_size": [vp, ctypes.POINTER(sz), ctypes.POINTER(sz)],
+            "fusedconv_gated_ffn_forward": [vp] * 9 + [sz, vp],
+            "fusedconv_gated_ffn_backward": [vp] * 13 + [sz, vp],
+            "fusedconv_gated_ffn_destroy": [vp],
         }
         for name, types in args.items():
             fn = getattr(lib, name)
@@ -210,3 +226,124 @@ def qk_norm_rotary_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_fre
         op.backward(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, axes, out_q, out_k, dqw,
                     dkw, ws, st)
     return out_q, out_k, dqw, dkw
+
+
+# ---------------------------------------------------- gated feed-forward block
+
+class GatedFfn(_Plan):
+    """A planned gated feed-forward block, forward and backward (fusedconv_gated_ffn_create)."""
+    _destroy = "fusedconv_gated_ffn_destroy"
+
+    def __init__(self, dtype, rows, in_features, hidden, out_features, x_stride, dy_stride, activation,
+                 alpha):
+        lib = _load()
+        self._create(lib.fusedconv_gated_ffn_create,
+                     GatedFfnDesc(dtype, rows, in_features, hidden, out_features, x_stride, dy_stride,
+                                  activation.encode(), alpha))
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(lib.fusedconv_gated_ffn_workspace_size(self._h, ctypes.byref(f), ctypes.byref(b)))
+        self.forward_bytes, self.backward_bytes = f.value, b.value
+
+    def forward(self, x, gate, up, down, y, g, u, ws, stream):
+        _check(_lib.fusedconv_gated_ffn_forward(
+            self._h, _ptr(x), _ptr(gate), _ptr(up), _ptr(down), _ptr(y), _ptr(g), _ptr(u), _ptr(ws),
+            0 if ws is None else ws.numel(), stream))
+
+    def backward(self, dy, x, gate, up, down, g, u, dx, dgate, dup, ddown, ws, stream):
+        _check(_lib.fusedconv_gated_ffn_backward(
+            self._h, _ptr(dy), _ptr(x), _ptr(gate), _ptr(up), _ptr(down), _ptr(g), _ptr(u), _ptr(dx),
+            _ptr(dgate), _ptr(dup), _ptr(ddown), _ptr(ws), 0 if ws is None else ws.numel(), stream))
+
+
+def _activation(name, params):
+    """(name, alpha): QuickGelu's parameter is 1.702 where none is given, as in a convolution."""
+    params = () if params is None else tuple(float(v) for v in params)
+    if len(params) > (1 if name == "QuickGelu" else 0):
+        raise FusedConvError(-12, f"activation {name} takes fewer parameters than {len(params)}")
+    return name, params[0] if params else 1.702
+
+
+def _rows(name, t, features, dtype, device):
+    """(rows, stride) of a [..., features] tensor whose rows lie at one stride."""
+    if t.dim() < 1 or int(t.shape[-1]) != features:
+        raise ValueError(f"{name} has shape {list(t.shape)}, expected [..., {features}]")
+    _t._expect(name, t, tuple(t.shape), dtype, device)
+    n, _, _, step = _t._norm_view(name, t, -1)
+    return n, step
+
+
+def _plan_gated(x, gate, up, down, activation, alpha, out, back):
+    """The plan of a call; back: dy, g and u of a backward call, or None."""
+    code = _t._code(x)
+    if gate.dim() != 2 or down.dim() != 2:
+        raise ValueError("gate and up must be [hidden, in], down [out, hidden]")
+    f, c = (int(n) for n in gate.shape)
+    o = int(down.shape[0])
+    rows, step = _rows("x", x, c, x.dtype, x.device)
+    _t._expect_whole("gate", gate, (f, c), x.dtype, x.device)
+    _t._expect_whole("up", up, (f, c), x.dtype, x.device)
+    _t._expect_whole("down", down, (o, f), x.dtype, x.device)
+    lead = tuple(x.shape[:-1])
+    y_shape, h_shape = lead + (o,), lead + (f,)
+    if out is not None:
+        _t._expect_whole("out", out, y_shape, x.dtype, x.device)
+    dy_step = o
+    if back is not None:
+        dy, g, u = back
+        _t._expect("dy", dy, y_shape, x.dtype, x.device)
+        dy_step = _rows("dy", dy, o, x.dtype, x.device)[1]
+        _t._expect_whole("g", g, h_shape, x.dtype, x.device)
+        _t._expect_whole("u", u, h_shape, x.dtype, x.device)
+    return GatedFfn(code, rows, c, f, o, step, dy_step, activation, alpha), y_shape, h_shape
+
+
+def gated_ffn(x, gate, up, down, *, activation="QuickGelu", activation_params=(1.0,), keep=False,
+              out=None, stream=None):
+    """(act(x gate^T) * (x up^T)) down^T: [..., out]; (y, g, u) with keep=True, the projections g =
+    x gate^T and u = x up^T [..., hidden] as gated_ffn_backward takes them.
+
+    x [..., in], a view whose rows lie at one stride is fine; gate, up [hidden, in], down [out,
+    hidden], x's dtype, contiguous (halves of one packed weight are); in, hidden and out are multiples
+    of 8.  activation: QuickGelu (v * sigmoid(alpha * v); as it stands, alpha = 1, SiLU), Gelu,
+    FastGelu, Sigmoid or Relu.  out: where to write, contiguous; it must not overlap an input."""
+    if _t.torch is None or _lib is None:
+        _setup()
+    activation, alpha = _activation(activation, activation_params)
+    key = ("gated_ffn", _meta(x), _meta(gate), _meta(up), _meta(down), activation, alpha, _meta(out))
+    op, y_shape, h_shape = _t._calls.get(key) or _remember(
+        key, _plan_gated(x, gate, up, down, activation, alpha, out, None))
+    torch = _t.torch
+    with _on(x.device, stream) as st:
+        if out is None:
+            out = torch.empty(y_shape, dtype=x.dtype, device=x.device)
+        g = u = None
+        if keep:
+            g = torch.empty(h_shape, dtype=x.dtype, device=x.device)
+            u = torch.empty(h_shape, dtype=x.dtype, device=x.device)
+        ws = torch.empty(op.forward_bytes, dtype=torch.uint8, device=x.device)
+        op.forward(x, gate, up, down, out, g, u, ws, st)
+    return (out, g, u) if keep else out
+
+
+def gated_ffn_backward(dy, x, gate, up, down, g, u, *, activation="QuickGelu",
+                       activation_params=(1.0,), weight_grads=True, stream=None):
+    """(dx, dgate, dup, ddown) of gated_ffn, from the projections g and u that it kept; the other
+    arguments as there.  All have x's dtype: the factors of their products are rounded to it.
+    weight_grads=False: the last three are None."""
+    if _t.torch is None or _lib is None:
+        _setup()
+    activation, alpha = _activation(activation, activation_params)
+    key = ("gated_ffn_backward", _meta(dy), _meta(x), _meta(gate), _meta(up), _meta(down), _meta(g),
+           _meta(u), activation, alpha)
+    op, _, _ = _t._calls.get(key) or _remember(
+        key, _plan_gated(x, gate, up, down, activation, alpha, None, (dy, g, u)))
+    torch = _t.torch
+    with _on(x.device, stream) as st:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dgate = dup = ddown = None
+        if weight_grads:
+            dgate, dup, ddown = (torch.empty(w.shape, dtype=x.dtype, device=x.device)
+                                 for w in (gate, up, down))
+        ws = torch.empty(op.backward_bytes, dtype=torch.uint8, device=x.device)
+        op.backward(dy, x, gate, up, down, g, u, dx, dgate, dup, ddown, ws, st)
+    return dx, dgate, dup, ddown

@@ -21,7 +21,8 @@ SOURCES = ["resolver.cpp", "planner.cpp", "capi.cpp", "kernels_direct.hip", "ker
            "kernels_backward.hip", "kernels_halo32.hip", "transformer.cpp",
            "kernels_layernorm.hip", "kernels_rotary.hip", "kernels_attention_d128.hip",
            "kernels_attention_d96.hip", "kernels_attention_d64.hip", "kernels_attention_d32.hip",
-           "block.cpp", "kernels_qk_norm.hip"]
+           "block.cpp", "kernels_qk_norm.hip", "gated_plan.cpp", "kernels_gated_f32.hip",
+           "kernels_gated_f16.hip", "kernels_gated_bf16.hip"]
 # Kernels specialised per activation: compiled once per activation id
 # (-DFC_ACT=k, k = 0 .. ACT_COUNT-1); unit 0 also holds the route entry points.
 ACT_SOURCES = ["kernels_depthwise.hip", "kernels_dwmfma.hip", "kernels_halo.hip",

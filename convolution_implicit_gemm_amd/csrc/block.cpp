@@ -1,18 +1,24 @@
 // Entry points of include/fusedconv_block.h: checks, handles, dispatch.
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <new>
 
 #include "block.h"
 #include "checks.h"
 
+using namespace fc;
+
 struct fusedconv_qk_norm_rotary {
   fusedconv_qk_norm_rotary_desc d;
   size_t workspace;
 };
 
-using namespace fc;
+struct fusedconv_gated_ffn {
+  GatedProblem p;
+  GatedPlan plan;
+};
 
 namespace {
 constexpr char kStrides[] =
@@ -146,5 +152,106 @@ int fusedconv_qk_norm_rotary_backward(const fusedconv_qk_norm_rotary* h, const v
 }
 
 void fusedconv_qk_norm_rotary_destroy(fusedconv_qk_norm_rotary* h) { delete h; }
+
+// ---------------------------------------------------- gated feed-forward block
+
+int fusedconv_gated_ffn_create(const fusedconv_gated_ffn_desc* d, fusedconv_gated_ffn** out) {
+  if (out) *out = nullptr;
+  if (!d || !out || !d->activation)
+    return fail(FUSEDCONV_ERR_NULL_ARG, "desc, its activation and out must not be NULL");
+  if (!known(d->dtype)) return fail(FUSEDCONV_ERR_DTYPE, "dtype is not float32, float16 or bfloat16");
+  if (d->rows < 0 || d->in < 8 || d->hidden < 8 || d->out < 8 || d->in % 8 || d->hidden % 8 || d->out % 8)
+    return fail(FUSEDCONV_ERR_OUTPUT_SHAPE,
+                "rows must be >= 0; in, hidden and out positive multiples of 8");
+  static const char* const names[] = {"Sigmoid", "Relu", "QuickGelu", "Gelu", "FastGelu"};  // GateAct
+  int act = 0;
+  while (act < 5 && strcmp(d->activation, names[act]) != 0) ++act;
+  if (act == 5)
+    return fail(FUSEDCONV_ERR_ACTIVATION, "activation is not QuickGelu, Gelu, FastGelu, Sigmoid or Relu");
+  if (!isfinite(d->alpha)) return fail(FUSEDCONV_ERR_ATTR_VALUE, "alpha must be finite");
+  const int64_t es = elem_size(d->dtype);
+  // a tile's 256 rows have to fit 31-bit byte offsets
+  const int64_t most = ((int64_t(1) << 31) / 256 - 1) / es;
+  if (d->in > most || d->hidden > most || d->out > most || d->rows > INT32_MAX / 2 ||
+      product(d->rows, d->hidden, 1, kMaxElements / 4) < 0 || product(d->rows, d->in, 1, kMaxElements / 4) < 0 ||
+      product(d->rows, d->out, 1, kMaxElements / 4) < 0)
+    return fail(FUSEDCONV_ERR_TOO_LARGE, "a tensor exceeds the index limits");
+  if (d->rows > 1 && (d->x_stride < 0 || d->dy_stride < 0 || d->x_stride % (16 / es) || d->dy_stride % (16 / es) ||
+                      d->x_stride > most || d->dy_stride > most))
+    return fail(FUSEDCONV_ERR_ALIGNMENT,
+                "strides must be non-negative, whole 16-byte pieces and within the index limits");
+  fusedconv_gated_ffn* h = new (std::nothrow) fusedconv_gated_ffn();
+  if (!h) return fail(FUSEDCONV_ERR_ALLOC, "out of host memory");
+  h->p = {d->dtype, (int32_t)d->rows, (int32_t)d->in, (int32_t)d->hidden, (int32_t)d->out, act, d->alpha,
+          d->rows > 1 ? d->x_stride : d->in, d->rows > 1 ? d->dy_stride : d->out};
+  plan_gated(h->p, h->plan);
+  *out = h;
+  clear_last_error();
+  return FUSEDCONV_OK;
+}
+
+int fusedconv_gated_ffn_workspace_size(const fusedconv_gated_ffn* h, size_t* forward_bytes,
+                                       size_t* backward_bytes) {
+  if (!h || !forward_bytes || !backward_bytes) return fail(FUSEDCONV_ERR_NULL_ARG, "NULL argument");
+  *forward_bytes = h->plan.forward_bytes;
+  *backward_bytes = h->plan.backward_bytes;
+  return FUSEDCONV_OK;
+}
+
+int fusedconv_gated_ffn_forward(const fusedconv_gated_ffn* h, const void* x, const void* gate,
+                                const void* up, const void* down, void* y, void* g, void* u,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!h) return fail(FUSEDCONV_ERR_NULL_ARG, "h is required");
+  if (!g != !u) return fail(FUSEDCONV_ERR_NULL_ARG, "give both g and u or neither");
+  if (h->p.m == 0) return FUSEDCONV_OK;
+  if (!x || !gate || !up || !down || !y)
+    return fail(FUSEDCONV_ERR_NULL_ARG, "x, gate, up, down and y are required");
+  for (const void* p : {x, gate, up, down, (const void*)y, (const void*)g, (const void*)u, (const void*)workspace})
+    if (!aligned16(p)) return fail(FUSEDCONV_ERR_ALIGNMENT, kAlignment);
+  if (!workspace || workspace_bytes < h->plan.forward_bytes)
+    return fail(FUSEDCONV_ERR_WORKSPACE,
+                "workspace smaller than fusedconv_gated_ffn_workspace_size() reports");
+  const int rc = ready(stream);
+  if (rc != FUSEDCONV_OK) return rc;
+  GatedArgs a{};
+  a.x = x; a.gate = gate; a.up = up; a.down = down;
+  a.y = y; a.g = g; a.u = u; a.ws = workspace; a.stream = stream;
+  return launched([&] {
+    return h->p.dtype == FUSEDCONV_F32   ? gated_forward_f32(h->p, h->plan, a)
+           : h->p.dtype == FUSEDCONV_F16 ? gated_forward_f16(h->p, h->plan, a)
+                                         : gated_forward_bf16(h->p, h->plan, a);
+  });
+}
+
+int fusedconv_gated_ffn_backward(const fusedconv_gated_ffn* h, const void* dy, const void* x,
+                                 const void* gate, const void* up, const void* down,
+                                 const void* g, const void* u, void* dx, void* dgate, void* dup,
+                                 void* ddown, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if (!h) return fail(FUSEDCONV_ERR_NULL_ARG, "h is required");
+  if (!dgate != !dup || !dgate != !ddown)
+    return fail(FUSEDCONV_ERR_NULL_ARG, "give all three of dgate, dup and ddown or none");
+  if (!gate || !up || !down || (h->p.m > 0 && (!dy || !x || !g || !u || !dx)))
+    return fail(FUSEDCONV_ERR_NULL_ARG, "a required pointer is NULL");
+  for (const void* p : {dy, x, gate, up, down, g, u, (const void*)dx, (const void*)dgate, (const void*)dup,
+                        (const void*)ddown, (const void*)workspace})
+    if (!aligned16(p)) return fail(FUSEDCONV_ERR_ALIGNMENT, kAlignment);
+  if (!workspace || workspace_bytes < h->plan.backward_bytes)
+    return fail(FUSEDCONV_ERR_WORKSPACE,
+                "workspace smaller than fusedconv_gated_ffn_workspace_size() reports");
+  const int rc = ready(stream);
+  if (rc != FUSEDCONV_OK) return rc;
+  GatedArgs a{};
+  a.dy = dy; a.x = x; a.gate = gate; a.up = up; a.down = down;
+  a.g = const_cast<void*>(g); a.u = const_cast<void*>(u);
+  a.dx = dx; a.dgate = dgate; a.dup = dup; a.ddown = ddown; a.ws = workspace; a.stream = stream;
+  return launched([&] {
+    return h->p.dtype == FUSEDCONV_F32   ? gated_backward_f32(h->p, h->plan, a)
+           : h->p.dtype == FUSEDCONV_F16 ? gated_backward_f16(h->p, h->plan, a)
+                                         : gated_backward_bf16(h->p, h->plan, a);
+  });
+}
+
+void fusedconv_gated_ffn_destroy(fusedconv_gated_ffn* h) { delete h; }
 
 }  // extern "C"

@@ -24,4 +24,40 @@ size_t qk_norm_workspace(const fusedconv_qk_norm_rotary_desc& d);
 int launch_qk_norm_forward(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a);
 int launch_qk_norm_backward(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a);
 
+// The gated feed-forward block.
+struct ProductPlan {
+  int32_t tile_rows;      // of a block: 256, 128 or 64
+  int32_t whole;          // tiles that one block computes; the others are split
+  int32_t splits;
+  int32_t tiles;
+  size_t part_bytes;
+};
+struct GatedProblem {
+  int32_t dtype;
+  int32_t m, c, f, o, act;
+  float alpha;
+  int64_t x_stride, dy_stride;  // elements
+};
+struct GatedPlan {
+  int32_t few;            // few rows: a wave streams rows of the weights
+  ProductPlan gate, down, hidden, input, weights;
+  // forward: h, then partial results; backward: dg, du, h, the scale, partial results
+  size_t hidden_bytes, forward_bytes, backward_bytes;
+};
+struct GatedArgs {
+  const void *x, *gate, *up, *down, *dy;
+  void *g, *u;            // forward: kept, or NULL; backward: read
+  void *y, *dx, *dgate, *dup, *ddown;
+  void* ws;
+  void* stream;
+};
+constexpr size_t kScaleBytes = 2048;  // maxima of dy's parts, the scale
+void plan_gated(const GatedProblem& p, GatedPlan& plan);
+int gated_forward_f32(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);
+int gated_forward_f16(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);
+int gated_forward_bf16(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);
+int gated_backward_f32(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);
+int gated_backward_f16(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);
+int gated_backward_bf16(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);
+
 }  // namespace fc

@@ -1,8 +1,8 @@
 /*
  * fusedconv_block.h -- C ABI of what a whole transformer block needs beside
- * fusedconv_transformer.h: norms of queries and keys with their rotation, and
- * their gradients.  Same library, same conventions, types, alignment and error
- * codes as there.
+ * fusedconv_transformer.h: norms of queries and keys with their rotation, the
+ * gated feed-forward block, and their gradients.  Same library, same conventions,
+ * types, alignment and error codes as there.
  */
 #ifndef FUSEDCONV_BLOCK_H
 #define FUSEDCONV_BLOCK_H
@@ -70,6 +70,53 @@ int fusedconv_qk_norm_rotary_backward(const fusedconv_qk_norm_rotary* h, const v
                                       float* dk_weight, void* workspace, size_t workspace_bytes,
                                       void* stream);
 void fusedconv_qk_norm_rotary_destroy(fusedconv_qk_norm_rotary* h);
+
+/* --------------------------------------------------- gated feed-forward block
+ *
+ *     g = x gate^T,  u = x up^T,  h = act(g) * u,  y = h down^T
+ * X is [rows][in], gate and up [hidden][in], down [out][hidden], Y [rows][out]:
+ * weights lie as a linear layer keeps them.  in, hidden and out are multiples of
+ * 8.  x_stride / dy_stride: elements from one row to the next (multiples of 16
+ * bytes); everything else is contiguous.  activation: "QuickGelu"
+ * (g * sigmoid(alpha * g); alpha 1 is SiLU), "Gelu", "FastGelu", "Sigmoid" or
+ * "Relu", as fusedconv_desc names them.  No biases.
+ *
+ * Backward, from g and u as the forward pass stored them (rounded to T):
+ *     dh = dy down,  dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u
+ *     dx = dg gate + du up,  dgate = dg^T x,  dup = du^T x,  ddown = dy^T h
+ * No atomics: the same call gives the same bits.  The weights' gradients are of T.
+ *
+ * Sums are fp32.  For 16-bit T the factors h, dg and du of the second products are
+ * rounded to T, as the inputs they meet are.  f16: h beyond 65504 is infinite; dg
+ * and du are rounded times a power of two that lifts dy's largest magnitude to
+ * 2^-6 or more, so that gradients of small dy keep their bits.
+ *
+ * Outputs overlap neither inputs nor each other.
+ */
+typedef struct fusedconv_gated_ffn_desc {
+  int32_t dtype;
+  int64_t rows, in, hidden, out;  /* rows >= 0; the others multiples of 8 */
+  int64_t x_stride, dy_stride;
+  const char* activation;
+  float alpha;                    /* QuickGelu's; finite */
+} fusedconv_gated_ffn_desc;
+
+typedef struct fusedconv_gated_ffn fusedconv_gated_ffn;
+
+int fusedconv_gated_ffn_create(const fusedconv_gated_ffn_desc* d, fusedconv_gated_ffn** out);
+int fusedconv_gated_ffn_workspace_size(const fusedconv_gated_ffn* h, size_t* forward_bytes,
+                                       size_t* backward_bytes);
+/* g, u: T [rows][hidden], kept for the backward pass, or both NULL. */
+int fusedconv_gated_ffn_forward(const fusedconv_gated_ffn* h, const void* x, const void* gate,
+                                const void* up, const void* down, void* y, void* g, void* u,
+                                void* workspace, size_t workspace_bytes, void* stream);
+/* dgate, dup: T [hidden][in]; ddown: T [out][hidden]; all three or none. */
+int fusedconv_gated_ffn_backward(const fusedconv_gated_ffn* h, const void* dy, const void* x,
+                                 const void* gate, const void* up, const void* down,
+                                 const void* g, const void* u, void* dx, void* dgate, void* dup,
+                                 void* ddown, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+void fusedconv_gated_ffn_destroy(fusedconv_gated_ffn* h);
 
 #ifdef __cplusplus
 }

@@ -1,8 +1,11 @@
 """64-bit definitions of a transformer block's further operators (norms of queries and keys with
-their rotation) and how far a 32-bit evaluation that rounds its result to T may be from them.  Plain
+their rotation, the gated feed-forward block) and how far a 32-bit evaluation that rounds its results
+(and, in the feed-forward block, the hidden factors of its products) to T may be from them.  Plain
 torch on the CPU, sharing no code with the kernels.  Bounds as in oracle/transformer.py: u is half a
 step of T (relative), e = 2^-24 half a step of float32, a sum of n products in float32 is off by at
 most n e times the sum of their magnitudes (first order)."""
+import math
+
 import torch
 
 from .transformer import E, _tiny, rotary, unit
@@ -56,3 +59,84 @@ def qk_norm_rotary_backward(dy, x, weight, positions, inv_freq, axes, interleave
     # a value's sum runs through all heads in the worst case
     b_dw = (rows + 8) * E * (e * v).abs().sum(over) + (b_e * v.abs() + e.abs() * b_v).sum(over)
     return (dx, (e * v).sum(over)), (limit + unit(x.dtype) * dx.abs() + _tiny(x.dtype), b_dw + 1e-30)
+
+
+# ------------------------------------------------------ gated feed-forward block
+
+def activation(name, alpha, v, fast):
+    """(value, slope) of a gate's activation in float64 and the limits of their 32-bit evaluation.
+    exp(z) is off by |z| e for its argument's rounding and a few steps; fast (16-bit types): twice that,
+    and the normal distribution function by 6e-7 (the formula's and its evaluation's part)."""
+    k = 2 if fast else 1
+    if name == "Relu":
+        on = (v > 0).double()
+        return v * on, on, torch.zeros_like(v), torch.zeros_like(v)
+    if name == "Gelu":
+        cdf = 0.5 * torch.erfc(-v / math.sqrt(2))
+        phi = torch.exp(-0.5 * v * v) / math.sqrt(2 * math.pi)
+        b_cdf = (6e-7 if fast else 0.0) + (v * v + 16) * E * cdf
+        b_phi = k * (v * v + 8) * E * phi
+        return (v * cdf, cdf + v * phi, v.abs() * b_cdf + E * (v * cdf).abs(),
+                b_cdf + v.abs() * b_phi + 2 * E * (cdf + (v * phi).abs()))
+    if name == "FastGelu":
+        c = math.sqrt(8 / math.pi)
+        z, dz = c * (v + 0.044715 * v ** 3), c * (1 + 3 * 0.044715 * v * v)
+    else:
+        c = alpha if name == "QuickGelu" else 1.0
+        z, dz = c * v, torch.full_like(v, c)
+    s, t = torch.sigmoid(z), torch.sigmoid(-z)
+    rel = k * (4 * z.abs() + 8) * E          # of s, and of t
+    if name == "Sigmoid":
+        return s, s * t, rel * s, (2 * rel + E) * s * t
+    fall = (v * s * t * dz).abs()
+    return v * s, s + v * s * t * dz, (rel + E) * (v * s).abs(), rel * s + (2 * rel + 8 * E) * fall + E * (s + fall)
+
+
+def gated_ffn(x, gate, up, down, name, alpha):
+    """((y, g, u), their limits) for x [rows, in], in float64."""
+    t, fast = x.dtype, x.dtype != torch.float32
+    v = unit(t) if fast else 0.0
+    small = 2.0 ** -25 if t == torch.float16 else 0.0   # a rounding below f16's normal range
+    x, gate, up, down = (w.double() for w in (x, gate, up, down))
+    c, f = x.shape[-1], down.shape[-1]
+    g, u = x @ gate.T, x @ up.T
+    b_g, b_u = (c + 2) * E * (x.abs() @ gate.abs().T), (c + 2) * E * (x.abs() @ up.abs().T)
+    value, _, b_value, _ = activation(name, alpha, g, fast)
+    h = value * u
+    b_h = (b_value + 1.2 * max(1.0, abs(alpha) if name == "QuickGelu" else 1.0) * b_g) * u.abs()
+    b_h = b_h + (value.abs() + b_value) * b_u + (E + v) * h.abs() + small
+    y = h @ down.T
+    b_y = b_h @ down.abs().T + (f + 2) * E * (h.abs() @ down.abs().T)
+    half, tiny = unit(t), _tiny(t)
+    return (y, g, u), (b_y + half * y.abs() + tiny, b_g + half * g.abs() + tiny, b_u + half * u.abs() + tiny)
+
+
+def gated_ffn_backward(dy, x, gate, up, down, g, u, name, alpha):
+    """((dx, dgate, dup, ddown), their limits) for the g and u given, in float64."""
+    t, fast = x.dtype, x.dtype != torch.float32
+    half, tiny = unit(t), _tiny(t)
+    v = half if fast else 0.0
+    # f16: dg and du are rounded times a power of two that lifts dy's largest value to 2^-6 at least
+    top = float(dy.abs().max()) if dy.numel() else 0.0
+    small = 2.0 ** -25 if t == torch.float16 else 0.0
+    small_d = min(small, 2.0 ** -19 * top) if t == torch.float16 else 0.0
+    dy, x, gate, up, down, g, u = (w.double() for w in (dy, x, gate, up, down, g, u))
+    m, o, f = x.shape[0], down.shape[0], down.shape[1]
+    dh = dy @ down
+    b_dh = (o + 2) * E * (dy.abs() @ down.abs())
+    value, slope, b_value, b_slope = activation(name, alpha, g, fast)
+    dg, du, h = dh * u * slope, dh * value, value * u
+    b_dg = b_dh * (u * slope).abs() + (dh.abs() + b_dh) * u.abs() * b_slope + (3 * E + v) * dg.abs() + small_d
+    b_du = b_dh * value.abs() + (dh.abs() + b_dh) * b_value + (2 * E + v) * du.abs() + small_d
+    b_h = b_value * u.abs() + (E + v) * h.abs() + small
+    dx = dg @ gate + du @ up
+    n = (2 * f + 2) * E
+    b_dx = (b_dg + n * dg.abs()) @ gate.abs() + (b_du + n * du.abs()) @ up.abs()
+    n = (m + 2) * E
+    out, limits = [dx], [b_dx]
+    for d, b, w in ((dg, b_dg, x), (du, b_du, x)):
+        out.append(d.T @ w)
+        limits.append((b + n * d.abs()).T @ w.abs())
+    out.append(dy.T @ h)
+    limits.append(dy.abs().T @ (b_h + n * h.abs()))
+    return out, [b + half * w.abs() + tiny for w, b in zip(out, limits)]
