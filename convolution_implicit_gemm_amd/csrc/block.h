@@ -26,7 +26,7 @@ int launch_qk_norm_backward(const fusedconv_qk_norm_rotary_desc& d, const QkArgs
 
 // The gated feed-forward block.
 struct ProductPlan {
-  int32_t tile_rows;      // of a block: 256, 128 or 64
+  int32_t tile_rows, tile_cols;  // of a block: 256 x 256; 256, 128 or 64 x 128
   int32_t whole;          // tiles that one block computes; the others are split
   int32_t splits;
   int32_t tiles;

@@ -194,17 +194,20 @@ __global__ __launch_bounds__(64) void k_gated_scale(const float* tops, int n, fl
 
 // ---------------------------------------------------------------- launches
 
-template <typename T, int FORM, int LB>
-int launch_tall(ProductK& k, const ProductPlan& plan, hipStream_t st) {
-  auto fn = k_product<T, LB, FORM>;
-  const int rc = set_max_dynamic_lds((const void*)fn, kProductLds<LB>);
+template <typename T, int FORM, int LB, int RB>
+int launch_shape(ProductK& k, const ProductPlan& plan, hipStream_t st) {
+  using S = Shape<T, LB, RB, FORM>;
+  void (*fn)(ProductK);
+  if constexpr (RB == 256) fn = k_product_turns<T, FORM>;
+  else fn = k_product<T, LB, FORM>;
+  const int rc = set_max_dynamic_lds((const void*)fn, S::kLds);
   if (rc != FUSEDCONV_OK) return rc;
   int tiles = 0;
   for (int i = 0; i < k.products; ++i) {
     Product& p = k.p[i];
     p.first = tiles;
     p.row_tiles = (p.rows + LB - 1) / LB;
-    p.col_tiles = (p.cols + (FORM == kGate ? 64 : kTileCols) - 1) / (FORM == kGate ? 64 : kTileCols);
+    p.col_tiles = (p.cols + S::CB - 1) / S::CB;
     tiles += p.row_tiles * p.col_tiles;
   }
   k.whole = plan.whole;
@@ -212,18 +215,19 @@ int launch_tall(ProductK& k, const ProductPlan& plan, hipStream_t st) {
   k.split_items = (tiles - plan.whole) * plan.splits;
   const int64_t blocks = xcd_grid(k.whole) + xcd_grid(k.split_items);
   if (blocks == 0) return FUSEDCONV_OK;
-  hipLaunchKernelGGL(fn, grid_of(blocks), dim3(256), kProductLds<LB>, st, k);
+  hipLaunchKernelGGL(fn, grid_of(blocks), dim3(64 * S::WAVES), S::kLds, st, k);
   if (k.split_items)
-    hipLaunchKernelGGL((k_product_join<T, LB, FORM>), grid_of((int64_t)(tiles - plan.whole) * (LB / 16)),
-                       dim3(256), 0, st, k);
+    hipLaunchKernelGGL((k_product_join<T, LB, RB, FORM>),
+                       grid_of((int64_t)(tiles - plan.whole) * (LB * RB / 2048)), dim3(256), 0, st, k);
   return hipPeekAtLastError() == hipSuccess ? FUSEDCONV_OK : FUSEDCONV_ERR_LAUNCH;
 }
 template <typename T, int FORM>
 int launch_product(ProductK k, const ProductPlan& plan, hipStream_t st) {
+  if (plan.tile_cols == 256) return launch_shape<T, FORM, 256, 256>(k, plan, st);
   switch (plan.tile_rows) {
-    case 256: return launch_tall<T, FORM, 256>(k, plan, st);
-    case 128: return launch_tall<T, FORM, 128>(k, plan, st);
-    default: return launch_tall<T, FORM, 64>(k, plan, st);
+    case 256: return launch_shape<T, FORM, 256, 128>(k, plan, st);
+    case 128: return launch_shape<T, FORM, 128, 128>(k, plan, st);
+    default: return launch_shape<T, FORM, 64, 128>(k, plan, st);
   }
 }
 

@@ -2,12 +2,11 @@
 //     out[l][r] = sum over k of L(l, k) R(r, k)
 // on the matrix cores, and what is done with it before it is stored.
 //
-// Either side lies in memory as rows of k ([l][k]) or as columns ([k][l]).  A
-// block of four waves owns LB x 128 results, a wave (LB / 2) x 64: its products
-// are 32 x 32 with R as the first operand, so that a lane holds four neighbouring
-// results of one row l.  Tiles of 64 bytes of k go from memory straight to LDS
-// through three buffers: while one is used, two are on their way, and the wait
-// leaves the newest in flight.
+// Either side lies in memory as rows of k ([l][k]) or as columns ([k][l]).  A wave
+// owns (LB / 2) x 64 results: its products are 32 x 32 with R as the first operand,
+// so that a lane holds four neighbouring results of one row l.  Tiles of 64 bytes of
+// k go from memory straight to LDS through three or five buffers: while one is used,
+// others are on their way, and the waits leave the newest in flight.
 //
 // Copies are buffer loads whose lanes outside a matrix have an offset outside the
 // buffer: those write zeros, so that edges of every axis, k included, take no
@@ -52,7 +51,7 @@ struct ProductK {
   int32_t products;
   int32_t whole;        // tiles that one block computes
   int32_t split_items, splits;  // the others' blocks; of one tile
-  float* part;          // [split_items][LB][128]
+  float* part;          // [split_items][LB][RB]
   // the hidden values, [m][f] of T
   void *g, *u, *h, *dg, *du;
   const float* scale;   // of dg and du: a power of two (NULL: 1)
@@ -254,16 +253,16 @@ __device__ __forceinline__ frag_t<T> load_terms(const T* tile, int step, int t) 
 
 // One side of a block's tile: SIZE rows (columns: COLS) of KB terms, 64 * SIZE
 // bytes of LDS.
-template <typename T, int SIZE, bool COLS>
+template <typename T, int SIZE, bool COLS, int WAVES>
 struct Side {
   static constexpr int KB = 64 / sizeof(T);
-  static constexpr int kCalls = SIZE / 64;  // copies of one wave
+  static constexpr int kCalls = SIZE / 16 / WAVES;  // copies of one wave
   using L = Tile<T, COLS ? SIZE : KB>;
   uint32_t off[kCalls];
 
   // Row of the LDS tile and term (of the stage) of this lane in copy i.
   static __device__ __forceinline__ int place(int wave, int i) {
-    return (wave + 4 * i) * 64 + (threadIdx.x & 63);
+    return (wave + WAVES * i) * 64 + (threadIdx.x & 63);
   }
   static __device__ __forceinline__ int lds_row(int wave, int i) { return place(wave, i) / L::NC; }
   static __device__ __forceinline__ int chunk(int wave, int i) {
@@ -289,11 +288,11 @@ struct Side {
     const Buffer from = buffer_at(base);
     if (terms >= KB) {
 #pragma unroll
-      for (int i = 0; i < kCalls; ++i) copy_buffer_to_lds(to + (wave + 4 * i) * 1024, off[i], from);
+      for (int i = 0; i < kCalls; ++i) copy_buffer_to_lds(to + (wave + WAVES * i) * 1024, off[i], from);
     } else {
 #pragma unroll
       for (int i = 0; i < kCalls; ++i)
-        copy_buffer_to_lds(to + (wave + 4 * i) * 1024, term(wave, i) < terms ? off[i] : kOutside, from);
+        copy_buffer_to_lds(to + (wave + WAVES * i) * 1024, term(wave, i) < terms ? off[i] : kOutside, from);
     }
   }
   // Operand of the 32 rows (columns) 32 * t .. of step `step`.
@@ -303,13 +302,23 @@ struct Side {
   }
 };
 
-constexpr int kTileCols = 128;
-template <int LB>
-constexpr int kStageBytes = (LB + kTileCols) * 64;
+// The two shapes of a block: LB x 128 results of four waves, two blocks to a compute
+// unit, each covering the other's waits and ends; and 256 x 256 of eight waves, which
+// read a quarter less per result.
+template <typename T, int LB, int RB, int FORM>
+struct Shape {
+  static constexpr bool LC = FORM == kWeights, RC = FORM >= kHidden;
+  static constexpr int WAVES = RB / 32, LT = LB / 64, KB = 64 / sizeof(T), STEPS = KB / 16;
+  static constexpr int CB = FORM == kGate ? RB / 2 : RB;  // columns of a tile
+  using SL = Side<T, LB, LC, WAVES>;
+  using SR = Side<T, RB, RC, WAVES>;
+  static constexpr int kCopies = SL::kCalls + SR::kCalls;  // of a wave and stage
+  static constexpr int kStage = (LB + RB) * 64;
+  static constexpr int kBuffers = RB == 256 ? 5 : 3;
+  static constexpr int kLds = kBuffers * kStage;
+};
 constexpr int kMeetRow = 68;  // floats of a row where a wave turns its results round
-template <int LB>
-constexpr int kProductLds = 3 * kStageBytes<LB>;
-static_assert(4 * 32 * kMeetRow * 4 <= kProductLds<64>);
+static_assert(4 * 32 * kMeetRow * 4 <= Shape<float, 64, 128, kDown>::kLds);
 
 // A tile's rows and columns: groups of 8 row tiles walk over the columns together,
 // so that blocks that run at one time on an XCD share both sides in its L2.
@@ -320,60 +329,58 @@ __device__ __forceinline__ void tile_place(const Product& p, int tile, int& row,
   col = in / rows;
 }
 
-template <typename T, int LB, int FORM>
-__global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
-  constexpr bool LC = FORM == kWeights, RC = FORM >= kHidden;
-  constexpr int KB = 64 / sizeof(T), STEPS = KB / 16, LT = LB / 64;
-  using SL = Side<T, LB, LC>;
-  using SR = Side<T, kTileCols, RC>;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
+// The tile of a block, or its share of one: what to copy, and where results go.
+template <typename T, int LB, int RB, int FORM>
+struct Work {
+  using S = Shape<T, LB, RB, FORM>;
+  Product p;
+  typename S::SL sl;
+  typename S::SR sr;
+  const char *lp, *rp, *lp2, *rp2;
+  int64_t l_step, r_step;
+  int wave, l0, r0, one, s0, s1;
+  bool partial;
+  float* part;
 
-  // the block's tile, or its share of one
-  int item = xcd_item(block_number(), a.whole), split = 0;
-  const int whole_blocks = (a.whole + 7) / 8 * 8;
-  bool partial = false;
-  if (block_number() >= whole_blocks) {
-    const int i = xcd_item(block_number() - whole_blocks, a.split_items);
-    if (i >= a.split_items) return;
-    partial = true;
-    split = i % a.splits;
-    item = a.whole + i / a.splits;
-  } else if (item >= a.whole) {
-    return;
+  __device__ __forceinline__ bool init(const ProductK& a) {
+    int item = xcd_item(block_number(), a.whole), split = 0;
+    const int whole_blocks = (a.whole + 7) / 8 * 8;
+    partial = block_number() >= whole_blocks;
+    if (partial) {
+      const int i = xcd_item(block_number() - whole_blocks, a.split_items);
+      if (i >= a.split_items) return false;
+      split = i % a.splits;
+      item = a.whole + i / a.splits;
+      part = a.part + (int64_t)i * LB * RB;
+    } else if (item >= a.whole) {
+      return false;
+    }
+    const int which = a.products > 1 ? (item >= a.p[1].first) + (a.products > 2 && item >= a.p[2].first) : 0;
+    p = a.p[which];
+    int row_tile, col_tile;
+    tile_place(p, item - p.first, row_tile, col_tile);
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    l0 = row_tile * LB;
+    r0 = col_tile * S::CB;
+    sl.init((uint32_t)p.ls, p.rows - l0, wave, false);
+    sr.init((uint32_t)p.rs, p.cols - r0, wave, FORM == kGate);
+    // kGate: a wave copies rows of gate or of up
+    const void* r = FORM == kGate && (wave & 2) ? p.r2 : p.r;
+    lp = (const char*)p.l + (S::LC ? (int64_t)l0 * sizeof(T) : l0 * p.ls);
+    rp = (const char*)r + (S::RC ? (int64_t)r0 * sizeof(T) : r0 * p.rs);
+    if constexpr (FORM == kInput) {
+      lp2 = (const char*)p.l2 + l0 * p.ls;
+      rp2 = (const char*)p.r2 + (int64_t)r0 * sizeof(T);
+    }
+    l_step = S::LC ? S::KB * p.ls : 64;
+    r_step = S::RC ? S::KB * p.rs : 64;
+    one = (p.depth + S::KB - 1) / S::KB;
+    const int stages = FORM == kInput ? 2 * one : one;
+    s0 = partial ? (int)((int64_t)stages * split / a.splits) : 0;
+    s1 = partial ? (int)((int64_t)stages * (split + 1) / a.splits) : stages;
+    return true;
   }
-  const int which = a.products > 1 ? (item >= a.p[1].first) + (a.products > 2 && item >= a.p[2].first) : 0;
-  const Product& p = a.p[which];
-  int row_tile, col_tile;
-  tile_place(p, item - p.first, row_tile, col_tile);
-
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int wl = wave & 1, wr = wave >> 1;
-  constexpr int CB = FORM == kGate ? 64 : kTileCols;  // columns of a tile
-  const int l0 = row_tile * LB, r0 = col_tile * CB;
-
-  SL sl;
-  SR sr;
-  sl.init((uint32_t)p.ls, p.rows - l0, wave, false);
-  sr.init((uint32_t)p.rs, p.cols - r0, wave, FORM == kGate);
-  // waves 0 and 1 copy rows of gate, 2 and 3 of up
-  const void* r_first = FORM == kGate && wave >= 2 ? p.r2 : p.r;
-  const char* lp = (const char*)p.l + (LC ? (int64_t)l0 * sizeof(T) : l0 * p.ls);
-  const char* rp = (const char*)r_first + (RC ? (int64_t)r0 * sizeof(T) : r0 * p.rs);
-  const char *lp2 = nullptr, *rp2 = nullptr;
-  if constexpr (FORM == kInput) {
-    lp2 = (const char*)p.l2 + l0 * p.ls;
-    rp2 = (const char*)p.r2 + (int64_t)r0 * sizeof(T);
-  }
-  const int64_t l_step = LC ? KB * p.ls : 64, r_step = RC ? KB * p.rs : 64;
-  const int one = (p.depth + KB - 1) / KB;
-  const int stages = FORM == kInput ? 2 * one : one;
-  const int s0 = partial ? (int)((int64_t)stages * split / a.splits) : 0;
-  const int s1 = partial ? (int)((int64_t)stages * (split + 1) / a.splits) : stages;
-
-  const uint32_t base = lds_offset(lds);
-  auto fetch = [&](int s, int buffer) {
-    const uint32_t to = base + buffer * kStageBytes<LB>;
+  __device__ __forceinline__ void fetch(uint32_t to, int s) const {
     const char *l = lp, *r = rp;
     if constexpr (FORM == kInput)
       if (s >= one) {
@@ -381,56 +388,30 @@ __global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
         l = lp2;
         r = rp2;
       }
-    sl.start(to, l + s * l_step, p.depth - s * KB, wave);
-    sr.start(to + LB * 64, r + s * r_step, p.depth - s * KB, wave);
-  };
-  f32x16 acc[2][LT];
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int t = 0; t < LT; ++t) acc[r][t] = zero16();
-  constexpr int kInFlight = SL::kCalls + SR::kCalls;
-  if (s0 < s1) fetch(s0, 0);
-  if (s0 + 1 < s1) fetch(s0 + 1, 1);
-  int buffer = 0;
-  for (int s = s0; s < s1; ++s) {
-    if (s + 1 < s1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kInFlight) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    lds_barrier();  // everyone's copies are there, and the buffer before this one is free
-    if (s + 2 < s1) fetch(s + 2, buffer == 0 ? 2 : buffer - 1);
-    const char* lt = lds + buffer * kStageBytes<LB>;
-    const char* rt = lt + LB * 64;
-#pragma unroll
-    for (int step = 0; step < STEPS; ++step) {
-      frag_t<T> r[2], l[LT];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) r[i] = SR::load(rt, 2 * wr + i, step);
-#pragma unroll
-      for (int i = 0; i < LT; ++i) l[i] = SL::load(lt, LT * wl + i, step);
-#pragma unroll
-      for (int i = 0; i < LT; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[j][i] = mma(r[j], l[i], acc[j][i]);
-    }
-    buffer = buffer == 2 ? 0 : buffer + 1;
+    sl.start(to, l + s * l_step, p.depth - s * S::KB, wave);
+    sr.start(to + LB * 64, r + s * r_step, p.depth - s * S::KB, wave);
   }
+};
 
-  // Turned round in LDS, 32 rows at a time, a wave by itself: a lane gets eight
-  // neighbouring results of a row.
-  lds_barrier();
-  float* meet = (float*)lds + wave * 32 * kMeetRow;
-  float* part = partial ? a.part + (int64_t)((item - a.whole) * a.splits + split) * LB * kTileCols : nullptr;
-  each_index<0, LT>([&](auto t) {
+// A wave's results, turned round in LDS 32 rows at a time, a wave by itself, so that
+// a lane gets eight neighbouring ones of a row.
+template <typename T, int LB, int RB, int FORM>
+__device__ __forceinline__ void finish_tile(const ProductK& a, const Work<T, LB, RB, FORM>& w,
+                                            const f32x16 (&acc)[2][LB / 64], char* lds) {
+  const Product& p = w.p;
+  const int lane = threadIdx.x & 63, h = lane >> 5, wl = w.wave & 1, wr = w.wave >> 1;
+  float* meet = (float*)lds + w.wave * 32 * kMeetRow;
+  each_index<0, LB / 64>([&](auto t) {
     const int row0 = wl * (LB / 2) + 32 * t;  // of the tile
     const int row8 = row0 + (lane >> 3), col8 = 64 * wr + 8 * (lane & 7);
     // dh's g and u are asked for first
     Held8<T> g[4], u[4];
     if constexpr (FORM == kHidden)
-      if (!partial)
+      if (!w.partial)
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-          if (l0 + row8 + 8 * n < p.rows && r0 + col8 < p.cols) {
-            const int64_t at = (int64_t)(l0 + row8 + 8 * n) * a.f + r0 + col8;
+          if (w.l0 + row8 + 8 * n < p.rows && w.r0 + col8 < p.cols) {
+            const int64_t at = (int64_t)(w.l0 + row8 + 8 * n) * a.f + w.r0 + col8;
             g[n].load((const T*)a.g + at);
             u[n].load((const T*)a.u + at);
           }
@@ -444,14 +425,14 @@ __global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
         store_piece<float, 4>(meet + (lane & 31) * kMeetRow + 32 * r + 8 * q + 4 * h, x);
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (FORM != kGate || partial) {
+    if (FORM != kGate || w.partial) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const int l = l0 + row8 + 8 * n, r = r0 + col8;
+        const int l = w.l0 + row8 + 8 * n, r = w.r0 + col8;
         float v[8];
         load8(meet + ((lane >> 3) + 8 * n) * kMeetRow + 8 * (lane & 7), v);
-        if (partial) {
-          store8(part + (row8 + 8 * n) * kTileCols + col8, v);
+        if (w.partial) {
+          store8(w.part + (row8 + 8 * n) * RB + col8, v);
         } else if (l < p.rows && r < p.cols) {
           if constexpr (FORM == kHidden) {
             float gv[8], uv[8];
@@ -467,7 +448,7 @@ __global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const int row = 16 * n + (lane >> 2), col = 8 * (lane & 3);
-        const int l = l0 + row0 + row, r = r0 + 32 * wr + col;
+        const int l = w.l0 + row0 + row, r = w.r0 + 32 * wr + col;
         float gv[8], uv[8];
         load8(meet + row * kMeetRow + col, gv);
         load8(meet + row * kMeetRow + 32 + col, uv);
@@ -478,39 +459,151 @@ __global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
   });
 }
 
-// Adds the shares of a tile up, in order, and stores them as k_product does.  A
-// block has 16 rows of a tile.
+// All operands of a wave in one stage, and their products.
+template <typename T, int LB, int RB, int FORM>
+struct Operands {
+  using S = Shape<T, LB, RB, FORM>;
+  frag_t<T> l[S::STEPS][S::LT], r[S::STEPS][2];
+  __device__ __forceinline__ void load(const char* stage, int wl, int wr) {
+#pragma unroll
+    for (int step = 0; step < S::STEPS; ++step) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) r[step][i] = S::SR::load(stage + LB * 64, 2 * wr + i, step);
+#pragma unroll
+      for (int i = 0; i < S::LT; ++i) l[step][i] = S::SL::load(stage, S::LT * wl + i, step);
+    }
+  }
+  __device__ __forceinline__ void use(f32x16 (&acc)[2][S::LT]) const {
+#pragma unroll
+    for (int step = 0; step < S::STEPS; ++step)
+#pragma unroll
+      for (int i = 0; i < S::LT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[j][i] = mma(r[step][j], l[step][i], acc[j][i]);
+  }
+};
+
 template <typename T, int LB, int FORM>
+__global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
+  using S = Shape<T, LB, 128, FORM>;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  Work<T, LB, 128, FORM> w;
+  if (!w.init(a)) return;
+  f32x16 acc[2][S::LT];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int t = 0; t < S::LT; ++t) acc[r][t] = zero16();
+  const uint32_t base = lds_offset(lds);
+  const int s1 = w.s1;
+  if (w.s0 < s1) w.fetch(base, w.s0);
+  if (w.s0 + 1 < s1) w.fetch(base + S::kStage, w.s0 + 1);
+  int buffer = 0;
+  for (int s = w.s0; s < s1; ++s) {
+    if (s + 1 < s1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::kCopies) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();  // everyone's copies are there, and the buffer before this one is free
+    if (s + 2 < s1) w.fetch(base + (buffer == 0 ? 2 : buffer - 1) * S::kStage, s + 2);
+    Operands<T, LB, 128, FORM> x;
+    x.load(lds + buffer * S::kStage, w.wave & 1, w.wave >> 1);
+    x.use(acc);
+    buffer = buffer == 2 ? 0 : buffer + 1;
+  }
+  lds_barrier();
+  finish_tile<T, LB, 128, FORM>(a, w, acc, lds);
+}
+
+// Eight waves, two to a SIMD, that take turns: waves 0 to 3 read a stage's operands
+// from LDS while waves 4 to 7 multiply, and the other way round.  Each half of a
+// turn ends at a barrier of the block; the second four begin one barrier later.  A
+// wave waits for its copies of the next stage before the barrier in front of its
+// products: by the time either four read that stage, both have passed it.  A buffer
+// is copied into after the barrier that follows its last reads.
+template <typename T, int FORM>
+__global__ __launch_bounds__(512, 2) void k_product_turns(ProductK a) {
+  using S = Shape<T, 256, 256, FORM>;
+  constexpr int D = S::kBuffers;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  Work<T, 256, 256, FORM> w;
+  if (!w.init(a)) return;
+  f32x16 acc[2][S::LT];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int t = 0; t < S::LT; ++t) acc[r][t] = zero16();
+  const uint32_t base = lds_offset(lds);
+  const int s0 = w.s0, s1 = w.s1;
+  auto turn = [] {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int n = 0; n < D - 1; ++n)
+    if (s0 + n < s1) w.fetch(base + n * S::kStage, s0 + n);
+  if (s0 + D - 1 <= s1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 2) * S::kCopies) : "memory");
+  else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  turn();
+  const bool later = w.wave >= 4;
+  if (later) turn();
+  int now = 0, next = D - 1;  // buffers of this stage and of the one to fetch
+  for (int s = s0; s < s1; ++s) {
+    Operands<T, 256, 256, FORM> x;
+    x.load(lds + now * S::kStage, w.wave & 1, w.wave >> 1);
+    if (s + D - 1 < s1) {
+      w.fetch(base + next * S::kStage, s + D - 1);
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((D - 2) * S::kCopies) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    }
+    turn();
+    __builtin_amdgcn_s_setprio(1);
+    x.use(acc);
+    __builtin_amdgcn_s_setprio(0);
+    turn();
+    now = now == D - 1 ? 0 : now + 1;
+    next = next == D - 1 ? 0 : next + 1;
+  }
+  if (!later) turn();
+  lds_barrier();
+  finish_tile<T, 256, 256, FORM>(a, w, acc, lds);
+}
+
+// Adds the shares of a tile up, in order, and stores them as k_product does.  A
+// block has 2048 results of a tile.
+template <typename T, int LB, int RB, int FORM>
 __global__ __launch_bounds__(256) void k_product_join(ProductK a) {
-  const int strips = LB / 16, item = a.whole + block_number() / strips;
+  constexpr int rows = 2048 / RB, strips = LB / rows, groups = RB / 8;
+  const int item = a.whole + block_number() / strips;
   if ((int64_t)(item - a.whole) * a.splits >= a.split_items) return;
   const int which = a.products > 1 ? (item >= a.p[1].first) + (a.products > 2 && item >= a.p[2].first) : 0;
   const Product& p = a.p[which];
   int row_tile, col_tile;
   tile_place(p, item - p.first, row_tile, col_tile);
-  const int row = block_number() % strips * 16 + (threadIdx.x >> 4), at = threadIdx.x & 15;
+  const int row = block_number() % strips * rows + threadIdx.x / groups, at = threadIdx.x % groups;
   const int l = row_tile * LB + row;
   if (l >= p.rows) return;
-  const float* part = a.part + ((int64_t)(item - a.whole) * a.splits * LB + row) * kTileCols;
+  const float* part = a.part + ((int64_t)(item - a.whole) * a.splits * LB + row) * RB;
   auto sum = [&](int col, float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     for (int s = 0; s < a.splits; ++s) {
       float x[8];
-      load8(part + (int64_t)s * LB * kTileCols + col, x);
+      load8(part + (int64_t)s * LB * RB + col, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += x[j];
     }
   };
   if constexpr (FORM == kGate) {
-    const int wr = at >> 2, col = 8 * (at & 3), r = col_tile * 64 + 32 * wr + col;
-    if (at >= 8 || r >= p.cols) return;
+    const int wr = at >> 2, col = 8 * (at & 3), r = col_tile * (RB / 2) + 32 * wr + col;
+    if (at >= RB / 16 || r >= p.cols) return;
     float g[8], u[8];
     sum(64 * wr + col, g);
     sum(64 * wr + 32 + col, u);
     finish_gate8<T>(a, l, r, g, u);
   } else {
-    const int r = col_tile * kTileCols + 8 * at;
+    const int r = col_tile * RB + 8 * at;
     if (r >= p.cols) return;
     float v[8];
     sum(8 * at, v);
