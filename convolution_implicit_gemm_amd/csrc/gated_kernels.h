@@ -126,11 +126,14 @@ __global__ __launch_bounds__(512) void k_gated_few(FewK a) {
   const int64_t at = (int64_t)m * a.cols + n;
   Piece<T, 4> o;
   if constexpr (TWO) {
-    const Curve<sizeof(T) == 2> curve(a.act, a.alpha);
     Piece<T, 4> g, u;
+    with_gate_act(a.act, [&](auto act) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o.v[j] = to_type<T>(gate_value<act, sizeof(T) == 2>(a.alpha, sum[0][j]) * sum[1][j]);
+    });
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      o.v[j] = to_type<T>(curve.value(sum[0][j]) * sum[1][j]);
       g.v[j] = to_type<T>(sum[0][j]);
       u.v[j] = to_type<T>(sum[1][j]);
     }
@@ -198,7 +201,7 @@ template <typename T, int FORM, int LB, int RB>
 int launch_shape(ProductK& k, const ProductPlan& plan, hipStream_t st) {
   using S = Shape<T, LB, RB, FORM>;
   void (*fn)(ProductK);
-  if constexpr (RB == 256) fn = k_product_turns<T, FORM>;
+  if constexpr (RB == 256) fn = k_product_wide<T, FORM>;
   else fn = k_product<T, LB, FORM>;
   const int rc = set_max_dynamic_lds((const void*)fn, S::kLds);
   if (rc != FUSEDCONV_OK) return rc;
@@ -215,7 +218,7 @@ int launch_shape(ProductK& k, const ProductPlan& plan, hipStream_t st) {
   k.split_items = (tiles - plan.whole) * plan.splits;
   const int64_t blocks = xcd_grid(k.whole) + xcd_grid(k.split_items);
   if (blocks == 0) return FUSEDCONV_OK;
-  hipLaunchKernelGGL(fn, grid_of(blocks), dim3(64 * S::WAVES), S::kLds, st, k);
+  hipLaunchKernelGGL(fn, grid_of(blocks), dim3(256), S::kLds, st, k);
   if (k.split_items)
     hipLaunchKernelGGL((k_product_join<T, LB, RB, FORM>),
                        grid_of((int64_t)(tiles - plan.whole) * (LB * RB / 2048)), dim3(256), 0, st, k);
@@ -223,7 +226,8 @@ int launch_shape(ProductK& k, const ProductPlan& plan, hipStream_t st) {
 }
 template <typename T, int FORM>
 int launch_product(ProductK k, const ProductPlan& plan, hipStream_t st) {
-  if (plan.tile_cols == 256) return launch_shape<T, FORM, 256, 256>(k, plan, st);
+  if constexpr (sizeof(T) == 2)
+    if (plan.tile_cols == 256) return launch_shape<T, FORM, 256, 256>(k, plan, st);
   switch (plan.tile_rows) {
     case 256: return launch_shape<T, FORM, 256, 128>(k, plan, st);
     case 128: return launch_shape<T, FORM, 128, 128>(k, plan, st);

@@ -17,7 +17,7 @@ struct TileCost {
   double stage[2], end;  // of a round: a stage (16-bit types, float32), the way out
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 256, {0.85, 8.6}, 5.0},
+    {256, 256, 256, {0.75, 0.0}, 5.0},
     {256, 128, 512, {1.1, 9.0}, 3.0},
     {128, 128, 512, {0.62, 4.7}, 1.5},
     {64, 128, 512, {0.40, 2.5}, 0.8},
@@ -30,6 +30,7 @@ ProductPlan plan_product(const GatedProblem& p, bool halved, int64_t stages, int
   ProductPlan best{};
   double best_time = 0;
   for (const TileCost& t : kTiles) {
+    if (wide && t.cols == 256) continue;
     int64_t tiles = 0;
     for (int i = 0; i < products; ++i)
       tiles += ceil_div(rows[i], t.rows) * ceil_div(cols[i], halved ? t.cols / 2 : t.cols);

@@ -4,9 +4,9 @@
 //
 // Either side lies in memory as rows of k ([l][k]) or as columns ([k][l]).  A wave
 // owns (LB / 2) x 64 results: its products are 32 x 32 with R as the first operand,
-// so that a lane holds four neighbouring results of one row l.  Tiles of 64 bytes of
-// k go from memory straight to LDS through three or five buffers: while one is used,
-// others are on their way, and the waits leave the newest in flight.
+// so that a lane holds four neighbouring results of one row l.  Tiles of 64 or
+// 128 bytes of k go from memory straight to LDS: while one is used, others are on
+// their way, and the waits leave the newest in flight.
 //
 // Copies are buffer loads whose lanes outside a matrix have an offset outside the
 // buffer: those write zeros, so that edges of every axis, k included, take no
@@ -63,56 +63,72 @@ struct ProductK {
 
 enum GateAct : int { kSigmoid = 0, kRelu, kQuickGelu, kGelu, kFastGelu };
 
-// The gate's activation and its derivative.  Sigmoid, v sigmoid(alpha v) and the
-// tanh form of Gelu (0.5 v (1 + tanh z) = v sigmoid(2 z)) are one formula with
-// z = v (c1 + c3 v^2), without a branch.  16-bit types take the hardware's
-// exponential and reciprocal and the short form of erfc, whose errors of about 1e-6
-// are far inside a step of theirs.
+// The gate's activation and its derivative.  The tanh form of Gelu is taken as
+// 0.5 v (1 + tanh z) = v sigmoid(2 z).  16-bit types take the hardware's exponential
+// and reciprocal, 1 - s for sigmoid(-z) and the short form of erfc, whose errors of
+// about 1e-6 are far inside a step of theirs.
 template <bool FAST>
-struct Curve {
-  float c1, c3;
-  int act;
-  __device__ __forceinline__ Curve(int a, float alpha)
-      : c1(a == kQuickGelu ? alpha : a == kFastGelu ? 1.5957691216057308f : 1.0f),
-        c3(a == kFastGelu ? 1.5957691216057308f * 0.044715f : 0.0f), act(a) {}
-  static __device__ __forceinline__ float sigmoid(float z) {
-    if constexpr (FAST) return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-    else return 1.0f / (1.0f + expf(-z));
+__device__ __forceinline__ float sigmoid_of(float z) {
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+  else return 1.0f / (1.0f + expf(-z));
+}
+template <int ACT, bool FAST>
+__device__ __forceinline__ float gate_value(float alpha, float v) {
+  if constexpr (ACT == kSigmoid) return sigmoid_of<FAST>(v);
+  if constexpr (ACT == kRelu) return v < 0.0f ? 0.0f : v;
+  if constexpr (ACT == kQuickGelu) return v * sigmoid_of<FAST>(alpha * v);
+  if constexpr (ACT == kFastGelu)
+    return v * sigmoid_of<FAST>(1.5957691216057308f * v * (1.0f + 0.044715f * v * v));
+  if constexpr (FAST) {
+    const float c = 0.5f * erfc_as(fabsf(v) * 0.70710678118654752f);
+    return v * (v < 0.0f ? c : 1.0f - c);
+  } else {
+    return v * (0.5f * erfcf(-0.70710678118654752f * v));
   }
-  static __device__ __forceinline__ float normal_cdf(float v) {
+}
+template <int ACT, bool FAST>
+__device__ __forceinline__ void gate_both(float alpha, float v, float& value, float& slope) {
+  if constexpr (ACT == kRelu) {
+    value = v < 0.0f ? 0.0f : v;
+    slope = v > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == kGelu) {
+    float cdf, phi;
     if constexpr (FAST) {
       const float c = 0.5f * erfc_as(fabsf(v) * 0.70710678118654752f);
-      return v < 0.0f ? c : 1.0f - c;
+      cdf = v < 0.0f ? c : 1.0f - c;
+      phi = __builtin_amdgcn_exp2f(-0.72134752044448170f * v * v);
     } else {
-      return 0.5f * erfcf(-0.70710678118654752f * v);
+      cdf = 0.5f * erfcf(-0.70710678118654752f * v);
+      phi = expf(-0.5f * v * v);
     }
-  }
-  // s with act(v) = v s, or s for the sigmoid itself
-  __device__ __forceinline__ float share(float v) const {
-    if (act == kGelu) return normal_cdf(v);
-    if (act == kRelu) return v > 0.0f ? 1.0f : 0.0f;
-    return sigmoid(bent(v));
-  }
-  __device__ __forceinline__ float bent(float v) const {  // (0 * v^2 may be NaN)
-    return v * (act == kFastGelu ? c1 + c3 * v * v : c1);
-  }
-  __device__ __forceinline__ float value(float v) const {
-    const float s = share(v);
-    return act == kSigmoid ? s : act == kRelu && v < 0.0f ? 0.0f : v * s;
-  }
-  __device__ __forceinline__ void both(float v, float& value, float& slope) const {
-    const float s = share(v);
-    value = act == kSigmoid ? s : act == kRelu && v < 0.0f ? 0.0f : v * s;
-    if (act == kGelu) {
-      slope = s + v * 0.39894228040143268f * (FAST ? __expf(-0.5f * v * v) : expf(-0.5f * v * v));
-    } else if (act == kRelu) {
-      slope = s;
-    } else {
-      const float fall = value * sigmoid(-bent(v));
-      slope = act == kSigmoid ? fall : s + fall * (act == kFastGelu ? c1 + 3.0f * c3 * v * v : c1);
+    value = v * cdf;
+    slope = cdf + v * 0.39894228040143268f * phi;
+  } else {
+    float z = v, dz = 1.0f;
+    if constexpr (ACT == kQuickGelu) {
+      z = alpha * v;
+      dz = alpha;
     }
+    if constexpr (ACT == kFastGelu) {
+      z = 1.5957691216057308f * v * (1.0f + 0.044715f * v * v);
+      dz = 1.5957691216057308f * (1.0f + 0.134145f * v * v);
+    }
+    const float s = sigmoid_of<FAST>(z), t = FAST ? 1.0f - s : sigmoid_of<FAST>(-z);
+    value = ACT == kSigmoid ? s : v * s;
+    slope = ACT == kSigmoid ? s * t : s + value * t * dz;
   }
-};
+}
+// f(tag) with the activation as a constant, once for several values.
+template <typename F>
+__device__ __forceinline__ void with_gate_act(int act, F&& f) {
+  switch (act) {
+    case kSigmoid: f(int_c<kSigmoid>{}); break;
+    case kRelu: f(int_c<kRelu>{}); break;
+    case kQuickGelu: f(int_c<kQuickGelu>{}); break;
+    case kGelu: f(int_c<kGelu>{}); break;
+    default: f(int_c<kFastGelu>{});
+  }
+}
 
 // ------------------------------------------------------------ what is stored
 
@@ -168,11 +184,12 @@ __device__ __forceinline__ void finish8(const ProductK& a, const Product& p, int
 template <typename T>
 __device__ __forceinline__ void finish_gate8(const ProductK& a, int l, int r, const float (&g)[8],
                                              const float (&u)[8]) {
-  const Curve<sizeof(T) == 2> curve(a.act, a.alpha);
   const int64_t at = (int64_t)l * a.f + r;
   float h[8];
+  with_gate_act(a.act, [&](auto act) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = curve.value(g[j]) * u[j];
+    for (int j = 0; j < 8; ++j) h[j] = gate_value<act, sizeof(T) == 2>(a.alpha, g[j]) * u[j];
+  });
   store8((T*)a.h + at, h);
   if (a.g) {
     store8((T*)a.g + at, g);
@@ -183,18 +200,19 @@ __device__ __forceinline__ void finish_gate8(const ProductK& a, int l, int r, co
 template <typename T>
 __device__ __forceinline__ void finish_hidden8(const ProductK& a, int l, int r, const float (&dh)[8],
                                                const float (&g)[8], const float (&u)[8]) {
-  const Curve<sizeof(T) == 2> curve(a.act, a.alpha);
   const int64_t at = (int64_t)l * a.f + r;
   const float scale = a.scale ? *a.scale : 1.0f;
   float dg[8], du[8], h[8];
+  with_gate_act(a.act, [&](auto act) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float value, slope;
-    curve.both(g[j], value, slope);
-    dg[j] = dh[j] * scale * u[j] * slope;
-    du[j] = dh[j] * scale * value;
-    h[j] = value * u[j];
-  }
+    for (int j = 0; j < 8; ++j) {
+      float value, slope;
+      gate_both<act, sizeof(T) == 2>(a.alpha, g[j], value, slope);
+      dg[j] = dh[j] * scale * u[j] * slope;
+      du[j] = dh[j] * scale * value;
+      h[j] = value * u[j];
+    }
+  });
   store8((T*)a.dg + at, dg);
   store8((T*)a.du + at, du);
   store8((T*)a.h + at, h);
@@ -251,18 +269,17 @@ __device__ __forceinline__ frag_t<T> load_terms(const T* tile, int step, int t) 
   }
 }
 
-// One side of a block's tile: SIZE rows (columns: COLS) of KB terms, 64 * SIZE
-// bytes of LDS.
-template <typename T, int SIZE, bool COLS, int WAVES>
+// One side of a block's tile: SIZE rows (columns: COLS) of BYTES of terms.
+template <typename T, int SIZE, bool COLS, int BYTES>
 struct Side {
-  static constexpr int KB = 64 / sizeof(T);
-  static constexpr int kCalls = SIZE / 16 / WAVES;  // copies of one wave
+  static constexpr int KB = BYTES / sizeof(T);
+  static constexpr int kCalls = SIZE * BYTES / 4096;  // copies of one wave
   using L = Tile<T, COLS ? SIZE : KB>;
   uint32_t off[kCalls];
 
   // Row of the LDS tile and term (of the stage) of this lane in copy i.
   static __device__ __forceinline__ int place(int wave, int i) {
-    return (wave + WAVES * i) * 64 + (threadIdx.x & 63);
+    return (wave + 4 * i) * 64 + (threadIdx.x & 63);
   }
   static __device__ __forceinline__ int lds_row(int wave, int i) { return place(wave, i) / L::NC; }
   static __device__ __forceinline__ int chunk(int wave, int i) {
@@ -288,12 +305,16 @@ struct Side {
     const Buffer from = buffer_at(base);
     if (terms >= KB) {
 #pragma unroll
-      for (int i = 0; i < kCalls; ++i) copy_buffer_to_lds(to + (wave + WAVES * i) * 1024, off[i], from);
+      for (int i = 0; i < kCalls; ++i) copy_buffer_to_lds(to + (wave + 4 * i) * 1024, off[i], from);
     } else {
 #pragma unroll
       for (int i = 0; i < kCalls; ++i)
-        copy_buffer_to_lds(to + (wave + WAVES * i) * 1024, term(wave, i) < terms ? off[i] : kOutside, from);
+        copy_buffer_to_lds(to + (wave + 4 * i) * 1024, term(wave, i) < terms ? off[i] : kOutside, from);
     }
+  }
+  // One copy of start().
+  __device__ __forceinline__ void copy(uint32_t to, Buffer from, int terms, int wave, int i) const {
+    copy_buffer_to_lds(to + (wave + 4 * i) * 1024, term(wave, i) < terms ? off[i] : kOutside, from);
   }
   // Operand of the 32 rows (columns) 32 * t .. of step `step`.
   static __device__ __forceinline__ frag_t<T> load(const char* tile, int t, int step) {
@@ -302,23 +323,23 @@ struct Side {
   }
 };
 
-// The two shapes of a block: LB x 128 results of four waves, two blocks to a compute
-// unit, each covering the other's waits and ends; and 256 x 256 of eight waves, which
-// read a quarter less per result.
+// The shapes of a block of four waves, LB x RB results: up to 256 x 128, two blocks
+// to a compute unit, each covering the other's waits and ends; and 256 x 256, one
+// block, which reads a third less from memory and from LDS per result.
 template <typename T, int LB, int RB, int FORM>
 struct Shape {
   static constexpr bool LC = FORM == kWeights, RC = FORM >= kHidden;
-  static constexpr int WAVES = RB / 32, LT = LB / 64, KB = 64 / sizeof(T), STEPS = KB / 16;
+  static constexpr int LT = LB / 64, BYTES = RB == 256 ? 128 : 64;  // BYTES: of a row in a stage
+  static constexpr int KB = BYTES / sizeof(T), STEPS = KB / 16;
   static constexpr int CB = FORM == kGate ? RB / 2 : RB;  // columns of a tile
-  using SL = Side<T, LB, LC, WAVES>;
-  using SR = Side<T, RB, RC, WAVES>;
+  using SL = Side<T, LB, LC, BYTES>;
+  using SR = Side<T, RB, RC, BYTES>;
   static constexpr int kCopies = SL::kCalls + SR::kCalls;  // of a wave and stage
-  static constexpr int kStage = (LB + RB) * 64;
-  static constexpr int kBuffers = RB == 256 ? 5 : 3;
-  static constexpr int kLds = kBuffers * kStage;
+  static constexpr int kStage = (LB + RB) * BYTES;
+  // three stages, or two and a side of a third
+  static constexpr int kLds = RB == 256 ? 2 * kStage + LB * BYTES : 3 * kStage;
 };
 constexpr int kMeetRow = 68;  // floats of a row where a wave turns its results round
-static_assert(4 * 32 * kMeetRow * 4 <= Shape<float, 64, 128, kDown>::kLds);
 
 // A tile's rows and columns: groups of 8 row tiles walk over the columns together,
 // so that blocks that run at one time on an XCD share both sides in its L2.
@@ -364,16 +385,15 @@ struct Work {
     r0 = col_tile * S::CB;
     sl.init((uint32_t)p.ls, p.rows - l0, wave, false);
     sr.init((uint32_t)p.rs, p.cols - r0, wave, FORM == kGate);
-    // kGate: a wave copies rows of gate or of up
-    const void* r = FORM == kGate && (wave & 2) ? p.r2 : p.r;
+    // kGate: a wave copies rows of gate or of up, or (256 columns) of both in turn
+    const void* r = FORM == kGate && RB == 128 && (wave & 2) ? p.r2 : p.r;
     lp = (const char*)p.l + (S::LC ? (int64_t)l0 * sizeof(T) : l0 * p.ls);
     rp = (const char*)r + (S::RC ? (int64_t)r0 * sizeof(T) : r0 * p.rs);
-    if constexpr (FORM == kInput) {
-      lp2 = (const char*)p.l2 + l0 * p.ls;
-      rp2 = (const char*)p.r2 + (int64_t)r0 * sizeof(T);
-    }
-    l_step = S::LC ? S::KB * p.ls : 64;
-    r_step = S::RC ? S::KB * p.rs : 64;
+    if constexpr (FORM == kInput) lp2 = (const char*)p.l2 + l0 * p.ls;
+    if constexpr (FORM == kInput) rp2 = (const char*)p.r2 + (int64_t)r0 * sizeof(T);
+    if constexpr (FORM == kGate) rp2 = (const char*)p.r2 + r0 * p.rs;
+    l_step = S::LC ? S::KB * p.ls : S::BYTES;
+    r_step = S::RC ? S::KB * p.rs : S::BYTES;
     one = (p.depth + S::KB - 1) / S::KB;
     const int stages = FORM == kInput ? 2 * one : one;
     s0 = partial ? (int)((int64_t)stages * split / a.splits) : 0;
@@ -393,62 +413,74 @@ struct Work {
   }
 };
 
-// A wave's results, turned round in LDS 32 rows at a time, a wave by itself, so that
-// a lane gets eight neighbouring ones of a row.
+// A wave's results, turned round in LDS, a wave by itself, so that a lane gets eight
+// neighbouring ones of a row: 32 or 64 rows of 64 columns at a time, then in a loop
+// over 8 rows (the code of an activation stands a few times only).
 template <typename T, int LB, int RB, int FORM>
 __device__ __forceinline__ void finish_tile(const ProductK& a, const Work<T, LB, RB, FORM>& w,
-                                            const f32x16 (&acc)[2][LB / 64], char* lds) {
+                                            const f32x16 (&acc)[RB / 64][LB / 64], char* lds) {
   const Product& p = w.p;
-  const int lane = threadIdx.x & 63, h = lane >> 5, wl = w.wave & 1, wr = w.wave >> 1;
-  float* meet = (float*)lds + w.wave * 32 * kMeetRow;
-  each_index<0, LB / 64>([&](auto t) {
-    const int row0 = wl * (LB / 2) + 32 * t;  // of the tile
-    const int row8 = row0 + (lane >> 3), col8 = 64 * wr + 8 * (lane & 7);
-    // dh's g and u are asked for first
-    Held8<T> g[4], u[4];
-    if constexpr (FORM == kHidden)
-      if (!w.partial)
+  const int lane = threadIdx.x & 63, h = lane >> 5, wl = w.wave & 1;
+  constexpr int LT = LB / 64, RP = RB / 128, AT = LT > 2 ? 2 : 1;  // AT: 32 rows each
+  static_assert(4 * 32 * AT * kMeetRow * 4 <= Shape<T, LB, RB, FORM>::kLds);
+  float* meet = (float*)lds + w.wave * 32 * AT * kMeetRow;
+  each_index<0, LT / AT * RP>([&](auto step) {
+    constexpr int t0 = step / RP * AT, pair = step % RP;
+    const int wr = RP * (w.wave >> 1) + pair;          // 64 columns of the tile
+    const int row0 = wl * (LB / 2) + 32 * t0;          // of the tile
+    each_index<0, AT>([&](auto t) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          if (w.l0 + row8 + 8 * n < p.rows && w.r0 + col8 < p.cols) {
-            const int64_t at = (int64_t)(w.l0 + row8 + 8 * n) * a.f + w.r0 + col8;
-            g[n].load((const T*)a.g + at);
-            u[n].load((const T*)a.u + at);
-          }
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+        for (int q = 0; q < 4; ++q) {
+          Piece<float, 4> x;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        Piece<float, 4> x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x.v[j] = acc[r][t][4 * q + j];
-        store_piece<float, 4>(meet + (lane & 31) * kMeetRow + 32 * r + 8 * q + 4 * h, x);
-      }
+          for (int j = 0; j < 4; ++j) x.v[j] = acc[2 * pair + r][t0 + t][4 * q + j];
+          store_piece<float, 4>(meet + (32 * t + (lane & 31)) * kMeetRow + 32 * r + 8 * q + 4 * h, x);
+        }
+    });
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (FORM != kGate || w.partial) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int l = w.l0 + row8 + 8 * n, r = w.r0 + col8;
+      const int row8 = row0 + (lane >> 3), col8 = 64 * wr + 8 * (lane & 7);
+      const int l8 = w.l0 + row8, r = w.r0 + col8;
+      const bool in = r < p.cols;
+      // dh's g and u of the next 8 rows are on their way
+      Held8<T> g, u;
+      auto ask = [&](int n, Held8<T>& g, Held8<T>& u) {
+        if constexpr (FORM == kHidden)
+          if (in && n < 4 * AT && l8 + 8 * n < p.rows && !w.partial) {
+            const int64_t at = (int64_t)(l8 + 8 * n) * a.f + r;
+            g.load((const T*)a.g + at);
+            u.load((const T*)a.u + at);
+          }
+      };
+      ask(0, g, u);
+#pragma unroll 1
+      for (int n = 0; n < 4 * AT; ++n) {
+        Held8<T> next_g, next_u;
+        ask(n + 1, next_g, next_u);
         float v[8];
         load8(meet + ((lane >> 3) + 8 * n) * kMeetRow + 8 * (lane & 7), v);
         if (w.partial) {
           store8(w.part + (row8 + 8 * n) * RB + col8, v);
-        } else if (l < p.rows && r < p.cols) {
+        } else if (in && l8 + 8 * n < p.rows) {
           if constexpr (FORM == kHidden) {
             float gv[8], uv[8];
-            g[n].values(gv);
-            u[n].values(uv);
-            finish_hidden8<T>(a, l, r, v, gv, uv);
+            g.values(gv);
+            u.values(uv);
+            finish_hidden8<T>(a, l8 + 8 * n, r, v, gv, uv);
           } else if constexpr (FORM != kGate) {
-            finish8<T>(a, p, l, r, v);
+            finish8<T>(a, p, l8 + 8 * n, r, v);
           }
         }
+        g = next_g;
+        u = next_u;
       }
     } else {
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int row = 16 * n + (lane >> 2), col = 8 * (lane & 3);
-        const int l = w.l0 + row0 + row, r = w.r0 + 32 * wr + col;
+      const int col = 8 * (lane & 3), r = w.r0 + 32 * wr + col;
+#pragma unroll 1
+      for (int n = 0; n < 2 * AT; ++n) {
+        const int row = 16 * n + (lane >> 2), l = w.l0 + row0 + row;
         float gv[8], uv[8];
         load8(meet + row * kMeetRow + col, gv);
         load8(meet + row * kMeetRow + 32 + col, uv);
@@ -458,30 +490,6 @@ __device__ __forceinline__ void finish_tile(const ProductK& a, const Work<T, LB,
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   });
 }
-
-// All operands of a wave in one stage, and their products.
-template <typename T, int LB, int RB, int FORM>
-struct Operands {
-  using S = Shape<T, LB, RB, FORM>;
-  frag_t<T> l[S::STEPS][S::LT], r[S::STEPS][2];
-  __device__ __forceinline__ void load(const char* stage, int wl, int wr) {
-#pragma unroll
-    for (int step = 0; step < S::STEPS; ++step) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) r[step][i] = S::SR::load(stage + LB * 64, 2 * wr + i, step);
-#pragma unroll
-      for (int i = 0; i < S::LT; ++i) l[step][i] = S::SL::load(stage, S::LT * wl + i, step);
-    }
-  }
-  __device__ __forceinline__ void use(f32x16 (&acc)[2][S::LT]) const {
-#pragma unroll
-    for (int step = 0; step < S::STEPS; ++step)
-#pragma unroll
-      for (int i = 0; i < S::LT; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[j][i] = mma(r[step][j], l[step][i], acc[j][i]);
-  }
-};
 
 template <typename T, int LB, int FORM>
 __global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
@@ -504,69 +512,124 @@ __global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier();  // everyone's copies are there, and the buffer before this one is free
     if (s + 2 < s1) w.fetch(base + (buffer == 0 ? 2 : buffer - 1) * S::kStage, s + 2);
-    Operands<T, LB, 128, FORM> x;
-    x.load(lds + buffer * S::kStage, w.wave & 1, w.wave >> 1);
-    x.use(acc);
+    const char* stage = lds + buffer * S::kStage;
+#pragma unroll
+    for (int step = 0; step < S::STEPS; ++step) {
+      frag_t<T> l[S::LT], r[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) r[i] = S::SR::load(stage + LB * 64, 2 * (w.wave >> 1) + i, step);
+#pragma unroll
+      for (int i = 0; i < S::LT; ++i) l[i] = S::SL::load(stage, S::LT * (w.wave & 1) + i, step);
+#pragma unroll
+      for (int i = 0; i < S::LT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[j][i] = mma(r[j], l[i], acc[j][i]);
+    }
     buffer = buffer == 2 ? 0 : buffer + 1;
   }
   lds_barrier();
   finish_tile<T, LB, 128, FORM>(a, w, acc, lds);
 }
 
-// Eight waves, two to a SIMD, that take turns: waves 0 to 3 read a stage's operands
-// from LDS while waves 4 to 7 multiply, and the other way round.  Each half of a
-// turn ends at a barrier of the block; the second four begin one barrier later.  A
-// wave waits for its copies of the next stage before the barrier in front of its
-// products: by the time either four read that stage, both have passed it.  A buffer
-// is copied into after the barrier that follows its last reads.
+// 256 x 256 results, 128 x 128 a wave, one wave to a SIMD: it has to keep the matrix
+// cores busy by itself.  A stage has 128 bytes of every row, whole lines (with 64 the
+// L2's requests were the limit: 8192 x 4096 x 11008: 628 us, with whole lines XXX),
+// and four steps of 16 products.  Between the products of a step the operands of the
+// next one are read and copies are started, so that none waits.  The order is written
+// out and kept (sched_barrier).
+// LDS holds five sides of stages, in turn L and R.  A stage's barrier stands in front
+// of its last step: behind it everyone's copies of the next stage have arrived, and
+// this stage's sides, whose last operands have been read, are free.  R of the stage
+// two on is copied into the one behind that barrier, L of the stage three on into the
+// other in the first two steps of the next stage.  Copies past the last stage write
+// zeros: the waits always count the same.
 template <typename T, int FORM>
-__global__ __launch_bounds__(512, 2) void k_product_turns(ProductK a) {
+__global__ __launch_bounds__(256, 1) void k_product_wide(ProductK a) {
   using S = Shape<T, 256, 256, FORM>;
-  constexpr int D = S::kBuffers;
+  static_assert(S::STEPS == 4 && S::LT == 4 && S::SL::kCalls == 8 && S::SR::kCalls == 8);
+  constexpr int kSide = 256 * S::BYTES;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   Work<T, 256, 256, FORM> w;
   if (!w.init(a)) return;
-  f32x16 acc[2][S::LT];
+  f32x16 acc[4][4];
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int t = 0; t < S::LT; ++t) acc[r][t] = zero16();
+    for (int t = 0; t < 4; ++t) acc[r][t] = zero16();
   const uint32_t base = lds_offset(lds);
-  const int s0 = w.s0, s1 = w.s1;
-  auto turn = [] {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+  const int s0 = w.s0, s1 = w.s1, wl = w.wave & 1, wr = w.wave >> 1;
+
+  // Copy i of a side of stage s; what it needs is worked out once a side.
+  Buffer from, from2;  // from2: kGate's second matrix
+  int terms;
+  auto prepare_l = [&](int s) {
+    const bool second = FORM == kInput && s >= w.one;
+    const int at = second ? s - w.one : s;
+    terms = s < s1 ? w.p.depth - at * S::KB : 0;
+    from = buffer_at((second ? w.lp2 : w.lp) + at * w.l_step);
+  };
+  auto prepare_r = [&](int s) {
+    const bool second = FORM == kInput && s >= w.one;
+    const int at = second ? s - w.one : s;
+    terms = s < s1 ? w.p.depth - at * S::KB : 0;
+    from = buffer_at((second ? w.rp2 : w.rp) + at * w.r_step);
+    if constexpr (FORM == kGate) from2 = buffer_at(w.rp2 + at * w.r_step);
+  };
+  auto copy_l = [&](uint32_t to, auto i) { w.sl.copy(to, from, terms, w.wave, i); };
+  auto copy_r = [&](uint32_t to, auto i) {
+    w.sr.copy(to, FORM == kGate && (i & 1) ? from2 : from, terms, w.wave, i);
+  };
+  // Operands in the order of their first use, two sets in turn.
+  frag_t<T> l[2][4], r[2][4];
+  auto read = [&](int side_l, int side_r, auto step, auto i) {
+    constexpr int set = step & 1;
+    const char *tl = lds + side_l * kSide, *tr = lds + side_r * kSide;
+    if constexpr (i == 0) r[set][0] = S::SR::load(tr, 4 * wr, step);
+    else if constexpr (i == 1) l[set][0] = S::SL::load(tl, 4 * wl, step);
+    else if constexpr (i < 5) r[set][i - 1] = S::SR::load(tr, 4 * wr + i - 1, step);
+    else l[set][i - 4] = S::SL::load(tl, 4 * wl + i - 4, step);
+  };
+  auto on = [](int side, int n) { return side + n < 5 ? side + n : side + n - 5; };
+
+  for (int n = 0; n < 2; ++n) {
+    prepare_l(s0 + n);
+    each_index<0, 8>([&](auto i) { copy_l(base + 2 * n * kSide, i); });
+    prepare_r(s0 + n);
+    each_index<0, 8>([&](auto i) { copy_r(base + (2 * n + 1) * kSide, i); });
+  }
+  asm volatile("s_waitcnt vmcnt(16)\n\ts_barrier" ::: "memory");
+  each_index<0, 8>([&](auto i) { read(0, 1, int_c<0>{}, i); });
+  // which operand is read and which copy is started before product n of a step
+  constexpr auto read_at = [](int n) { return n > 11 || n % 3 == 2 ? -1 : n / 3 * 2 + n % 3; };
+  constexpr auto copy_at = [](int n) { return n > 11 || n % 3 != 2 ? -1 : n / 3; };
+  auto multiply = [&](auto set, auto n) {
+    acc[n % 4][n / 4] = mma(r[set][n % 4], l[set][n / 4], acc[n % 4][n / 4]);
     __builtin_amdgcn_sched_barrier(0);
   };
-  for (int n = 0; n < D - 1; ++n)
-    if (s0 + n < s1) w.fetch(base + n * S::kStage, s0 + n);
-  if (s0 + D - 1 <= s1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 2) * S::kCopies) : "memory");
-  else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  turn();
-  const bool later = w.wave >= 4;
-  if (later) turn();
-  int now = 0, next = D - 1;  // buffers of this stage and of the one to fetch
+  int side = 0;  // where L of the stage lies
   for (int s = s0; s < s1; ++s) {
-    Operands<T, 256, 256, FORM> x;
-    x.load(lds + now * S::kStage, w.wave & 1, w.wave >> 1);
-    if (s + D - 1 < s1) {
-      w.fetch(base + next * S::kStage, s + D - 1);
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((D - 2) * S::kCopies) : "memory");
-    } else {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    }
-    turn();
-    __builtin_amdgcn_s_setprio(1);
-    x.use(acc);
-    __builtin_amdgcn_s_setprio(0);
-    turn();
-    now = now == D - 1 ? 0 : now + 1;
-    next = next == D - 1 ? 0 : next + 1;
+    const int side_r = on(side, 1), free = on(side, 4);
+    prepare_l(s + 2);
+    each_index<0, 3>([&](auto step) {
+      each_index<0, 16>([&](auto n) {
+        if constexpr (read_at(n) >= 0) read(side, side_r, int_c<step + 1>{}, int_c<read_at(n)>{});
+        if constexpr (step < 2 && copy_at(n) >= 0) copy_l(base + free * kSide, int_c<4 * step + copy_at(n)>{});
+        multiply(int_c<(step & 1)>{}, n);
+      });
+    });
+    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    prepare_r(s + 2);
+    const uint32_t to = base + side * kSide;
+    side = on(side, 2);
+    const int next_r = on(side, 1);
+    each_index<0, 16>([&](auto n) {
+      if constexpr (n % 2 == 0) read(side, next_r, int_c<0>{}, int_c<n / 2>{});
+      else copy_r(to, int_c<n / 2>{});
+      multiply(int_c<1>{}, n);
+    });
   }
-  if (!later) turn();
-  lds_barrier();
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   finish_tile<T, 256, 256, FORM>(a, w, acc, lds);
 }
 

@@ -86,10 +86,13 @@ def activation(name, alpha, v, fast):
         z, dz = c * v, torch.full_like(v, c)
     s, t = torch.sigmoid(z), torch.sigmoid(-z)
     rel = k * (4 * z.abs() + 8) * E          # of s, and of t
+    # fast: t = 1 - s, off by what s is and by e
+    b_t = rel * s + E if fast else rel * t
     if name == "Sigmoid":
-        return s, s * t, rel * s, (2 * rel + E) * s * t
+        return s, s * t, rel * s, rel * s * t + s * b_t + E * s * t
     fall = (v * s * t * dz).abs()
-    return v * s, s + v * s * t * dz, (rel + E) * (v * s).abs(), rel * s + (2 * rel + 8 * E) * fall + E * (s + fall)
+    return (v * s, s + v * s * t * dz, (rel + E) * (v * s).abs(),
+            rel * s + (rel + 8 * E) * fall + (v * s * dz).abs() * b_t + E * (s + fall))
 
 
 def gated_ffn(x, gate, up, down, name, alpha):
