@@ -25,6 +25,15 @@ int launch_qk_norm_forward(const fusedconv_qk_norm_rotary_desc& d, const QkArgs&
 int launch_qk_norm_backward(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a);
 
 // The gated feed-forward block.
+// What a launch computes; the products of the block (m rows, c in, f hidden, o out):
+enum ProductForm : int {
+  kGate = 0,  // g = x gate^T, u = x up^T: act(g) * u        L rows, R rows (two matrices)
+  kDown,      // y = h down^T                                L rows, R rows
+  kHidden,    // dh = dy down: dg, du and h                  L rows, R columns
+  kInput,     // dx = dg gate + du up                        L rows, R columns (two terms)
+  kWeights    // dgate = dg^T x, dup = du^T x, ddown = dy^T h  L columns, R columns
+};
+
 struct ProductPlan {
   int32_t tile_rows, tile_cols;  // of a block: 256 x 256; 256, 128 or 64 x 128
   int32_t whole;          // tiles that one block computes; the others are split

@@ -226,7 +226,7 @@ int launch_shape(ProductK& k, const ProductPlan& plan, hipStream_t st) {
 }
 template <typename T, int FORM>
 int launch_product(ProductK k, const ProductPlan& plan, hipStream_t st) {
-  if constexpr (sizeof(T) == 2)
+  if constexpr (sizeof(T) == 2 && FORM != kHidden)
     if (plan.tile_cols == 256) return launch_shape<T, FORM, 256, 256>(k, plan, st);
   switch (plan.tile_rows) {
     case 256: return launch_shape<T, FORM, 256, 128>(k, plan, st);

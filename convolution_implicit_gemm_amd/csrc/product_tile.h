@@ -26,15 +26,6 @@
 
 namespace fc {
 
-// What a launch computes; the products of the block (m rows, c in, f hidden, o out):
-enum ProductForm : int {
-  kGate = 0,  // g = x gate^T, u = x up^T: act(g) * u        L rows, R rows (two matrices)
-  kDown,      // y = h down^T                                L rows, R rows
-  kHidden,    // dh = dy down: dg, du and h                  L rows, R columns
-  kInput,     // dx = dg gate + du up                        L rows, R columns (two terms)
-  kWeights    // dgate = dg^T x, dup = du^T x, ddown = dy^T h  L columns, R columns
-};
-
 struct Product {
   const void *l, *r;    // first term
   const void *l2, *r2;  // kInput: the second; kGate: r2 is up
@@ -414,77 +405,98 @@ struct Work {
 };
 
 // A wave's results, turned round in LDS, a wave by itself, so that a lane gets eight
-// neighbouring ones of a row: 32 or 64 rows of 64 columns at a time, then in a loop
-// over 8 rows (the code of an activation stands a few times only).
+// neighbouring ones of a row: whole lines are stored (from the registers as they are,
+// 32 bytes of a row at a time, the products of a block took up to a third longer).
+// Some rows of COLS columns at a time, then a loop over them (the code of an
+// activation stands a few times only).
 template <typename T, int LB, int RB, int FORM>
 __device__ __forceinline__ void finish_tile(const ProductK& a, const Work<T, LB, RB, FORM>& w,
                                             const f32x16 (&acc)[RB / 64][LB / 64], char* lds) {
   const Product& p = w.p;
   const int lane = threadIdx.x & 63, h = lane >> 5, wl = w.wave & 1;
-  constexpr int LT = LB / 64, RP = RB / 128, AT = LT > 2 ? 2 : 1;  // AT: 32 rows each
-  static_assert(4 * 32 * AT * kMeetRow * 4 <= Shape<T, LB, RB, FORM>::kLds);
-  float* meet = (float*)lds + w.wave * 32 * AT * kMeetRow;
+  // kGate has g and u of a value side by side: with 256 columns, 64 of each
+  constexpr int COLS = FORM == kGate && RB == 256 ? 128 : 64, CT = COLS / 32;
+  constexpr int LT = LB / 64, RP = RB / 2 / COLS, AT = LT > 2 && COLS == 64 ? 2 : 1;  // AT: 32 rows each
+  constexpr int ROW = COLS + 4;  // floats
+  static_assert(4 * 32 * AT * ROW * 4 <= Shape<T, LB, RB, FORM>::kLds);
+  float* meet = (float*)lds + w.wave * 32 * AT * ROW;
   each_index<0, LT / AT * RP>([&](auto step) {
-    constexpr int t0 = step / RP * AT, pair = step % RP;
-    const int wr = RP * (w.wave >> 1) + pair;          // 64 columns of the tile
-    const int row0 = wl * (LB / 2) + 32 * t0;          // of the tile
+    constexpr int t0 = step / RP * AT, part = step % RP;
+    const int col0 = (RP * (w.wave >> 1) + part) * COLS;  // of the tile
+    const int row0 = wl * (LB / 2) + 32 * t0;             // of the tile
     each_index<0, AT>([&](auto t) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < CT; ++r) {
+        // two products of 32 columns are g's and u's in turn
+        const int to = FORM == kGate ? (r & 1) * (COLS / 2) + (r >> 1) * 32 : 32 * r;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           Piece<float, 4> x;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x.v[j] = acc[2 * pair + r][t0 + t][4 * q + j];
-          store_piece<float, 4>(meet + (32 * t + (lane & 31)) * kMeetRow + 32 * r + 8 * q + 4 * h, x);
+          for (int j = 0; j < 4; ++j) x.v[j] = acc[CT * part + r][t0 + t][4 * q + j];
+          store_piece<float, 4>(meet + (32 * t + (lane & 31)) * ROW + to + 8 * q + 4 * h, x);
         }
+      }
     });
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (FORM != kGate || w.partial) {
-      const int row8 = row0 + (lane >> 3), col8 = 64 * wr + 8 * (lane & 7);
-      const int l8 = w.l0 + row8, r = w.r0 + col8;
-      const bool in = r < p.cols;
-      // dh's g and u of the next 8 rows are on their way
-      Held8<T> g, u;
-      auto ask = [&](int n, Held8<T>& g, Held8<T>& u) {
-        if constexpr (FORM == kHidden)
-          if (in && n < 4 * AT && l8 + 8 * n < p.rows && !w.partial) {
-            const int64_t at = (int64_t)(l8 + 8 * n) * a.f + r;
-            g.load((const T*)a.g + at);
-            u.load((const T*)a.u + at);
-          }
-      };
-      ask(0, g, u);
-#pragma unroll 1
-      for (int n = 0; n < 4 * AT; ++n) {
-        Held8<T> next_g, next_u;
-        ask(n + 1, next_g, next_u);
+    if (w.partial) {
+      // a share: [LB][RB] as they lie here
+      constexpr int LANES = COLS / 8, ROWS = 64 / LANES;
+#pragma unroll 2
+      for (int n = 0; n < 32 * AT / ROWS; ++n) {
+        const int row = ROWS * n + lane / LANES, col = 8 * (lane % LANES);
         float v[8];
-        load8(meet + ((lane >> 3) + 8 * n) * kMeetRow + 8 * (lane & 7), v);
-        if (w.partial) {
-          store8(w.part + (row8 + 8 * n) * RB + col8, v);
-        } else if (in && l8 + 8 * n < p.rows) {
-          if constexpr (FORM == kHidden) {
-            float gv[8], uv[8];
-            g.values(gv);
-            u.values(uv);
-            finish_hidden8<T>(a, l8 + 8 * n, r, v, gv, uv);
-          } else if constexpr (FORM != kGate) {
-            finish8<T>(a, p, l8 + 8 * n, r, v);
-          }
-        }
-        g = next_g;
-        u = next_u;
+        load8(meet + row * ROW + col, v);
+        store8(w.part + (row0 + row) * RB + col0 + col, v);
       }
+    } else if constexpr (FORM == kGate) {
+      constexpr int LANES = COLS / 16, ROWS = 64 / LANES;
+      const int col = 8 * (lane % LANES), r = w.r0 + col0 / 2 + col;
+      if (r < p.cols)
+#pragma unroll 2
+        for (int n = 0; n < 32 * AT / ROWS; ++n) {
+          const int row = ROWS * n + lane / LANES, l = w.l0 + row0 + row;
+          float gv[8], uv[8];
+          load8(meet + row * ROW + col, gv);
+          load8(meet + row * ROW + COLS / 2 + col, uv);
+          if (l < p.rows) finish_gate8<T>(a, l, r, gv, uv);
+        }
     } else {
-      const int col = 8 * (lane & 3), r = w.r0 + 32 * wr + col;
+      const int row = lane >> 3, col = 8 * (lane & 7), l = w.l0 + row0 + row, r = w.r0 + col0 + col;
+      const bool in = r < p.cols;
+      const float* from = meet + row * ROW + col;
+      if constexpr (FORM == kHidden) {
+        // g and u of the next 8 rows are on their way
+        Held8<T> g[2], u[2];
+        auto ask = [&](int n, auto i) {
+          if (in && n < 4 * AT && l + 8 * n < p.rows) {
+            const int64_t at = (int64_t)(l + 8 * n) * a.f + r;
+            g[i].load((const T*)a.g + at);
+            u[i].load((const T*)a.u + at);
+          }
+        };
+        auto use = [&](int n, auto i) {
+          float v[8], gv[8], uv[8];
+          load8(from + 8 * n * ROW, v);
+          g[i].values(gv);
+          u[i].values(uv);
+          if (in && l + 8 * n < p.rows) finish_hidden8<T>(a, l + 8 * n, r, v, gv, uv);
+        };
+        ask(0, int_c<0>{});
 #pragma unroll 1
-      for (int n = 0; n < 2 * AT; ++n) {
-        const int row = 16 * n + (lane >> 2), l = w.l0 + row0 + row;
-        float gv[8], uv[8];
-        load8(meet + row * kMeetRow + col, gv);
-        load8(meet + row * kMeetRow + 32 + col, uv);
-        if (l < p.rows && r < p.cols) finish_gate8<T>(a, l, r, gv, uv);
+        for (int n = 0; n < 4 * AT; n += 2) {
+          ask(n + 1, int_c<1>{});
+          use(n, int_c<0>{});
+          ask(n + 2, int_c<0>{});
+          use(n + 1, int_c<1>{});
+        }
+      } else if (in) {
+#pragma unroll
+        for (int n = 0; n < 4 * AT; ++n) {
+          float v[8];
+          load8(from + 8 * n * ROW, v);
+          if (l + 8 * n < p.rows) finish8<T>(a, p, l + 8 * n, r, v);
+        }
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -659,11 +671,13 @@ __global__ __launch_bounds__(256) void k_product_join(ProductK a) {
     }
   };
   if constexpr (FORM == kGate) {
-    const int wr = at >> 2, col = 8 * (at & 3), r = col_tile * (RB / 2) + 32 * wr + col;
+    // COLS columns of a share are half g's, half u's, as finish_tile has them
+    constexpr int HALF = RB == 256 ? 64 : 32;
+    const int r = col_tile * (RB / 2) + 8 * at, from = 8 * at / HALF * 2 * HALF + 8 * at % HALF;
     if (at >= RB / 16 || r >= p.cols) return;
     float g[8], u[8];
-    sum(64 * wr + col, g);
-    sum(64 * wr + 32 + col, u);
+    sum(from, g);
+    sum(from + HALF, u);
     finish_gate8<T>(a, l, r, g, u);
   } else {
     const int r = col_tile * RB + 8 * at;
