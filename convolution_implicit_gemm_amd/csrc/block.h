@@ -60,7 +60,7 @@ struct GatedArgs {
   void* ws;
   void* stream;
 };
-constexpr size_t kScaleBytes = 2048;  // maxima of dy's parts, the scale
+constexpr size_t kScaleBytes = 8192;  // maxima of dy's parts, the scale
 void plan_gated(const GatedProblem& p, GatedPlan& plan);
 int gated_forward_f32(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);
 int gated_forward_f16(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);

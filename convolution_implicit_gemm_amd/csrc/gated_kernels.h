@@ -53,7 +53,7 @@ struct FewK {
 };
 
 template <typename T, int MT, bool TWO>
-__global__ __launch_bounds__(512) void k_gated_few(FewK a) {
+__global__ __launch_bounds__(TWO ? 512 : 1024) void k_gated_few(FewK a) {
   constexpr int NW = TWO ? 2 : 1, U = 4;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -154,6 +154,9 @@ int launch_few(const FewK& k, hipStream_t st) {
   const int steps = (int)(((int64_t)k.depth * sizeof(T) + 63) / 64);
   // about eight waves to a compute unit, each with terms to sum
   int waves = blocks >= 512 ? 4 : 8;
+#ifdef FC_EXPERIMENT
+  if (const char* e = getenv(TWO ? "FCW2" : "FCW1")) waves = atoi(e);
+#endif
   while (waves > 2 && waves * 4 > steps) waves /= 2;
   const int mt = k.rows > 16 ? 2 : 1;
   const size_t lds = (size_t)waves * (TWO ? 2 : 1) * mt * 1024;
@@ -165,25 +168,32 @@ int launch_few(const FewK& k, hipStream_t st) {
 // ------------------------------------------------------------ the scale of dy
 
 // Largest magnitudes of dy's parts, one a block; infinite and NaN values count as 0.
+// A wave takes rows, four at a time in flight.
+constexpr int kTops = 1024;  // parts at most
 template <typename T>
 __global__ __launch_bounds__(256) void k_gated_tops(const T* dy, int64_t stride, int32_t rows, int32_t cols,
                                                     float* tops) {
   __shared__ float meet[4];
   constexpr int P = 16 / sizeof(T);
-  const int per = cols / P;
+  const int per = cols / P, waves = 4 * gridDim.x, lane = threadIdx.x & 63;
   float top = 0.f;
-  for (int row = blockIdx.x; row < rows; row += gridDim.x)
-    for (int i = threadIdx.x; i < per; i += 256) {
-      const Piece<T, P> x = load_piece<T, P>(dy + row * stride + i * P);
+  for (int64_t row = 4 * blockIdx.x + (threadIdx.x >> 6); row < rows; row += 4 * waves)
+    for (int i = lane; i < per; i += 64) {
+      Piece<T, P> x[4];
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const float v = fabsf((float)x.v[j]);
-        if (v < INFINITY) top = fmaxf(top, v);
-      }
+      for (int n = 0; n < 4; ++n)  // past the end: the row itself again
+        x[n] = load_piece<T, P>(dy + (row + n * waves < rows ? row + n * waves : row) * stride + i * P);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float v = fabsf((float)x[n].v[j]);
+          if (v < INFINITY) top = fmaxf(top, v);
+        }
     }
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
-  if ((threadIdx.x & 63) == 0) meet[threadIdx.x >> 6] = top;
+  if (lane == 0) meet[threadIdx.x >> 6] = top;
   __syncthreads();
   if (threadIdx.x == 0) tops[blockIdx.x] = fmaxf(fmaxf(meet[0], meet[1]), fmaxf(meet[2], meet[3]));
 }
@@ -275,16 +285,17 @@ int backward(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a) {
   k.dg = ws;
   k.du = ws + plan.hidden_bytes;
   k.h = ws + 2 * plan.hidden_bytes;
+  static_assert((kTops + 1) * sizeof(float) <= kScaleBytes);
   float* tops = (float*)(ws + 3 * plan.hidden_bytes);
   k.part = (float*)(ws + 3 * plan.hidden_bytes + kScaleBytes);
   int rc = FUSEDCONV_OK;
   if (p.m > 0) {
     if constexpr (std::is_same<T, _Float16>::value) {
-      const int blocks = p.m < 256 ? p.m : 256;
+      const int blocks = p.m < 4 * kTops ? (p.m + 3) / 4 : kTops;
       hipLaunchKernelGGL((k_gated_tops<T>), dim3(blocks), dim3(256), 0, st, (const T*)a.dy, p.dy_stride, p.m,
                          p.o, tops);
-      hipLaunchKernelGGL(k_gated_scale, dim3(1), dim3(64), 0, st, tops, blocks, tops + 256);
-      k.scale = tops + 256;
+      hipLaunchKernelGGL(k_gated_scale, dim3(1), dim3(64), 0, st, tops, blocks, tops + kTops);
+      k.scale = tops + kTops;
     }
     k.p[0] = Product{a.dy, a.down, nullptr, nullptr, nullptr, p.dy_stride * es, p.f * es, p.m, p.f, p.o};
     rc = launch_product<T, kHidden>(k, plan.hidden, st);

@@ -11,9 +11,9 @@
 // of a group runs over lanes without LDS.  Cosines and sines of a block's tokens
 // are made once for all heads, in LDS (turns.h).
 //
-// The weights' gradients: a lane keeps the sums of its 16 values over all heads
-// and tokens of its block; blocks walk over the tokens, and a second launch adds
-// their sums in a fixed order.
+// The weights' gradients: a lane sums its 16 values up over the heads of some
+// tokens, and keeps the sums of all its block's tokens in LDS; blocks walk over the
+// tokens, and a second launch adds their sums in a fixed order.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -32,7 +32,7 @@ struct QkSide {  // q, or k
   const void *x, *w, *dy;
   void* y;
   int64_t xs[3], ys[3], ds[3];
-  FastDiv heads;  // d = 0: there is no k
+  FastDiv heads;
 };
 
 struct QkK {
@@ -42,7 +42,7 @@ struct QkK {
   const int32_t* axes;
   float* part;
   int64_t pos_batch;
-  int32_t tokens, pairs, num_axes, pos_type, tok, d;
+  int32_t tokens, pairs, num_axes, pos_type, tok, d, sides;
   int32_t lanes;                 // of a group
   int32_t turned, pieces;        // pieces (of a half, interleaved: in all) that turn; in all
   int32_t chunks;                // of tok tokens
@@ -51,23 +51,23 @@ struct QkK {
 };
 
 // The pieces of item i of a head: where they begin, whether there are any, and
-// whether they turn.
+// whether they turn.  FULL: every lane's items are whole pairs of pieces that turn.
 struct Item {
   int at[2];
   bool on[2], turn;
   int pair;  // the first pair
 };
-template <int W, bool INTER>
+template <int W, bool INTER, bool FULL>
 __device__ __forceinline__ Item item_of(const QkK& a, int i) {
   Item m;
   if constexpr (INTER) {  // pieces 2i, 2i + 1, each turned by itself
     m.at[0] = 2 * i * W;
     m.at[1] = m.at[0] + W;
-    m.on[0] = 2 * i < a.pieces;
-    m.on[1] = 2 * i + 1 < a.pieces;
+    m.on[0] = FULL || 2 * i < a.pieces;
+    m.on[1] = FULL || 2 * i + 1 < a.pieces;
     m.turn = false;  // by position, below
     m.pair = i * W;
-  } else if (i < a.turned) {
+  } else if (FULL || i < a.turned) {
     m.at[0] = i * W;
     m.at[1] = a.pairs + i * W;
     m.on[0] = m.on[1] = m.turn = true;
@@ -85,12 +85,12 @@ __device__ __forceinline__ Item item_of(const QkK& a, int i) {
 }
 
 // (x, y) of every pair of an item turned by SIGN times its angle.
-template <int W, bool INTER, int SIGN>
+template <int W, bool INTER, bool FULL, int SIGN>
 __device__ __forceinline__ void turn_item(const QkK& a, const Item& m, const float2* cs, float* v) {
   if constexpr (INTER) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
-      if (m.at[p] < 2 * a.pairs)
+      if (FULL || m.at[p] < 2 * a.pairs)
 #pragma unroll
         for (int j = 0; j < W; j += 2) {
           const float2 c = cs[(m.at[p] + j) >> 1];
@@ -99,7 +99,7 @@ __device__ __forceinline__ void turn_item(const QkK& a, const Item& m, const flo
           v[p * W + j + 1] = y * c.x + x * s;
         }
   } else {
-    if (m.turn)
+    if (FULL || m.turn)
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const float2 c = cs[m.pair + j];
@@ -120,58 +120,62 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
+// A lane's values of a head, as they were loaded.
 template <typename T, int W>
 struct Held {
   Piece<T, W> p[kHeld / W];
+  __device__ __forceinline__ void values(float (&v)[kHeld]) const {
+#pragma unroll
+    for (int n = 0; n < kHeld / W; ++n)
+#pragma unroll
+      for (int j = 0; j < W; ++j) v[n * W + j] = (float)p[n].v[j];
+  }
 };
 
-template <typename T, int W, bool INTER, bool BACK>
+template <typename T, int W, bool INTER, bool FULL, bool BACK>
 __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
   constexpr int N = kHeld / (2 * W);  // items of a lane
-  extern __shared__ float2 table[];   // [tok][pairs]; backward, at the end: the lanes' sums
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  // backward: the lanes' sums [q, k][kHeld / 4][256][4], then (both) [tok][pairs]
+  float* kept = (float*)lds;
+  float2* table = (float2*)(lds + (BACK ? 2 * kHeld * 256 * sizeof(float) : 0));
   const int group = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes;
   const int groups = 256 / a.lanes;
   Item items[N];
 #pragma unroll
-  for (int n = 0; n < N; ++n) items[n] = item_of<W, INTER>(a, lane + n * a.lanes);
+  for (int n = 0; n < N; ++n) items[n] = item_of<W, INTER, FULL>(a, lane + n * a.lanes);
 
   auto load = [&](const T* x, Held<T, W>& h) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        if (items[n].on[p]) {
+        if (FULL || items[n].on[p]) {
           h.p[2 * n + p] = load_piece<T, W>(x + items[n].at[p]);
         } else {
 #pragma unroll
           for (int j = 0; j < W; ++j) h.p[2 * n + p].v[j] = (T)0.f;
         }
   };
-  auto floats = [&](const Held<T, W>& h, float (&v)[kHeld]) {
-#pragma unroll
-    for (int n = 0; n < kHeld / W; ++n)
-#pragma unroll
-      for (int j = 0; j < W; ++j) v[n * W + j] = (float)h.p[n].v[j];
-  };
   auto store = [&](T* y, const float (&v)[kHeld]) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        if (items[n].on[p]) {
+        if (FULL || items[n].on[p]) {
           Piece<T, W> o;
 #pragma unroll
           for (int j = 0; j < W; ++j) o.v[j] = to_type<T>(v[(2 * n + p) * W + j]);
           store_piece<T, W>(y + items[n].at[p], o);
         }
   };
-
-  float sums[2][kHeld];  // backward
+  // sums of this thread in LDS
+  auto kept_at = [&](int which, int q) {
+    return reinterpret_cast<Piece<float, 4>*>(kept + ((which * (kHeld / 4) + q) * 256 + threadIdx.x) * 4);
+  };
   if constexpr (BACK)
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j) sums[s][j] = 0.f;
+    for (int q = 0; q < kHeld / 2; ++q) *kept_at(0, q) = Piece<float, 4>{0.f, 0.f, 0.f, 0.f};
 
   for (int chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
     const int t0 = chunk * a.tok, tok = min(a.tok, a.tokens - t0);
@@ -183,74 +187,97 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
                          a.inv_freq, a.axes, p);
     }
     __syncthreads();
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
+#pragma unroll 1
+    for (int which = 0; which < a.sides; ++which) {
       const QkSide& side = a.side[which];
-      if (side.heads.d == 0) break;
       Held<T, W> wh;
       if (side.w) load((const T*)side.w, wh);
+      float sums[kHeld];  // backward
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) sums[j] = 0.f;
       const int units = tok * side.heads.d;
+      // a unit's token in the chunk, and its x, dy and y
+      struct Place {
+        const T *x, *dy;
+        T* y;
+        int t;
+      };
+      auto place = [&](int u) {
+        Place at;
+        at.t = quotient(u, side.heads);
+        const int h = u - at.t * side.heads.d;
+        const int b = quotient(t0 + at.t, a.len), s = t0 + at.t - b * (int)a.len.d;
+        at.x = (const T*)side.x + b * side.xs[0] + s * side.xs[1] + h * side.xs[2];
+        at.y = (T*)side.y + b * side.ys[0] + s * side.ys[1] + h * side.ys[2];
+        if constexpr (BACK) at.dy = (const T*)side.dy + b * side.ds[0] + s * side.ds[1] + h * side.ds[2];
+        return at;
+      };
       for (int u = group; u < units; u += groups) {
-        const int t = quotient(u, side.heads), h = u - t * side.heads.d;
-        const int b = quotient(t0 + t, a.len), s = t0 + t - b * (int)a.len.d;
-        const T* x = (const T*)side.x + b * side.xs[0] + s * side.xs[1] + h * side.xs[2];
-        T* y = (T*)side.y + b * side.ys[0] + s * side.ys[1] + h * side.ys[2];
-        const float2* cs = table + t * a.pairs;
+        const Place at = place(u);
         Held<T, W> xh, dh;
-        load(x, xh);
-        if constexpr (BACK)
-          load((const T*)side.dy + b * side.ds[0] + s * side.ds[1] + h * side.ds[2], dh);
+        load(at.x, xh);
+        if constexpr (BACK) load(at.dy, dh);
+        const float2* cs = table + at.t * a.pairs;
         float v[kHeld], sq = 0.f;
-        floats(xh, v);
+        xh.values(v);
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) sq += v[j] * v[j];
-        const float r = 1.0f / sqrtf(group_sum(sq, a.lanes) * a.inv_d + a.eps);
+        const float r = rsqrtf(group_sum(sq, a.lanes) * a.inv_d + a.eps);
         float w[kHeld];
-        if (side.w) floats(wh, w);
+        if (side.w) {
+#pragma unroll
+          for (int n = 0; n < kHeld / W; ++n) stay_packed(wh.p[n]);
+          wh.values(w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kHeld; ++j) w[j] = 1.f;
+        }
         if constexpr (!BACK) {
 #pragma unroll
-          for (int j = 0; j < kHeld; ++j) v[j] = side.w ? v[j] * r * w[j] : v[j] * r;
+          for (int j = 0; j < kHeld; ++j) v[j] = v[j] * r * w[j];
 #pragma unroll
-          for (int n = 0; n < N; ++n) turn_item<W, INTER, 1>(a, items[n], cs, v + 2 * n * W);
+          for (int n = 0; n < N; ++n) turn_item<W, INTER, FULL, 1>(a, items[n], cs, v + 2 * n * W);
         } else {
           float e[kHeld], dot = 0.f;
-          floats(dh, e);
+          dh.values(e);
 #pragma unroll
-          for (int n = 0; n < N; ++n) turn_item<W, INTER, -1>(a, items[n], cs, e + 2 * n * W);
+          for (int n = 0; n < N; ++n) turn_item<W, INTER, FULL, -1>(a, items[n], cs, e + 2 * n * W);
 #pragma unroll
           for (int j = 0; j < kHeld; ++j) {
             v[j] *= r;
-            sums[which][j] += e[j] * v[j];
-            if (side.w) e[j] *= w[j];
-            dot += e[j] * v[j];
+            const float ev = e[j] * v[j];
+            sums[j] += ev;
+            dot += ev * w[j];
           }
           dot = group_sum(dot, a.lanes) * a.inv_d;
 #pragma unroll
-          for (int j = 0; j < kHeld; ++j) v[j] = r * (e[j] - v[j] * dot);
+          for (int j = 0; j < kHeld; ++j) v[j] = r * (e[j] * w[j] - v[j] * dot);
         }
-        store(y, v);
+        store(at.y, v);
       }
+      if constexpr (BACK)
+#pragma unroll
+        for (int q = 0; q < kHeld / 4; ++q) {
+          Piece<float, 4> k = *kept_at(which, q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) k.v[j] += sums[4 * q + j];
+          *kept_at(which, q) = k;
+        }
     }
   }
 
   if constexpr (BACK) {
     if (!a.part) return;
-    float* meet = (float*)table;  // [groups][kHeld][lanes]
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j)
-        meet[(group * kHeld + j) * a.lanes + lane] = sums[which][j];
-      __syncthreads();
-      // one thread a (value, lane) of the group adds the groups up
-      for (int i = threadIdx.x; i < kHeld * a.lanes; i += 256) {
-        float sum = 0.f;
-        for (int g = 0; g < groups; ++g) sum += meet[g * kHeld * a.lanes + i];
-        const int j = i / a.lanes, n = j / (2 * W), p = j / W % 2;
-        const Item m = item_of<W, INTER>(a, i % a.lanes + n * a.lanes);
-        if (m.on[p]) a.part[((int64_t)blockIdx.x * 2 + which) * a.d + m.at[p] + j % W] = sum;
-      }
+    __syncthreads();
+    // one thread a (value, lane) of the group adds the groups up
+    for (int i = threadIdx.x; i < 2 * kHeld * a.lanes; i += 256) {
+      const int which = i >= kHeld * a.lanes, at = i - which * kHeld * a.lanes;
+      const int j = at % kHeld, l = at / kHeld, n = j / (2 * W), p = j / W % 2;
+      float sum = 0.f;
+      for (int g = 0; g < groups; ++g)
+        sum += kept[((which * (kHeld / 4) + j / 4) * 256 + g * a.lanes + l) * 4 + j % 4];
+      const Item m = item_of<W, INTER, FULL>(a, l + n * a.lanes);
+      if (m.on[p]) a.part[((int64_t)blockIdx.x * 2 + which) * a.d + m.at[p] + j % W] = sum;
     }
   }
 }
@@ -308,6 +335,7 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
   k.num_axes = d.num_axes;
   k.pos_type = d.position_dtype;
   k.d = (int32_t)d.head_dim;
+  k.sides = d.kv_heads ? 2 : 1;
   k.eps = d.eps;
   k.inv_d = 1.0f / (float)d.head_dim;
   k.len = fast_div((uint32_t)std::max<int64_t>(d.len, 1));
@@ -323,8 +351,11 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
   const int held = kHeld / (2 * w);
   k.lanes = 1;
   while (k.lanes * held < items) k.lanes *= 2;
+  // every lane full: with pieces of 16 bytes a kernel without their conditions
+  const bool full = (size_t)w * (d.dtype == FUSEDCONV_F32 ? 4 : 2) == 16 && 2 * k.pairs == k.d &&
+                    k.lanes * kHeld == k.d;
   size_t lds = (size_t)k.tok * k.pairs * sizeof(float2);
-  if (back) lds = std::max(lds, (size_t)256 * kHeld * sizeof(float));
+  if (back) lds += (size_t)2 * 256 * kHeld * sizeof(float);
   const hipStream_t st = (hipStream_t)a.stream;
   const int64_t chunks = ((int64_t)k.tokens + k.tok - 1) / k.tok;
   k.chunks = (int32_t)chunks;
@@ -337,10 +368,10 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
         constexpr int width = decltype(W)::value;
         constexpr bool in = decltype(inter)::value;
         if constexpr (width * sizeof(T) <= 16 && !(in && width == 1)) {
-          if (back)
-            hipLaunchKernelGGL((k_qk_norm<T, width, in, true>), dim3(blocks), dim3(256), lds, st, k);
-          else
-            hipLaunchKernelGGL((k_qk_norm<T, width, in, false>), dim3(blocks), dim3(256), lds, st, k);
+          auto fn = back ? k_qk_norm<T, width, in, false, true> : k_qk_norm<T, width, in, false, false>;
+          if constexpr (width * sizeof(T) == 16)
+            if (full) fn = back ? k_qk_norm<T, width, in, true, true> : k_qk_norm<T, width, in, true, false>;
+          hipLaunchKernelGGL(fn, dim3(blocks), dim3(256), lds, st, k);
         }
       };
       auto wide = [&](auto inter) {
