@@ -297,15 +297,15 @@ def _plan_gated(x, gate, up, down, activation, alpha, out, back):
     return GatedFfn(code, rows, c, f, o, step, dy_step, activation, alpha), y_shape, h_shape
 
 
-def gated_ffn(x, gate, up, down, *, activation="QuickGelu", activation_params=(1.0,), keep=False,
+def gated_ffn(x, gate, up, down, *, activation="Silu", activation_params=None, keep=False,
               out=None, stream=None):
     """(act(x gate^T) * (x up^T)) down^T: [..., out]; (y, g, u) with keep=True, the projections g =
     x gate^T and u = x up^T [..., hidden] as gated_ffn_backward takes them.
 
     x [..., in], a view whose rows lie at one stride is fine; gate, up [hidden, in], down [out,
     hidden], x's dtype, contiguous (halves of one packed weight are); in, hidden and out are multiples
-    of 8.  activation: QuickGelu (v * sigmoid(alpha * v); as it stands, alpha = 1, SiLU), Gelu,
-    FastGelu, Sigmoid or Relu.  out: where to write, contiguous; it must not overlap an input."""
+    of 8.  activation: Silu, or QuickGelu (activation_params=[alpha]), Gelu, FastGelu, Sigmoid or Relu
+    as a convolution names them.  out: where to write, contiguous; it must not overlap an input."""
     if _t.torch is None or _lib is None:
         _setup()
     activation, alpha = _activation(activation, activation_params)
@@ -325,8 +325,8 @@ def gated_ffn(x, gate, up, down, *, activation="QuickGelu", activation_params=(1
     return (out, g, u) if keep else out
 
 
-def gated_ffn_backward(dy, x, gate, up, down, g, u, *, activation="QuickGelu",
-                       activation_params=(1.0,), weight_grads=True, stream=None):
+def gated_ffn_backward(dy, x, gate, up, down, g, u, *, activation="Silu",
+                       activation_params=None, weight_grads=True, stream=None):
     """(dx, dgate, dup, ddown) of gated_ffn, from the projections g and u that it kept; the other
     arguments as there.  All have x's dtype: the factors of their products are rounded to it.
     weight_grads=False: the last three are None."""

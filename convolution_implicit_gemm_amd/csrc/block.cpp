@@ -63,7 +63,8 @@ int fusedconv_qk_norm_rotary_create(const fusedconv_qk_norm_rotary_desc* d,
   fusedconv_qk_norm_rotary* h = new (std::nothrow) fusedconv_qk_norm_rotary();
   if (!h) return fail(FUSEDCONV_ERR_ALLOC, "out of host memory");
   h->d = *d;
-  h->workspace = qk_norm_workspace(*d);
+  const int64_t tokens = d->batch * d->len;
+  h->workspace = (size_t)(tokens < kQkBlocks ? tokens : kQkBlocks) * 2 * d->head_dim * sizeof(float);
   *out = h;
   clear_last_error();
   return FUSEDCONV_OK;
@@ -164,17 +165,20 @@ int fusedconv_gated_ffn_create(const fusedconv_gated_ffn_desc* d, fusedconv_gate
     return fail(FUSEDCONV_ERR_OUTPUT_SHAPE,
                 "rows must be >= 0; in, hidden and out positive multiples of 8");
   static const char* const names[] = {"Sigmoid", "Relu", "QuickGelu", "Gelu", "FastGelu"};  // GateAct
+  const bool silu = strcmp(d->activation, "Silu") == 0;  // QuickGelu with alpha 1
+  const char* name = silu ? "QuickGelu" : d->activation;
   int act = 0;
-  while (act < 5 && strcmp(d->activation, names[act]) != 0) ++act;
+  while (act < 5 && strcmp(name, names[act]) != 0) ++act;
   if (act == 5)
-    return fail(FUSEDCONV_ERR_ACTIVATION, "activation is not QuickGelu, Gelu, FastGelu, Sigmoid or Relu");
+    return fail(FUSEDCONV_ERR_ACTIVATION, "activation is not Silu, QuickGelu, Gelu, FastGelu, Sigmoid or Relu");
   if (!isfinite(d->alpha)) return fail(FUSEDCONV_ERR_ATTR_VALUE, "alpha must be finite");
   const int64_t es = elem_size(d->dtype);
   // a tile's 256 rows have to fit 31-bit byte offsets
   const int64_t most = ((int64_t(1) << 31) / 256 - 1) / es;
   if (d->in > most || d->hidden > most || d->out > most || d->rows > INT32_MAX / 2 ||
       product(d->rows, d->hidden, 1, kMaxElements / 4) < 0 || product(d->rows, d->in, 1, kMaxElements / 4) < 0 ||
-      product(d->rows, d->out, 1, kMaxElements / 4) < 0)
+      product(d->rows, d->out, 1, kMaxElements / 4) < 0 || product(d->hidden, d->in, 1, kMaxElements / 8) < 0 ||
+      product(d->out, d->hidden, 1, kMaxElements / 8) < 0)  // tiles and blocks stay below 2^31
     return fail(FUSEDCONV_ERR_TOO_LARGE, "a tensor exceeds the index limits");
   if (d->rows > 1 && (d->x_stride < 0 || d->dy_stride < 0 || d->x_stride % (16 / es) || d->dy_stride % (16 / es) ||
                       d->x_stride > most || d->dy_stride > most))
@@ -182,7 +186,8 @@ int fusedconv_gated_ffn_create(const fusedconv_gated_ffn_desc* d, fusedconv_gate
                 "strides must be non-negative, whole 16-byte pieces and within the index limits");
   fusedconv_gated_ffn* h = new (std::nothrow) fusedconv_gated_ffn();
   if (!h) return fail(FUSEDCONV_ERR_ALLOC, "out of host memory");
-  h->p = {d->dtype, (int32_t)d->rows, (int32_t)d->in, (int32_t)d->hidden, (int32_t)d->out, act, d->alpha,
+  h->p = {d->dtype, (int32_t)d->rows, (int32_t)d->in, (int32_t)d->hidden, (int32_t)d->out, act,
+          silu ? 1.0f : d->alpha,
           d->rows > 1 ? d->x_stride : d->in, d->rows > 1 ? d->dy_stride : d->out};
   plan_gated(h->p, h->plan);
   *out = h;

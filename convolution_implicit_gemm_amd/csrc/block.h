@@ -20,7 +20,9 @@ struct QkArgs {
   float* part;              // workspace: [blocks][q, k][head_dim]
   void* stream;
 };
-size_t qk_norm_workspace(const fusedconv_qk_norm_rotary_desc& d);
+// Blocks of the backward pass, whose sums meet in the workspace: a few to a compute
+// unit, so that the sums are few.
+constexpr int kQkBlocks = 1024;
 int launch_qk_norm_forward(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a);
 int launch_qk_norm_backward(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a);
 

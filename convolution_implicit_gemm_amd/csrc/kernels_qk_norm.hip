@@ -300,10 +300,6 @@ __global__ __launch_bounds__(1024) void k_qk_norm_join(const float* part, int bl
   }
 }
 
-// Blocks whose sums meet: the backward pass keeps a few blocks to a compute unit,
-// so that the sums are few.
-constexpr int kMostBlocks = 1024;
-
 int tokens_of_block(const fusedconv_qk_norm_rotary_desc& d, int most) {
   // about two table entries a thread, fewer while that leaves compute units
   // without a block
@@ -360,7 +356,7 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
   const int64_t chunks = ((int64_t)k.tokens + k.tok - 1) / k.tok;
   k.chunks = (int32_t)chunks;
   // One axis of a launch holds fewer than 2^32 threads: more tokens are walked over.
-  const int blocks = (int)std::min<int64_t>(chunks, back ? kMostBlocks : 1 << 23);
+  const int blocks = (int)std::min<int64_t>(chunks, back ? kQkBlocks : 1 << 23);
   if (blocks > 0)
     with_type(d.dtype, [&](auto tag) {
       using T = typename decltype(tag)::type;
@@ -391,10 +387,6 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
 
 }  // namespace
 
-size_t qk_norm_workspace(const fusedconv_qk_norm_rotary_desc& d) {
-  const int64_t tokens = d.batch * d.len;
-  return (size_t)std::min<int64_t>(tokens, kMostBlocks) * 2 * d.head_dim * sizeof(float);
-}
 int launch_qk_norm_forward(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a) {
   return launch(d, a, false);
 }

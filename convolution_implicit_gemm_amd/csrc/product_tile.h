@@ -219,9 +219,13 @@ typedef uint32_t Buffer __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ Buffer buffer_at(const char* base) {
   const uint64_t at = (uint64_t)base;
   // raw bytes: no stride, kOutside of them
-  return Buffer{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
-                (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xffffu), kOutside,
-                0x00020000u};
+  Buffer b{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
+           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xffffu), kOutside, 0x00020000u};
+  // A scalar register that a vector instruction has written (readfirstlane) may be
+  // read by a memory instruction five wait states later; the compiler does not see
+  // that the copies below are any.
+  asm volatile("s_nop 4" : "+s"(b));
+  return b;
 }
 __device__ __forceinline__ void copy_buffer_to_lds(uint32_t to, uint32_t off, Buffer from) {
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(

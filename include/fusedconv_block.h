@@ -77,9 +77,9 @@ void fusedconv_qk_norm_rotary_destroy(fusedconv_qk_norm_rotary* h);
  * X is [rows][in], gate and up [hidden][in], down [out][hidden], Y [rows][out]:
  * weights lie as a linear layer keeps them.  in, hidden and out are multiples of
  * 8.  x_stride / dy_stride: elements from one row to the next (multiples of 16
- * bytes); everything else is contiguous.  activation: "QuickGelu"
- * (g * sigmoid(alpha * g); alpha 1 is SiLU), "Gelu", "FastGelu", "Sigmoid" or
- * "Relu", as fusedconv_desc names them.  No biases.
+ * bytes); everything else is contiguous.  activation: "Silu"
+ * (g * sigmoid(g)), or "QuickGelu" (g * sigmoid(alpha * g)), "Gelu", "FastGelu",
+ * "Sigmoid" or "Relu" as fusedconv_desc names them.  No biases.
  *
  * Backward, from g and u as the forward pass stored them (rounded to T):
  *     dh = dy down,  dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u
