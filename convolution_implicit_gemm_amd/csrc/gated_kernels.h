@@ -25,7 +25,9 @@ namespace {
 // rows of the weights (of gate and of up), its waves share the terms, 256 bytes of
 // every row a wave at a time, with the next ones on their way; the waves' sums meet in
 // LDS.  Products are 16 x 16 with the weights as the first operand: a lane ends
-// with four neighbouring results of one row of x.
+// with four neighbouring results of one row of x.  4096 x 11008, bf16, both
+// launches: one row 59 us (271 MB, 4.6 TB/s), 16 rows 74 us, 32 rows 97 us: every
+// block reads all of x, from the L2, beside its weights.
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t Chunk __attribute__((ext_vector_type(4)));  // 16 bytes: terms of one row
 
@@ -54,13 +56,15 @@ struct FewK {
 
 template <typename T, int MT, bool TWO>
 __global__ __launch_bounds__(TWO ? 512 : 1024) void k_gated_few(FewK a) {
+  // Steps of 64 bytes in a group.  One row of 4096 x 11008, both launches: with two
+  // 60.5 us, four 58.9, six 58.6 (32 rows 121 for 97), eight 71.
   constexpr int NW = TWO ? 2 : 1, U = 4;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
   const int n0 = block_number() * 16;
   if (n0 >= a.cols) return;
-  const int bytes = a.depth * (int)sizeof(T), steps = (bytes + 63) >> 6;
+  const int bytes = a.depth * (int)sizeof(T);
   // rows past the end repeat the last one; what they give is not stored
   const char* w[NW];
   w[0] = (const char*)a.w + min(n0 + row, a.cols - 1) * a.ws + quarter * 16;
@@ -77,10 +81,11 @@ __global__ __launch_bounds__(TWO ? 512 : 1024) void k_gated_few(FewK a) {
   struct Group {
     Chunk w[U][NW], x[U][MT];
   };
-  auto load = [&](int s0, Group& g) {
+  // steps s0 .. s0 + U - 1; whole: all of them lie inside a row
+  auto load = [&](auto whole, int s0, Group& g) {
 #pragma unroll
     for (int s = 0; s < U; ++s) {
-      const bool in = (s0 + s) * 64 + quarter * 16 < bytes;
+      const bool in = whole || (s0 + s) * 64 + quarter * 16 < bytes;
       const int64_t at = (int64_t)(s0 + s) * 64;
 #pragma unroll
       for (int n = 0; n < NW; ++n) g.w[s][n] = in ? *(const Chunk*)(w[n] + at) : Chunk{0, 0, 0, 0};
@@ -96,15 +101,20 @@ __global__ __launch_bounds__(TWO ? 512 : 1024) void k_gated_few(FewK a) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[n][t] = mma16(g.w[s][n], g.x[s][t], acc[n][t], T{});
   };
-  const int step = waves * U;
+  // whole groups of U steps in turn, and first the rest behind them: without its
+  // conditions in the loop the loads of a group are issued in a row
+  const int groups = bytes / (64 * U);
+  const bool rest = bytes % (64 * U) != 0 && groups % waves == wave;
   Group a0, a1;
-  int s = wave * U;
-  if (s < steps) load(s, a0);
-  for (; s < steps; s += 2 * step) {
-    if (s + step < steps) load(s + step, a1);
+  if (rest) load(int_c<0>{}, groups * U, a1);
+  int n = wave;
+  if (n < groups) load(int_c<1>{}, n * U, a0);
+  if (rest) use(a1);
+  for (; n < groups; n += 2 * waves) {
+    if (n + waves < groups) load(int_c<1>{}, (n + waves) * U, a1);
     use(a0);
-    if (s + step >= steps) break;
-    if (s + 2 * step < steps) load(s + 2 * step, a0);
+    if (n + waves >= groups) break;
+    if (n + 2 * waves < groups) load(int_c<1>{}, (n + 2 * waves) * U, a0);
     use(a1);
   }
 
@@ -121,9 +131,9 @@ __global__ __launch_bounds__(TWO ? 512 : 1024) void k_gated_few(FewK a) {
     sum[n] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int v = 0; v < waves; ++v) sum[n] += meet[((v * NW + n) * MT + wave) * 64 + lane];
   }
-  const int m = 16 * wave + row, n = n0 + 4 * quarter;
-  if (m >= a.rows || n >= a.cols) return;
-  const int64_t at = (int64_t)m * a.cols + n;
+  const int m = 16 * wave + row, col = n0 + 4 * quarter;
+  if (m >= a.rows || col >= a.cols) return;
+  const int64_t at = (int64_t)m * a.cols + col;
   Piece<T, 4> o;
   if constexpr (TWO) {
     Piece<T, 4> g, u;
@@ -152,11 +162,10 @@ template <typename T, bool TWO>
 int launch_few(const FewK& k, hipStream_t st) {
   const int blocks = (k.cols + 15) / 16;
   const int steps = (int)(((int64_t)k.depth * sizeof(T) + 63) / 64);
-  // about eight waves to a compute unit, each with terms to sum
+  // About eight waves to a compute unit, each with terms to sum (both launches, one
+  // row, 2048 x 5632 and 16 rows, 4096 x 11008: 23.9 and 73.5 us so; four waves
+  // throughout 26.3 and 75.6, eight 24.2 and 74.5).
   int waves = blocks >= 512 ? 4 : 8;
-#ifdef FC_EXPERIMENT
-  if (const char* e = getenv(TWO ? "FCW2" : "FCW1")) waves = atoi(e);
-#endif
   while (waves > 2 && waves * 4 > steps) waves /= 2;
   const int mt = k.rows > 16 ? 2 : 1;
   const size_t lds = (size_t)waves * (TWO ? 2 : 1) * mt * 1024;
@@ -199,6 +208,7 @@ __global__ __launch_bounds__(256) void k_gated_tops(const T* dy, int64_t stride,
 }
 __global__ __launch_bounds__(64) void k_gated_scale(const float* tops, int n, float* scale) {
   float top = 0.f;
+#pragma unroll 8
   for (int i = threadIdx.x; i < n; i += 64) top = fmaxf(top, tops[i]);
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));

@@ -14,6 +14,10 @@
 // The weights' gradients: a lane sums its 16 values up over the heads of some
 // tokens, and keeps the sums of all its block's tokens in LDS; blocks walk over the
 // tokens, and a second launch adds their sums in a fixed order.
+//
+// Memory bounds both directions: 256 x 196 tokens, 12 heads of 64 in Q and K, bf16,
+// forward 65 us (308 MB, 4.8 TB/s), backward 99 us (463 MB, 4.7 TB/s); a copy of
+// 1 GiB runs at 5.0.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -289,6 +293,7 @@ __global__ __launch_bounds__(1024) void k_qk_norm_join(const float* part, int bl
   const int col = blockIdx.x * 16 + threadIdx.x % 16, row = threadIdx.x / 16;
   float sum = 0.f;
   if (col < 2 * d)
+#pragma unroll 8
     for (int b = row; b < blocks; b += 64) sum += part[(int64_t)b * 2 * d + col];
   meet[row][threadIdx.x % 16] = sum;
   __syncthreads();
