@@ -3,13 +3,23 @@
 //     r = 1 / sqrt(mean(x^2) + eps),  n = x * r * w,  y = R(t) n
 //     e = R(-t) dy,  dw = sum e * x * r,  a = e * w,  dx = r * (a - x r * mean(a * x r))
 //
-// A head is held by a group of G lanes, 16 values a lane, between its loads and
-// its stores, so that every value is read once and written once.  A lane's values
-// are pairs of pieces of W values that turn with each other: of the two halves of
-// the turned part, or, interleaved and behind the turned part, neighbours.  W is
-// 16 bytes where the pairs fill such pieces and less where they do not.  The sum
-// of a group runs over lanes without LDS.  Cosines and sines of a block's tokens
-// are made once for all heads, in LDS (turns.h).
+// A head is held by a group of lanes, 16 values a lane in pieces of 16 bytes, between
+// its loads and its stores, so that every value is read once and written once.  The
+// sum of a group runs over lanes without LDS.  Cosines and sines of a block's tokens
+// are made once for all heads, in LDS (turns.h).  Values that turn with each other
+// meet in one of three ways:
+//   kHalves   the two halves of the turned part are whole pieces: a lane has pairs of
+//             pieces, one of either half, and behind the turned part neighbours
+//   kNext     interleaved: a lane has neighbouring pieces; the table goes on behind
+//             the turned part with angles of zero
+//   kCross    halves that are no whole pieces: neighbouring pieces, and a value's
+//             other half comes through LDS, where the group has left its values.
+//             Pieces of 2 to 8 bytes instead, as kHalves would need, took 149 us
+//             (36 pairs of 72 values; backward 273) and 202 us (18 pairs of 88; 385)
+//             where this takes 111 (220) and 123 (244): 256 x 196 tokens, 12 heads in
+//             Q and K, bf16; a copy 69 (103) and 84 (126).  LDS bounds it.
+// A group has as many lanes as its head fills (heads of 80: 108 us in 8 lanes, 88 in
+// 5); where that is no power of two its sums take a few shuffles more.
 //
 // The weights' gradients: a lane sums its 16 values up over the heads of some
 // tokens, and keeps the sums of all its block's tokens in LDS; blocks walk over the
@@ -31,6 +41,7 @@ namespace fc {
 namespace {
 
 constexpr int kHeld = 16;  // values of a head that a lane holds
+enum Meet : int { kHalves = 0, kNext, kCross };
 
 struct QkSide {  // q, or k
   const void *x, *w, *dy;
@@ -47,80 +58,106 @@ struct QkK {
   float* part;
   int64_t pos_batch;
   int32_t tokens, pairs, num_axes, pos_type, tok, d, sides;
-  int32_t lanes;                 // of a group
-  int32_t turned, pieces;        // pieces (of a half, interleaved: in all) that turn; in all
+  int32_t lanes;                 // of a group, 1 to 16
+  int32_t turned, pieces;        // kHalves: pieces of a half that turn; pieces of a head
+  int32_t entries;               // of the table, a token
   int32_t chunks;                // of tok tokens
   float eps, inv_d;
   FastDiv len;
 };
 
 // The pieces of item i of a head: where they begin, whether there are any, and
-// whether they turn.  FULL: every lane's items are whole pairs of pieces that turn.
+// (kHalves) whether they turn.  FULL: every lane's items are whole pairs of pieces,
+// and (kHalves) all of them turn.
 struct Item {
   int at[2];
   bool on[2], turn;
-  int pair;  // the first pair
 };
-template <int W, bool INTER, bool FULL>
+template <int W, int MEET, bool FULL>
 __device__ __forceinline__ Item item_of(const QkK& a, int i) {
   Item m;
-  if constexpr (INTER) {  // pieces 2i, 2i + 1, each turned by itself
-    m.at[0] = 2 * i * W;
-    m.at[1] = m.at[0] + W;
-    m.on[0] = FULL || 2 * i < a.pieces;
-    m.on[1] = FULL || 2 * i + 1 < a.pieces;
-    m.turn = false;  // by position, below
-    m.pair = i * W;
-  } else if (FULL || i < a.turned) {
+  if (MEET == kHalves && (FULL || i < a.turned)) {
     m.at[0] = i * W;
     m.at[1] = a.pairs + i * W;
     m.on[0] = m.on[1] = m.turn = true;
-    m.pair = i * W;
   } else {
-    const int p = 2 * a.turned + 2 * (i - a.turned);
+    const int p = MEET == kHalves ? 2 * a.turned + 2 * (i - a.turned) : 2 * i;
     m.at[0] = p * W;
     m.at[1] = m.at[0] + W;
-    m.on[0] = p < a.pieces;
-    m.on[1] = p + 1 < a.pieces;
+    m.on[0] = FULL || p < a.pieces;
+    m.on[1] = FULL || p + 1 < a.pieces;
     m.turn = false;
-    m.pair = 0;
   }
   return m;
 }
 
-// (x, y) of every pair of an item turned by SIGN times its angle.
-template <int W, bool INTER, bool FULL, int SIGN>
-__device__ __forceinline__ void turn_item(const QkK& a, const Item& m, const float2* cs, float* v) {
-  if constexpr (INTER) {
+// kCross: where value v of a group's head lies among the values it leaves in LDS; a
+// lane's run of 2 W begins a bank behind that of the lane before it.
+template <int W>
+__device__ __forceinline__ int cross_at(int v) { return v + v / (2 * W); }
+
+// Where entry e of a token lies in the table: 16 bytes are left out behind what one
+// lane reads in a row, so that the lanes begin in different banks.
+template <int W, int MEET>
+__device__ __forceinline__ int table_at(int e) { return e + e / (MEET == kCross ? 2 * W : W) * 2; }
+
+// Every pair of a lane's values turned by SIGN times its angle.  kCross: own is where
+// run n's values go in LDS, other where the other halves of all values are (a zero
+// for those that have none).
+template <int W, int MEET, bool FULL, int SIGN>
+__device__ __forceinline__ void turn_values(const QkK& a, const Item (&items)[kHeld / (2 * W)], const float2* cs,
+                                            float* cross, const int (&own)[kHeld / (2 * W)],
+                                            const int (&other)[kHeld], float (&v)[kHeld]) {
+  constexpr int N = kHeld / (2 * W);
+  if constexpr (MEET == kCross) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-      if (FULL || m.at[p] < 2 * a.pairs)
+    for (int j = 0; j < kHeld; ++j) cross[own[j / (2 * W)] + j % (2 * W)] = v[j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int j = 0; j < W; j += 2) {
-          const float2 c = cs[(m.at[p] + j) >> 1];
-          const float s = SIGN * c.y, x = v[p * W + j], y = v[p * W + j + 1];
-          v[p * W + j] = x * c.x - y * s;
-          v[p * W + j + 1] = y * c.x + x * s;
-        }
+    for (int j = 0; j < kHeld; ++j) {
+      const float2 c = cs[table_at<W, MEET>(items[j / (2 * W)].at[0]) + j % (2 * W)];
+      v[j] = v[j] * c.x + cross[other[j]] * (SIGN * c.y);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   } else {
-    if (FULL || m.turn)
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        const float2 c = cs[m.pair + j];
-        const float s = SIGN * c.y, x = v[j], y = v[W + j];
-        v[j] = x * c.x - y * s;
-        v[W + j] = y * c.x + x * s;
+    for (int n = 0; n < N; ++n) {
+      float* z = v + 2 * n * W;
+      if constexpr (MEET == kNext) {
+#pragma unroll
+        for (int j = 0; j < 2 * W; j += 2) {
+          const float2 c = cs[table_at<W, MEET>(items[n].at[0] >> 1) + (j >> 1)];
+          const float s = SIGN * c.y, x = z[j], y = z[j + 1];
+          z[j] = x * c.x - y * s;
+          z[j + 1] = y * c.x + x * s;
+        }
+      } else if (FULL || items[n].turn) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float2 c = cs[table_at<W, MEET>(items[n].at[0]) + j];
+          const float s = SIGN * c.y, x = z[j], y = z[W + j];
+          z[j] = x * c.x - y * s;
+          z[W + j] = y * c.x + x * s;
+        }
       }
+    }
   }
 }
 
 // Sum over the group's lanes; their number is the same for the whole launch.
-__device__ __forceinline__ float group_sum(float v, int lanes) {
+__device__ __forceinline__ float group_sum(float v, int lanes, int lane) {
+  if (lanes & (lanes - 1)) {  // not a power of two: the first lane adds up
+    const int self = threadIdx.x & 63;
+    for (int off = lanes > 8 ? 8 : lanes > 4 ? 4 : 2; off; off /= 2) {
+      const float x = __shfl(v, self + off);
+      if (lane + off < lanes) v += x;
+    }
+    return __shfl(v, self - lane);
+  }
   if (lanes > 1) v = add_lane<1, true>(v);
   if (lanes > 2) v = add_lane<2, false>(v);
   if (lanes > 4) v = add_lane<4, false>(v);
   if (lanes > 8) v = add_lane<8, false>(v);
-  if (lanes > 16) v = add_lane<16, false>(v);
   return v;
 }
 
@@ -136,18 +173,43 @@ struct Held {
   }
 };
 
-template <typename T, int W, bool INTER, bool FULL, bool BACK>
+template <typename T, int MEET, bool FULL, bool BACK>
 __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
-  constexpr int N = kHeld / (2 * W);  // items of a lane
+  constexpr int W = 16 / sizeof(T), N = kHeld / (2 * W);  // N: items of a lane
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  // backward: the lanes' sums [q, k][kHeld / 4][256][4], then (both) [tok][pairs]
+  // backward: the lanes' sums [q, k][kHeld / 4][256][4]; kCross: the groups' values, a
+  // zero; (all) the table [tok][entries]
+  constexpr int kCrossed = MEET == kCross ? (256 * kHeld + 256 * kHeld / (2 * W) + 4) : 0;
   float* kept = (float*)lds;
-  float2* table = (float2*)(lds + (BACK ? 2 * kHeld * 256 * sizeof(float) : 0));
-  const int group = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes;
-  const int groups = 256 / a.lanes;
+  float* cross = kept + (BACK ? 2 * kHeld * 256 : 0);
+  float2* table = (float2*)(cross + kCrossed);
+  // a wave's groups, and lanes of none behind them
+  const int per = 64 / a.lanes, groups = 4 * per;
+  const int in_wave = (threadIdx.x & 63) / a.lanes, lane = (threadIdx.x & 63) % a.lanes;
+  const int group = in_wave < per ? (threadIdx.x >> 6) * per + in_wave : groups;
   Item items[N];
 #pragma unroll
-  for (int n = 0; n < N; ++n) items[n] = item_of<W, INTER, FULL>(a, lane + n * a.lanes);
+  for (int n = 0; n < N; ++n) items[n] = item_of<W, MEET, FULL>(a, lane + n * a.lanes);
+  int own[N], other[kHeld];  // kCross
+  if constexpr (MEET == kCross) {
+    const int region = min(group, groups - 1) * cross_at<W>(kHeld * a.lanes);
+#pragma unroll
+    for (int n = 0; n < N; ++n) own[n] = region + cross_at<W>(items[n].at[0]);
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int v = items[j / (2 * W)].at[0] + j % (2 * W);
+      other[j] = v >= 2 * a.pairs ? kCrossed - 1 : region + cross_at<W>(v < a.pairs ? v + a.pairs : v - a.pairs);
+    }
+    if (threadIdx.x == 0) cross[kCrossed - 1] = 0.f;
+  }
+  if constexpr (MEET != kHalves) {  // behind the turned part
+    const int turned = MEET == kCross ? 2 * a.pairs : a.pairs;
+    const int rest = (MEET == kCross ? kHeld : kHeld / 2) * a.lanes - turned;
+    for (int i = threadIdx.x; i < a.tok * rest; i += 256) {
+      const int t = i / rest;
+      table[t * a.entries + table_at<W, MEET>(turned + i - t * rest)] = make_float2(1.f, 0.f);
+    }
+  }
 
   auto load = [&](const T* x, Held<T, W>& h) {
 #pragma unroll
@@ -187,8 +249,15 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
     for (int i = threadIdx.x; i < tok * a.pairs; i += 256) {
       const int t = i / a.pairs, p = i - t * a.pairs;
       const int b = quotient(t0 + t, a.len), s = t0 + t - b * (int)a.len.d;
-      table[i] = turn_of(a.pos, a.pos_type, b * a.pos_batch + (int64_t)s * a.num_axes, a.num_axes,
-                         a.inv_freq, a.axes, p);
+      const float2 c = turn_of(a.pos, a.pos_type, b * a.pos_batch + (int64_t)s * a.num_axes, a.num_axes,
+                               a.inv_freq, a.axes, p);
+      float2* to = table + t * a.entries;
+      if constexpr (MEET == kCross) {
+        to[table_at<W, MEET>(p)] = make_float2(c.x, -c.y);
+        to[table_at<W, MEET>(p + a.pairs)] = c;
+      } else {
+        to[table_at<W, MEET>(p)] = c;
+      }
     }
     __syncthreads();
 #pragma unroll 1
@@ -216,17 +285,17 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
         if constexpr (BACK) at.dy = (const T*)side.dy + b * side.ds[0] + s * side.ds[1] + h * side.ds[2];
         return at;
       };
-      for (int u = group; u < units; u += groups) {
+      for (int u = group < groups ? group : units; u < units; u += groups) {
         const Place at = place(u);
         Held<T, W> xh, dh;
         load(at.x, xh);
         if constexpr (BACK) load(at.dy, dh);
-        const float2* cs = table + at.t * a.pairs;
+        const float2* cs = table + at.t * a.entries;
         float v[kHeld], sq = 0.f;
         xh.values(v);
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) sq += v[j] * v[j];
-        const float r = rsqrtf(group_sum(sq, a.lanes) * a.inv_d + a.eps);
+        const float r = rsqrtf(group_sum(sq, a.lanes, lane) * a.inv_d + a.eps);
         float w[kHeld];
         if (side.w) {
 #pragma unroll
@@ -239,13 +308,11 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
         if constexpr (!BACK) {
 #pragma unroll
           for (int j = 0; j < kHeld; ++j) v[j] = v[j] * r * w[j];
-#pragma unroll
-          for (int n = 0; n < N; ++n) turn_item<W, INTER, FULL, 1>(a, items[n], cs, v + 2 * n * W);
+          turn_values<W, MEET, FULL, 1>(a, items, cs, cross, own, other, v);
         } else {
           float e[kHeld], dot = 0.f;
           dh.values(e);
-#pragma unroll
-          for (int n = 0; n < N; ++n) turn_item<W, INTER, FULL, -1>(a, items[n], cs, e + 2 * n * W);
+          turn_values<W, MEET, FULL, -1>(a, items, cs, cross, own, other, e);
 #pragma unroll
           for (int j = 0; j < kHeld; ++j) {
             v[j] *= r;
@@ -253,7 +320,7 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
             sums[j] += ev;
             dot += ev * w[j];
           }
-          dot = group_sum(dot, a.lanes) * a.inv_d;
+          dot = group_sum(dot, a.lanes, lane) * a.inv_d;
 #pragma unroll
           for (int j = 0; j < kHeld; ++j) v[j] = r * (e[j] * w[j] - v[j] * dot);
         }
@@ -278,9 +345,10 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
       const int which = i >= kHeld * a.lanes, at = i - which * kHeld * a.lanes;
       const int j = at % kHeld, l = at / kHeld, n = j / (2 * W), p = j / W % 2;
       float sum = 0.f;
-      for (int g = 0; g < groups; ++g)
-        sum += kept[((which * (kHeld / 4) + j / 4) * 256 + g * a.lanes + l) * 4 + j % 4];
-      const Item m = item_of<W, INTER, FULL>(a, l + n * a.lanes);
+      for (int wave = 0; wave < 4; ++wave)
+        for (int g = 0; g < per; ++g)
+          sum += kept[((which * (kHeld / 4) + j / 4) * 256 + 64 * wave + g * a.lanes + l) * 4 + j % 4];
+      const Item m = item_of<W, MEET, FULL>(a, l + n * a.lanes);
       if (m.on[p]) a.part[((int64_t)blockIdx.x * 2 + which) * a.d + m.at[p] + j % W] = sum;
     }
   }
@@ -306,10 +374,10 @@ __global__ __launch_bounds__(1024) void k_qk_norm_join(const float* part, int bl
 }
 
 int tokens_of_block(const fusedconv_qk_norm_rotary_desc& d, int most) {
-  // about two table entries a thread, fewer while that leaves compute units
-  // without a block
+  // about four table entries a thread (of a pair; kCross has two to a pair), fewer while
+  // that leaves compute units without a block
   const int64_t tokens = d.batch * d.len;
-  int tok = (int)std::min<int64_t>(std::max<int64_t>(512 / d.pairs, 1), most);
+  int tok = std::min(std::max(most, 1), 32);
   while (tok > 1 && (tokens + tok - 1) / tok < 2048) tok /= 2;
   return tok;
 }
@@ -342,21 +410,21 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
   k.len = fast_div((uint32_t)std::max<int64_t>(d.len, 1));
   const bool sums = a.dqw || a.dkw;
   k.part = sums ? a.part : nullptr;
-  k.tok = tokens_of_block(d, 32);
-  // the widest pieces that the turned part (of a half, or of both) and the head consist of
-  int w = d.dtype == FUSEDCONV_F32 ? 4 : 8;
-  while ((d.interleaved ? 2 * d.pairs : d.pairs) % w != 0) w /= 2;
+  const int es = d.dtype == FUSEDCONV_F32 ? 4 : 2, w = 16 / es;
+  const int meet = d.interleaved ? kNext : d.pairs % w == 0 ? kHalves : kCross;
   k.pieces = k.d / w;
-  k.turned = (int32_t)(d.interleaved ? 2 * d.pairs : d.pairs) / w;
-  const int items = d.interleaved ? (k.pieces + 1) / 2 : k.turned + (k.pieces - 2 * k.turned + 1) / 2;
+  k.turned = (int32_t)d.pairs / w;
+  const int items = meet == kHalves ? k.turned + (k.pieces - 2 * k.turned + 1) / 2 : (k.pieces + 1) / 2;
   const int held = kHeld / (2 * w);
-  k.lanes = 1;
-  while (k.lanes * held < items) k.lanes *= 2;
-  // every lane full: with pieces of 16 bytes a kernel without their conditions
-  const bool full = (size_t)w * (d.dtype == FUSEDCONV_F32 ? 4 : 2) == 16 && 2 * k.pairs == k.d &&
-                    k.lanes * kHeld == k.d;
-  size_t lds = (size_t)k.tok * k.pairs * sizeof(float2);
+  k.lanes = (items + held - 1) / held;
+  const bool full = k.lanes * kHeld == k.d && (meet != kHalves || 2 * k.pairs == k.d);
+  k.entries = meet == kHalves ? k.pairs : (meet == kNext ? kHeld / 2 : kHeld) * k.lanes;
+  k.tok = tokens_of_block(d, (meet == kCross ? 1024 : 512) / k.entries);
+  const int run = meet == kCross ? 2 * w : w;
+  k.entries += (k.entries + run - 1) / run * 2;  // table_at()
+  size_t lds = (size_t)k.tok * k.entries * sizeof(float2);
   if (back) lds += (size_t)2 * 256 * kHeld * sizeof(float);
+  if (meet == kCross) lds += (size_t)(256 * kHeld + 256 * kHeld / (2 * w) + 4) * sizeof(float);
   const hipStream_t st = (hipStream_t)a.stream;
   const int64_t chunks = ((int64_t)k.tokens + k.tok - 1) / k.tok;
   k.chunks = (int32_t)chunks;
@@ -365,24 +433,15 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
   if (blocks > 0)
     with_type(d.dtype, [&](auto tag) {
       using T = typename decltype(tag)::type;
-      auto go = [&](auto W, auto inter) {
-        constexpr int width = decltype(W)::value;
-        constexpr bool in = decltype(inter)::value;
-        if constexpr (width * sizeof(T) <= 16 && !(in && width == 1)) {
-          auto fn = back ? k_qk_norm<T, width, in, false, true> : k_qk_norm<T, width, in, false, false>;
-          if constexpr (width * sizeof(T) == 16)
-            if (full) fn = back ? k_qk_norm<T, width, in, true, true> : k_qk_norm<T, width, in, true, false>;
-          hipLaunchKernelGGL(fn, dim3(blocks), dim3(256), lds, st, k);
-        }
+      auto go = [&](auto m) {
+        constexpr int how = decltype(m)::value;
+        auto fn = back ? (full ? k_qk_norm<T, how, true, true> : k_qk_norm<T, how, false, true>)
+                       : (full ? k_qk_norm<T, how, true, false> : k_qk_norm<T, how, false, false>);
+        hipLaunchKernelGGL(fn, dim3(blocks), dim3(256), lds, st, k);
       };
-      auto wide = [&](auto inter) {
-        if (w == 8) go(std::integral_constant<int, 8>{}, inter);
-        else if (w == 4) go(std::integral_constant<int, 4>{}, inter);
-        else if (w == 2) go(std::integral_constant<int, 2>{}, inter);
-        else go(std::integral_constant<int, 1>{}, inter);
-      };
-      if (d.interleaved) wide(std::true_type{});
-      else wide(std::false_type{});
+      if (meet == kNext) go(std::integral_constant<int, kNext>{});
+      else if (meet == kHalves) go(std::integral_constant<int, kHalves>{});
+      else go(std::integral_constant<int, kCross>{});
     });
   if (sums)  // without tokens they are zero
     hipLaunchKernelGGL(k_qk_norm_join, dim3((2 * k.d + 15) / 16), dim3(1024), 0, st, a.part, blocks, k.d,

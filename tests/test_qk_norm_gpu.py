@@ -186,3 +186,27 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want))
     assert len(there) == 6
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("d,pairs", [(64, 32), (72, 36), (88, 18), (24, 5), (256, 100)])
+def test_heads_that_are_not_finite(d, pairs, dtype, interleaved):
+    """NaN and infinities in one head, and in one head's gradient, reach that head only."""
+    q, k, qw, kw, pos, freq, ax = (dev(t) for t in inputs((2, 9, 5, 5, d, pairs, 1, 100), dtype))
+    dq, dk = (dev(randn(n, *q.shape, dtype=q.dtype)) for n in (21, 22))
+
+    def run():
+        y = fc.qk_norm_rotary(q, k, qw, kw, pos, freq, ax, interleaved=interleaved)
+        return (*y, *fc.qk_norm_rotary_backward(dq, dk, q, k, qw, kw, pos, freq, ax, interleaved=interleaved)[:2])
+
+    want = run()
+    q[0, 3, 1, d - 1], q[1, 8, 4, 0], k[0, 0, 0, d // 2] = float("nan"), float("inf"), float("nan")
+    dq[1, 2, 3, 0], dk[0, 5, 2, d - 1] = float("nan"), float("inf")
+    hit = [[(0, 3, 1), (1, 8, 4)], [(0, 0, 0)], [(0, 3, 1), (1, 8, 4), (1, 2, 3)], [(0, 0, 0), (0, 5, 2)]]
+    for a, b, heads in zip(run(), want, hit):
+        same = torch.ones(a.shape[:3], dtype=torch.bool)
+        for head in heads:
+            same[head] = False
+            assert not torch.isfinite(a[head]).all()
+        assert torch.equal(a[same], b[same])
