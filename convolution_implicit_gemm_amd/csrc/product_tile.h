@@ -224,14 +224,22 @@ __device__ __forceinline__ Buffer buffer_at(const char* base) {
   // A scalar register that a vector instruction has written (readfirstlane) may be
   // read by a memory instruction five wait states later; the compiler does not see
   // that the copies below are any.
+#ifdef __OPTIMIZE__
   asm volatile("s_nop 4" : "+s"(b));
+#endif
   return b;
 }
 __device__ __forceinline__ void copy_buffer_to_lds(uint32_t to, uint32_t off, Buffer from) {
+#ifdef __OPTIMIZE__
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(
                    __builtin_amdgcn_readfirstlane(to)),
                "v"(off), "s"(from)
                : "memory");
+#else  // unoptimised code has no scalar registers for an operand: the same by a load and a store
+  const char* base = (const char*)(from[0] | (uint64_t)from[1] << 32);
+  *(__attribute__((address_space(3))) Buffer*)(to + 16 * (threadIdx.x & 63)) =
+      off < kOutside ? *(const Buffer*)(base + off) : Buffer{0, 0, 0, 0};
+#endif
 }
 
 // Terms 16 * step .. + 15 (natural order: 8 * (lane / 32) ...) of the columns
