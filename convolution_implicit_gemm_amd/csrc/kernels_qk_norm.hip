@@ -349,7 +349,8 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
         for (int g = 0; g < per; ++g)
           sum += kept[((which * (kHeld / 4) + j / 4) * 256 + 64 * wave + g * a.lanes + l) * 4 + j % 4];
       const Item m = item_of<W, MEET, FULL>(a, l + n * a.lanes);
-      if (m.on[p]) a.part[((int64_t)blockIdx.x * 2 + which) * a.d + m.at[p] + j % W] = sum;
+      const int value = (p ? m.at[1] : m.at[0]) + j % W;  // an index here would put m into scratch memory
+      if (p ? m.on[1] : m.on[0]) a.part[((int64_t)blockIdx.x * 2 + which) * a.d + value] = sum;
     }
   }
 }
