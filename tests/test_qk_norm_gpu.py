@@ -210,3 +210,53 @@ def test_heads_that_are_not_finite(d, pairs, dtype, interleaved):
             same[head] = False
             assert not torch.isfinite(a[head]).all()
         assert torch.equal(a[same], b[same])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,pairs", [(72, 36), (88, 18), (24, 5), (40, 20), (256, 100), (136, 68)])
+def test_over_its_inputs(d, pairs, dtype, interleaved):
+    """Results over q and k; gradients over the gradients given, and over q and k."""
+    q, k, *rest = (dev(t) for t in inputs((2, 37, 5, 3, d, pairs, 2, 100), dtype, 60))
+    dq, dk = dev(randn(61, *q.shape, dtype=q.dtype)), dev(randn(62, *k.shape, dtype=q.dtype))
+    want = fc.qk_norm_rotary(q, k, *rest, interleaved=interleaved)
+    grads = fc.qk_norm_rotary_backward(dq, dk, q, k, *rest, interleaved=interleaved)
+    at = q.clone(), k.clone()
+    fc.qk_norm_rotary(*at, *rest, interleaved=interleaved, out_q=at[0], out_k=at[1])
+    assert all(torch.equal(a, b) for a, b in zip(at, want))
+    for over_gradients in (True, False):
+        at, gr = (q.clone(), k.clone()), (dq.clone(), dk.clone())
+        to = gr if over_gradients else at
+        got = fc.qk_norm_rotary_backward(*gr, *at, *rest, interleaved=interleaved, out_q=to[0], out_k=to[1])
+        assert all(torch.equal(a, b) for a, b in zip(got, grads))
+
+
+@pytest.mark.parametrize("d,pairs,interleaved", [(128, 64, False), (72, 36, False), (72, 30, True)])
+def test_beyond_32_bits(d, pairs, interleaved):
+    """Q of more than 2^32 bytes: tokens on both sides of the limit as by themselves, the weights'
+    gradients as those of two halves."""
+    b, h = 2, 64
+    s = 2 ** 32 // (2 * 2 * h * d) + 900
+    g = torch.Generator(device="cuda").manual_seed(70)
+    q, dq = (torch.empty(b, s, h, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    w = torch.rand(d, generator=g, device="cuda").bfloat16()
+    pos = torch.randint(0, 100000, (b, s, 1), generator=g, device="cuda")
+    freq, ax = torch.rand(pairs, generator=g, device="cuda"), torch.zeros(pairs, dtype=torch.int32, device="cuda")
+    y = fc.qk_norm_rotary(q, None, w, None, pos, freq, ax, interleaved=interleaved)
+    dx, _, dw, _ = fc.qk_norm_rotary_backward(dq, None, q, None, w, None, pos, freq, ax, interleaved=interleaved)
+    sums = 0
+    for n in range(b):
+        part = slice(n, n + 1)
+        e = fc.qk_norm_rotary_backward(dq[part], None, q[part], None, w, None, pos[part], freq, ax,
+                                       interleaved=interleaved)
+        assert torch.equal(dx[part], e[0])
+        sums = sums + e[2].double()
+        for at in (slice(0, 50), slice(s - 1000, s)):
+            z = fc.qk_norm_rotary(q[part, at], None, w, None, pos[part, at].contiguous(), freq, ax,
+                                  interleaved=interleaved)
+            assert torch.equal(y[part, at], z)
+    # sums of s * h products of about 1 in two groupings, of up to 2000 additions a lane and 1024 blocks'
+    # sums in float32: each rounds by 2^-24 of partial sums of at most a few times (s * h)^0.5
+    assert float((dw.double() - sums).abs().max()) < 3000 * 2 ** -24 * 5 * (b * s * h) ** 0.5
+    del q, dq, y, dx
+    torch.cuda.empty_cache()
