@@ -52,7 +52,7 @@ struct GatedProblem {
 struct GatedPlan {
   int32_t few;            // few rows: a wave streams rows of the weights
   ProductPlan gate, down, hidden, input, weights;
-  // forward: h, then partial results; backward: dg, du, h, the scale, partial results
+  // forward: h, then partial results; backward: dg, du, h, their scale, partial results
   size_t hidden_bytes, forward_bytes, backward_bytes;
 };
 struct GatedArgs {
@@ -62,7 +62,7 @@ struct GatedArgs {
   void* ws;
   void* stream;
 };
-constexpr size_t kScaleBytes = 8192;  // maxima of dy's parts, the scale
+constexpr size_t kScaleBytes = 9472;  // f16: the scale of dg and du, what it comes from
 void plan_gated(const GatedProblem& p, GatedPlan& plan);
 int gated_forward_f32(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);
 int gated_forward_f16(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a);

@@ -9,10 +9,16 @@
 // gradients are one launch.  Compiled once per type (FC_TYPE), kernels_gated_*.hip.
 //
 // h, dg and du are rounded to T: they are factors of the next products, which for
-// 16-bit T take 16-bit factors.  f16's normal values end at 2^-14: dg and du are
-// rounded as 2^s times themselves, where 2^s lifts dy's largest value to between
-// 2^-6 and 2^-5 (never below itself); what they pass on is divided by it again.
+// 16-bit T take 16-bit factors.  f16's normal values lie between 2^-14 and 2^16: dg and
+// du are rounded as 2^s times themselves, where 2^s lifts dy's largest value to between
+// 2^-6 and 2^-5 (never below itself); what they pass on is divided by it again.  What
+// dh, u and the slope make of dy is known behind the product only: it keeps the largest
+// factor, and where that is beyond f16 a second launch, which otherwise ends at once
+// (16 rows of 1024 x 2736: 42 us without it, 43.5 with it), takes the product again with
+// the scale that fits it.
 #pragma once
+
+#include <algorithm>
 
 #include "internal.h"
 #include "product_tile.h"
@@ -177,16 +183,16 @@ int launch_few(const FewK& k, hipStream_t st) {
 // ------------------------------------------------------------ the scale of dy
 
 // Largest magnitudes of dy's parts, one a block; infinite and NaN values count as 0.
-// A wave takes rows, four at a time in flight.
-constexpr int kTops = 1024;  // parts at most
+// A wave takes rows, four at a time in flight.  The words that no block has, and the
+// slots of the largest factors, are cleared.
 template <typename T>
-__global__ __launch_bounds__(256) void k_gated_tops(const T* dy, int64_t stride, int32_t rows, int32_t cols,
-                                                    float* tops) {
-  __shared__ float meet[4];
+__global__ __launch_bounds__(1024) void k_gated_tops(const T* dy, int64_t stride, int32_t rows, int32_t cols,
+                                                     uint32_t* words) {
+  __shared__ float meet[16];
   constexpr int P = 16 / sizeof(T);
-  const int per = cols / P, waves = 4 * gridDim.x, lane = threadIdx.x & 63;
+  const int per = cols / P, blocks = gridDim.x, waves = 16 * blocks, lane = threadIdx.x & 63;
   float top = 0.f;
-  for (int64_t row = 4 * blockIdx.x + (threadIdx.x >> 6); row < rows; row += 4 * waves)
+  for (int64_t row = 16 * blockIdx.x + (threadIdx.x >> 6); row < rows; row += 4 * waves)
     for (int i = lane; i < per; i += 64) {
       Piece<T, P> x[4];
 #pragma unroll
@@ -200,19 +206,18 @@ __global__ __launch_bounds__(256) void k_gated_tops(const T* dy, int64_t stride,
           if (v < INFINITY) top = fmaxf(top, v);
         }
     }
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
+  top = wave_max(top);
   if (lane == 0) meet[threadIdx.x >> 6] = top;
   __syncthreads();
-  if (threadIdx.x == 0) tops[blockIdx.x] = fmaxf(fmaxf(meet[0], meet[1]), fmaxf(meet[2], meet[3]));
-}
-__global__ __launch_bounds__(64) void k_gated_scale(const float* tops, int n, float* scale) {
-  float top = 0.f;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < n; i += 64) top = fmaxf(top, tops[i]);
+  if (threadIdx.x == 0) {
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
-  if (threadIdx.x == 0) *scale = top > 0.f ? ldexpf(1.f, max(0, -6 - ilogbf(top))) : 1.f;
+    for (int n = 1; n < 16; ++n) top = fmaxf(top, meet[n]);
+    words[FactorScale::kTops + blockIdx.x] = __float_as_uint(top);
+  }
+  for (int i = blockIdx.x + blocks * (1 + threadIdx.x); i < FactorScale::kParts; i += blocks * 1024)
+    words[FactorScale::kTops + i] = 0;
+  for (int i = blockIdx.x + blocks * threadIdx.x; i < 64; i += blocks * 1024)
+    words[FactorScale::kSlots + i * FactorScale::kStep] = 0;
 }
 
 // ---------------------------------------------------------------- launches
@@ -236,9 +241,9 @@ int launch_shape(ProductK& k, const ProductPlan& plan, hipStream_t st) {
   k.whole = plan.whole;
   k.splits = plan.splits;
   k.split_items = (tiles - plan.whole) * plan.splits;
-  const int64_t blocks = xcd_grid(k.whole) + xcd_grid(k.split_items);
-  if (blocks == 0) return FUSEDCONV_OK;
-  hipLaunchKernelGGL(fn, grid_of(blocks), dim3(256), S::kLds, st, k);
+  // the second run finds the shares of split tiles as the first one left them
+  const int64_t blocks = xcd_grid(k.whole) + (k.again ? 0 : xcd_grid(k.split_items));
+  if (blocks) hipLaunchKernelGGL(fn, grid_of(blocks), dim3(256), S::kLds, st, k);
   if (k.split_items)
     hipLaunchKernelGGL((k_product_join<T, LB, RB, FORM>),
                        grid_of((int64_t)(tiles - plan.whole) * (LB * RB / 2048)), dim3(256), 0, st, k);
@@ -295,21 +300,23 @@ int backward(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a) {
   k.dg = ws;
   k.du = ws + plan.hidden_bytes;
   k.h = ws + 2 * plan.hidden_bytes;
-  static_assert((kTops + 1) * sizeof(float) <= kScaleBytes);
-  float* tops = (float*)(ws + 3 * plan.hidden_bytes);
+  static_assert(FactorScale::kWords * sizeof(uint32_t) <= kScaleBytes);
   k.part = (float*)(ws + 3 * plan.hidden_bytes + kScaleBytes);
   int rc = FUSEDCONV_OK;
   if (p.m > 0) {
-    if constexpr (std::is_same<T, _Float16>::value) {
-      const int blocks = p.m < 4 * kTops ? (p.m + 3) / 4 : kTops;
-      hipLaunchKernelGGL((k_gated_tops<T>), dim3(blocks), dim3(256), 0, st, (const T*)a.dy, p.dy_stride, p.m,
-                         p.o, tops);
-      hipLaunchKernelGGL(k_gated_scale, dim3(1), dim3(64), 0, st, tops, blocks, tops + kTops);
-      k.scale = tops + kTops;
+    if constexpr (is_scaled<T>) {
+      k.scale = (uint32_t*)(ws + 3 * plan.hidden_bytes);
+      const int64_t blocks = std::min((p.m + int64_t(15)) / 16, (int64_t)FactorScale::kParts);
+      hipLaunchKernelGGL((k_gated_tops<T>), dim3((unsigned)blocks), dim3(1024), 0, st, (const T*)a.dy, p.dy_stride,
+                         p.m, p.o, k.scale);
     }
     k.p[0] = Product{a.dy, a.down, nullptr, nullptr, nullptr, p.dy_stride * es, p.f * es, p.m, p.f, p.o};
-    rc = launch_product<T, kHidden>(k, plan.hidden, st);
-    if (rc != FUSEDCONV_OK) return rc;
+    for (int again = 0; again <= (int)is_scaled<T>; ++again) {
+      k.again = again;
+      rc = launch_product<T, kHidden>(k, plan.hidden, st);
+      if (rc != FUSEDCONV_OK) return rc;
+    }
+    k.again = 0;
     k.p[0] = Product{k.dg, a.gate, k.du, a.up, a.dx, p.f * es, p.c * es, p.m, p.c, p.f, 0, 0, 0, 1};
     rc = launch_product<T, kInput>(k, plan.input, st);
     if (rc != FUSEDCONV_OK) return rc;

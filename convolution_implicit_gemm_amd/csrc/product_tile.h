@@ -45,7 +45,8 @@ struct ProductK {
   float* part;          // [split_items][LB][RB]
   // the hidden values, [m][f] of T
   void *g, *u, *h, *dg, *du;
-  const float* scale;   // of dg and du: a power of two (NULL: 1)
+  uint32_t* scale;      // f16: of dg and du, as FactorScale has it; NULL: 1
+  int32_t again;        // kHidden: the second run, with the scale that fits, or nothing to do
   int32_t f, act;
   float alpha;
 };
@@ -160,15 +161,64 @@ struct Held8 {
   }
 };
 
+// The scale of dg and du in f16, words of 32 bits.  The first one is a guess from dy's
+// parts' largest magnitudes; kHidden keeps the largest factor that it gave, and where
+// that is beyond f16 runs again with the scale that takes it to 2^14.  What is behind it
+// divides by the one held.  The largest factors are kept in slots, a line each: 6000
+// waves' atomics on one address took 200 us of the 18464 rows' backward pass (1024 x
+// 2736).
+struct FactorScale {
+  static constexpr int kHeld = 0, kTops = 32, kParts = 256, kSlots = kTops + kParts, kStep = 32;
+  static constexpr int kWords = kSlots + 64 * kStep;
+};
+template <typename T>
+inline constexpr bool is_scaled = std::is_same<T, _Float16>::value;
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) v = fmaxf(v, __shfl_xor(v, off));
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+__device__ __forceinline__ float first_scale(const uint32_t* words) {
+  const Piece<float, 4> x =
+      load_piece<float, 4>((const float*)words + FactorScale::kTops + 4 * (threadIdx.x & 63));
+  const float top = wave_max(fmaxf(fmaxf(x.v[0], x.v[1]), fmaxf(x.v[2], x.v[3])));
+  return top > 0.f ? ldexpf(1.f, max(0, -6 - ilogbf(top))) : 1.f;
+}
+// kHidden's second run: its scale; false where the first run's factors fit.
+template <typename T, int FORM>
+__device__ __forceinline__ bool second_scale(const ProductK& a, float& scale) {
+  if constexpr (FORM == kHidden && is_scaled<T>) {
+    if (!a.again) return true;
+    const float first = first_scale(a.scale);
+    const float top = wave_max(
+        __uint_as_float(a.scale[FactorScale::kSlots + (threadIdx.x & 63) * FactorScale::kStep]));
+    scale = top <= 65504.0f ? first : ldexpf(first, 14 - ilogbf(top));
+    if (block_number() == 0 && threadIdx.x == 0) a.scale[FactorScale::kHeld] = __float_as_uint(scale);
+    return scale != first;
+  }
+  return true;
+}
+// A wave's largest factor joins the others': an integer maximum, the same in any order.
+template <typename T>
+__device__ __forceinline__ void record_top(const ProductK& a, float top) {
+  if constexpr (is_scaled<T>) {
+    if (a.again) return;
+    top = wave_max(top);
+    if ((threadIdx.x & 63) == 0)
+      atomicMax(a.scale + FactorScale::kSlots + (block_number() & 63) * FactorScale::kStep, __float_as_uint(top));
+  }
+}
+
 // Eight results r .. r + 7 of row l, which is one of the product's.
 template <typename T>
 __device__ __forceinline__ void finish8(const ProductK& a, const Product& p, int l, int r,
                                         float (&v)[8]) {
-  if (p.scaled && a.scale) {
-    const float back = 1.0f / *a.scale;
+  if constexpr (is_scaled<T>)
+    if (p.scaled && a.scale) {
+      const float back = 1.0f / __uint_as_float(a.scale[FactorScale::kHeld]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= back;
-  }
+      for (int j = 0; j < 8; ++j) v[j] *= back;
+    }
   store8((T*)p.out + (int64_t)l * p.cols + r, v);
 }
 // Eight hidden values: g and u of row l.
@@ -187,12 +237,12 @@ __device__ __forceinline__ void finish_gate8(const ProductK& a, int l, int r, co
     store8((T*)a.u + at, u);
   }
 }
-// Eight gradients dh of hidden values whose g and u are given.
+// Eight gradients dh of hidden values whose g and u are given; scale: of dg and du; top:
+// the largest of them of this lane so far.
 template <typename T>
 __device__ __forceinline__ void finish_hidden8(const ProductK& a, int l, int r, const float (&dh)[8],
-                                               const float (&g)[8], const float (&u)[8]) {
+                                               const float (&g)[8], const float (&u)[8], float scale, float& top) {
   const int64_t at = (int64_t)l * a.f + r;
-  const float scale = a.scale ? *a.scale : 1.0f;
   float dg[8], du[8], h[8];
   with_gate_act(a.act, [&](auto act) {
 #pragma unroll
@@ -204,6 +254,12 @@ __device__ __forceinline__ void finish_hidden8(const ProductK& a, int l, int r, 
       h[j] = value * u[j];
     }
   });
+  if constexpr (is_scaled<T>)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // infinite inputs keep their infinite results
+      const float x = fabsf(dg[j]), y = fabsf(du[j]);
+      top = fmaxf(top, fmaxf(x < INFINITY ? x : 0.0f, y < INFINITY ? y : 0.0f));
+    }
   store8((T*)a.dg + at, dg);
   store8((T*)a.du + at, du);
   store8((T*)a.h + at, h);
@@ -365,6 +421,7 @@ struct Work {
   int wave, l0, r0, one, s0, s1;
   bool partial;
   float* part;
+  float scale;  // kHidden's second run
 
   __device__ __forceinline__ bool init(const ProductK& a) {
     int item = xcd_item(block_number(), a.whole), split = 0;
@@ -432,6 +489,8 @@ __device__ __forceinline__ void finish_tile(const ProductK& a, const Work<T, LB,
   constexpr int ROW = COLS + 4;  // floats
   static_assert(4 * 32 * AT * ROW * 4 <= Shape<T, LB, RB, FORM>::kLds);
   float* meet = (float*)lds + w.wave * 32 * AT * ROW;
+  float scale = 1.f, top = 0.f;  // kHidden
+  if constexpr (FORM == kHidden && is_scaled<T>) scale = a.again ? w.scale : first_scale(a.scale);
   each_index<0, LT / AT * RP>([&](auto step) {
     constexpr int t0 = step / RP * AT, part = step % RP;
     const int col0 = (RP * (w.wave >> 1) + part) * COLS;  // of the tile
@@ -492,7 +551,7 @@ __device__ __forceinline__ void finish_tile(const ProductK& a, const Work<T, LB,
           load8(from + 8 * n * ROW, v);
           g[i].values(gv);
           u[i].values(uv);
-          if (in && l + 8 * n < p.rows) finish_hidden8<T>(a, l + 8 * n, r, v, gv, uv);
+          if (in && l + 8 * n < p.rows) finish_hidden8<T>(a, l + 8 * n, r, v, gv, uv, scale, top);
         };
         ask(0, int_c<0>{});
 #pragma unroll 1
@@ -513,6 +572,8 @@ __device__ __forceinline__ void finish_tile(const ProductK& a, const Work<T, LB,
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   });
+  if constexpr (FORM == kHidden)
+    if (!w.partial) record_top<T>(a, top);
 }
 
 template <typename T, int LB, int FORM>
@@ -520,7 +581,7 @@ __global__ __launch_bounds__(256, 2) void k_product(ProductK a) {
   using S = Shape<T, LB, 128, FORM>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   Work<T, LB, 128, FORM> w;
-  if (!w.init(a)) return;
+  if (!second_scale<T, FORM>(a, w.scale) || !w.init(a)) return;
   f32x16 acc[2][S::LT];
 #pragma unroll
   for (int r = 0; r < 2; ++r)
@@ -663,6 +724,10 @@ __global__ __launch_bounds__(256, 1) void k_product_wide(ProductK a) {
 template <typename T, int LB, int RB, int FORM>
 __global__ __launch_bounds__(256) void k_product_join(ProductK a) {
   constexpr int rows = 2048 / RB, strips = LB / rows, groups = RB / 8;
+  float scale = 1.f;
+  if (!second_scale<T, FORM>(a, scale)) return;
+  if constexpr (FORM == kHidden && is_scaled<T>)
+    if (!a.again) scale = first_scale(a.scale);
   const int item = a.whole + block_number() / strips;
   if ((int64_t)(item - a.whole) * a.splits >= a.split_items) return;
   const int which = a.products > 1 ? (item >= a.p[1].first) + (a.products > 2 && item >= a.p[2].first) : 0;
@@ -671,7 +736,7 @@ __global__ __launch_bounds__(256) void k_product_join(ProductK a) {
   tile_place(p, item - p.first, row_tile, col_tile);
   const int row = block_number() % strips * rows + threadIdx.x / groups, at = threadIdx.x % groups;
   const int l = row_tile * LB + row;
-  if (l >= p.rows) return;
+  if (FORM != kHidden && l >= p.rows) return;
   const float* part = a.part + ((int64_t)(item - a.whole) * a.splits * LB + row) * RB;
   auto sum = [&](int col, float (&v)[8]) {
 #pragma unroll
@@ -695,15 +760,20 @@ __global__ __launch_bounds__(256) void k_product_join(ProductK a) {
     finish_gate8<T>(a, l, r, g, u);
   } else {
     const int r = col_tile * RB + 8 * at;
-    if (r >= p.cols) return;
+    if (FORM != kHidden && r >= p.cols) return;
     float v[8];
-    sum(8 * at, v);
     if constexpr (FORM == kHidden) {
-      float g[8], u[8];
-      load8((const T*)a.g + (int64_t)l * a.f + r, g);
-      load8((const T*)a.u + (int64_t)l * a.f + r, u);
-      finish_hidden8<T>(a, l, r, v, g, u);
+      float top = 0.f;
+      if (l < p.rows && r < p.cols) {
+        float g[8], u[8];
+        sum(8 * at, v);
+        load8((const T*)a.g + (int64_t)l * a.f + r, g);
+        load8((const T*)a.u + (int64_t)l * a.f + r, u);
+        finish_hidden8<T>(a, l, r, v, g, u, scale, top);
+      }
+      record_top<T>(a, top);
     } else {
+      sum(8 * at, v);
       finish8<T>(a, p, l, r, v);
     }
   }

@@ -89,7 +89,9 @@ void fusedconv_qk_norm_rotary_destroy(fusedconv_qk_norm_rotary* h);
  * Sums are fp32.  For 16-bit T the factors h, dg and du of the second products are
  * rounded to T, as the inputs they meet are.  f16: h beyond 65504 is infinite; dg
  * and du are rounded times a power of two that lifts dy's largest magnitude to
- * 2^-6 or more, so that gradients of small dy keep their bits.
+ * 2^-6 or more, so that gradients of small dy keep their bits, or that takes the
+ * largest dg or du to 2^14 where it would be beyond 65504 so (the product that makes
+ * them is then taken twice).
  *
  * Outputs overlap neither inputs nor each other.
  */
