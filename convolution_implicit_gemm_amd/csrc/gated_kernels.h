@@ -10,12 +10,12 @@
 //
 // h, dg and du are rounded to T: they are factors of the next products, which for
 // 16-bit T take 16-bit factors.  f16's normal values lie between 2^-14 and 2^16: dg and
-// du are rounded as 2^s times themselves, where 2^s lifts dy's largest value to between
-// 2^-6 and 2^-5 (never below itself); what they pass on is divided by it again.  What
-// dh, u and the slope make of dy is known behind the product only: it keeps the largest
-// factor, and where that is beyond f16 a second launch, which otherwise ends at once
-// (16 rows of 1024 x 2736: 42 us without it, 43.5 with it), takes the product again with
-// the scale that fits it.
+// du are rounded as 2^s times themselves, where 2^s takes dy's largest value to between
+// 2^8 and 2^9; what they pass on is divided by it again.  What dh, u and the slope make
+// of dy is known behind the product only: it keeps the largest factor, and where that is
+// beyond f16 or below 2^4 a second launch, which otherwise ends at once (16 rows of
+// 1024 x 2736: 42 us without it, 43.5 with it), takes the product again with the scale
+// that fits it.
 #pragma once
 
 #include <algorithm>

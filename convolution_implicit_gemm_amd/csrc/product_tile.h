@@ -161,10 +161,11 @@ struct Held8 {
   }
 };
 
-// The scale of dg and du in f16, words of 32 bits.  The first one is a guess from dy's
-// parts' largest magnitudes; kHidden keeps the largest factor that it gave, and where
-// that is beyond f16 runs again with the scale that takes it to 2^14.  What is behind it
-// divides by the one held.  The largest factors are kept in slots, a line each: 6000
+// The scale of dg and du in f16, words of 32 bits.  The first one is a guess: it takes
+// dy's largest magnitude to 2^8.  kHidden keeps the largest factor that this gave, and
+// where that is beyond f16 or below 2^4 runs again with the scale that takes it to 2^14.
+// So the largest factor lies 2^18 or more above 2^-14, where values begin to lose bits.
+// What is behind it divides by the one held.  The largest factors are kept in slots, a line each: 6000
 // waves' atomics on one address took 200 us of the 18464 rows' backward pass (1024 x
 // 2736).
 struct FactorScale {
@@ -182,7 +183,7 @@ __device__ __forceinline__ float first_scale(const uint32_t* words) {
   const Piece<float, 4> x =
       load_piece<float, 4>((const float*)words + FactorScale::kTops + 4 * (threadIdx.x & 63));
   const float top = wave_max(fmaxf(fmaxf(x.v[0], x.v[1]), fmaxf(x.v[2], x.v[3])));
-  return top > 0.f ? ldexpf(1.f, max(0, -6 - ilogbf(top))) : 1.f;
+  return top > 0.f ? ldexpf(1.f, 8 - ilogbf(top)) : 1.f;
 }
 // kHidden's second run: its scale; false where the first run's factors fit.
 template <typename T, int FORM>
@@ -192,7 +193,9 @@ __device__ __forceinline__ bool second_scale(const ProductK& a, float& scale) {
     const float first = first_scale(a.scale);
     const float top = wave_max(
         __uint_as_float(a.scale[FactorScale::kSlots + (threadIdx.x & 63) * FactorScale::kStep]));
-    scale = top <= 65504.0f ? first : ldexpf(first, 14 - ilogbf(top));
+    // factors below 2^-40 of it are no longer followed: no result would hold them
+    const bool fits = top == 0.f || (top >= 16.0f && top <= 65504.0f);
+    scale = fits ? first : ldexpf(first, 14 - max(ilogbf(top), -40));
     if (block_number() == 0 && threadIdx.x == 0) a.scale[FactorScale::kHeld] = __float_as_uint(scale);
     return scale != first;
   }

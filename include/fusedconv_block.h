@@ -87,11 +87,12 @@ void fusedconv_qk_norm_rotary_destroy(fusedconv_qk_norm_rotary* h);
  * No atomics: the same call gives the same bits.  The weights' gradients are of T.
  *
  * Sums are fp32.  For 16-bit T the factors h, dg and du of the second products are
- * rounded to T, as the inputs they meet are.  f16: h beyond 65504 is infinite; dg
- * and du are rounded times a power of two that lifts dy's largest magnitude to
- * 2^-6 or more, so that gradients of small dy keep their bits, or that takes the
- * largest dg or du to 2^14 where it would be beyond 65504 so (the product that makes
- * them is then taken twice).
+ * rounded to T, as the inputs they meet are.  f16: h beyond 65504 is infinite, and
+ * below 2^-14 its steps are 2^-24; dg and du are rounded times a power of two that
+ * takes dy's largest magnitude to 2^8, or, where that leaves the largest of them
+ * beyond 65504 or below 2^4, takes this to 2^14 (the product that makes them is then
+ * taken twice): whatever the sizes of dy, the weights and u, a factor keeps its bits
+ * down to 2^-18 of the largest one or further.
  *
  * Outputs overlap neither inputs nor each other.
  */

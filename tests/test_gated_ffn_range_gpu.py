@@ -1,5 +1,5 @@
 """float16's factors dg and du in the gated feed-forward block's backward pass: gradients that its results
-hold are finite, however far dh, u and the slopes take the factors above dy's size."""
+hold keep their bits, however far dh, u and the slopes take the factors from dy's size."""
 import sys
 
 import pytest
@@ -41,7 +41,7 @@ def apart(got, want):
 LIMIT = 2 * unit(torch.float16)
 
 
-def check(args):
+def check(args, rows=None):
     got = fc.gated_ffn_backward(*args)
     again = fc.gated_ffn_backward(*args)
     want, limits = ref.gated_ffn_backward(*args, "QuickGelu", 1.0)
@@ -50,6 +50,8 @@ def check(args):
         assert torch.isfinite(e.half()).all(), f"{name}: not a case for float16"
         within(name, a, e.cpu(), l.cpu())
         assert apart(a, e) < LIMIT, (name, apart(a, e))
+    for part in rows or ():
+        assert apart(got[0][part], want[0][part]) < LIMIT, (part, apart(got[0][part], want[0][part]))
     return got
 
 
@@ -69,6 +71,10 @@ def test_large_factors(m):
 SIZES = [  # rows, in, hidden, out, dy, x, weights, down, u
     (300, 256, 264, 256, 1e-5, 1.0, None, 8.0, 3e3),          # factors 2^20 times dy
     (2000, 264, 1032, 264, 0.25, 5e-4, 1e-4, 8.0, 2e3),       # factors that float16 does not hold, results it does
+    (700, 512, 512, 512, 1e-3, 500.0, 4000.0, 1e-4, 1.0),     # factors 2^10 below dy
+    (700, 512, 512, 512, 0.01, 500.0, 4000.0, 1e-4, 1e-3),    # and 2^20
+    (4100, 1032, 2056, 1032, 1e-3, 500.0, 4000.0, 1e-4, 1.0),  # in large tiles
+    (300, 200, 72, 104, 1e-3, 500.0, 4000.0, 1e-4, 1.0),
 ]
 
 
@@ -77,6 +83,19 @@ def test_factors_of_any_size(size):
     log(f"CASE gated_ffn range {size}")
     m, c, f, o, dy, x, w, down, u = size
     check(inputs(m, c, f, o, dy, x, w, down, 1.0, u))
+
+
+@pytest.mark.parametrize("quiet", [2.0 ** -10, 2.0 ** -13])
+@pytest.mark.parametrize("down", [None, 1e-4])
+def test_quiet_rows(down, quiet):
+    """Rows whose dy is a thousandth of the others' have gradients as good as theirs."""
+    log(f"CASE gated_ffn range quiet {down} {quiet}")
+    m = 600
+    w = 8e3 if down else 64.0
+    dy, x, gate, up, dn, g, u = inputs(m, 512, 512, 512, 1.0 if down else 0.02, 1.0, w, down)
+    half = slice(m // 2, m)
+    dy[half] = (dy[half].float() * quiet).half()
+    check((dy, x, gate, up, dn, g, u), (slice(0, m // 2), half))
 
 
 def test_rows_that_are_not_finite():
