@@ -57,12 +57,24 @@ enum GateAct : int { kSigmoid = 0, kRelu, kQuickGelu, kGelu, kFastGelu };
 
 // The gate's activation and its derivative.  The tanh form of Gelu is taken as
 // 0.5 v (1 + tanh z) = v sigmoid(2 z).  16-bit types take the hardware's exponential
-// and reciprocal, 1 - s for sigmoid(-z) and the short form of erfc, whose errors of
-// about 1e-6 are far inside a step of theirs.
+// and reciprocal and the short form of erfc: off by about 1e-6.
 template <bool FAST>
 __device__ __forceinline__ float sigmoid_of(float z) {
   if constexpr (FAST) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
   else return 1.0f / (1.0f + expf(-z));
+}
+// s = sigmoid(z) and t = sigmoid(-z), each to a few steps of its own: the smaller one is
+// e / (1 + e), e = exp(-|z|).  (1 - s for it is off by 1 % at z = 12 and zero from 17 on.)
+template <bool FAST>
+__device__ __forceinline__ void sigmoids_of(float z, float& s, float& t) {
+  if constexpr (FAST) {
+    const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+    s = z < 0.0f ? e * r : r;
+    t = z < 0.0f ? r : e * r;
+  } else {
+    s = sigmoid_of<false>(z);
+    t = sigmoid_of<false>(-z);
+  }
 }
 template <int ACT, bool FAST>
 __device__ __forceinline__ float gate_value(float alpha, float v) {
@@ -105,7 +117,8 @@ __device__ __forceinline__ void gate_both(float alpha, float v, float& value, fl
       z = 1.5957691216057308f * v * (1.0f + 0.044715f * v * v);
       dz = 1.5957691216057308f * (1.0f + 0.134145f * v * v);
     }
-    const float s = sigmoid_of<FAST>(z), t = FAST ? 1.0f - s : sigmoid_of<FAST>(-z);
+    float s, t;
+    sigmoids_of<FAST>(z, s, t);
     value = ACT == kSigmoid ? s : v * s;
     slope = ACT == kSigmoid ? s * t : s + value * t * dz;
   }

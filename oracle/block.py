@@ -86,13 +86,15 @@ def activation(name, alpha, v, fast):
         z, dz = c * v, torch.full_like(v, c)
     s, t = torch.sigmoid(z), torch.sigmoid(-z)
     rel = k * (4 * z.abs() + 8) * E          # of s, and of t
-    # fast: t = 1 - s, off by what s is and by e
-    b_t = rel * s + E if fast else rel * t
+    # where exp(-|z|) is below 2^-126, that is |z| > 87, it may be zero, and s or t with it.  What that
+    # takes from v s and from v s t dz is largest at that border, where |v| < 90 for alpha >= 1 and
+    # dz < 30
+    least = 2.0 ** -126
     if name == "Sigmoid":
-        return s, s * t, rel * s, rel * s * t + s * b_t + E * s * t
-    fall = (v * s * t * dz).abs()
-    return (v * s, s + v * s * t * dz, (rel + E) * (v * s).abs(),
-            rel * s + (rel + 8 * E) * fall + (v * s * dz).abs() * b_t + E * (s + fall))
+        return s, s * t, rel * s + least, (2 * rel + E) * s * t + least
+    fall, v_s = (v * s * t * dz).abs(), (v * s).abs()
+    return (v * s, s + v * s * t * dz, (rel + E) * v_s + 90 * least,
+            rel * s + (2 * rel + 8 * E) * fall + E * (s + fall) + (1 + 90 * 30) * least)
 
 
 def gated_ffn(x, gate, up, down, name, alpha):
