@@ -66,7 +66,7 @@ def qk_norm_rotary_backward(dy, x, weight, positions, inv_freq, axes, interleave
 def activation(name, alpha, v, fast):
     """(value, slope) of a gate's activation in float64 and the limits of their 32-bit evaluation.
     exp(z) is off by |z| e for its argument's rounding and a few steps; fast (16-bit types): twice that,
-    and the normal distribution function by 6e-7 (the formula's and its evaluation's part)."""
+    and the smaller tail of the normal distribution by 4.2e-6 of itself (a fitted formula's part)."""
     k = 2 if fast else 1
     if name == "Relu":
         on = (v > 0).double()
@@ -74,7 +74,12 @@ def activation(name, alpha, v, fast):
     if name == "Gelu":
         cdf = 0.5 * torch.erfc(-v / math.sqrt(2))
         phi = torch.exp(-0.5 * v * v) / math.sqrt(2 * math.pi)
-        b_cdf = (6e-7 if fast else 0.0) + (v * v + 16) * E * cdf
+        # float32: the argument v / sqrt 2 is off by half a step of the constant (0.3 e) and of the
+        # product (e), which is 1.3 v^2 e of a tail
+        b_cdf = (1.3 * v * v + 16) * E * cdf
+        if fast:
+            tail = 0.5 * torch.erfc(v.abs() / math.sqrt(2))
+            b_cdf = (4.2e-6 + 2 * (v * v + 16) * E) * tail + E * cdf
         b_phi = k * (v * v + 8) * E * phi
         return (v * cdf, cdf + v * phi, v.abs() * b_cdf + E * (v * cdf).abs(),
                 b_cdf + v.abs() * b_phi + 2 * E * (cdf + (v * phi).abs()))
