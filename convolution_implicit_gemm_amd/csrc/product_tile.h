@@ -130,8 +130,11 @@ __device__ __forceinline__ void gate_both(float alpha, float v, float& value, fl
       dz = alpha;
     }
     if constexpr (ACT == kFastGelu) {
-      z = 1.5957691216057308f * v * (1.0f + 0.044715f * v * v);
-      dz = 1.5957691216057308f * (1.0f + 0.134145f * v * v);
+      // from 16 on one sigmoid is 1 and the other 0 (z = 317): the square of a larger v may
+      // be infinite, and the product below 0 * inf
+      const float near = fminf(fmaxf(v, -16.0f), 16.0f);
+      z = 1.5957691216057308f * near * (1.0f + 0.044715f * near * near);
+      dz = 1.5957691216057308f * (1.0f + 0.134145f * near * near);
     }
     float s, t;
     sigmoids_of<FAST>(z, s, t);

@@ -90,16 +90,17 @@ def activation(name, alpha, v, fast):
         c = alpha if name == "QuickGelu" else 1.0
         z, dz = c * v, torch.full_like(v, c)
     s, t = torch.sigmoid(z), torch.sigmoid(-z)
-    rel = k * (4 * z.abs() + 8) * E          # of s, and of t
+    # z is off by 4 |z| e at most; d s / dz = s t
+    rel_s, rel_t = k * (4 * z.abs() * t + 8) * E, k * (4 * z.abs() * s + 8) * E
     # where exp(-|z|) is below 2^-126, that is |z| > 87, it may be zero, and s or t with it.  What that
     # takes from v s and from v s t dz is largest at that border, where |v| < 90 for alpha >= 1 and
     # dz < 30
     least = 2.0 ** -126
     if name == "Sigmoid":
-        return s, s * t, rel * s + least, (2 * rel + E) * s * t + least
+        return s, s * t, rel_s * s + least, (rel_s + rel_t + E) * s * t + least
     fall, v_s = (v * s * t * dz).abs(), (v * s).abs()
-    return (v * s, s + v * s * t * dz, (rel + E) * v_s + 90 * least,
-            rel * s + (2 * rel + 8 * E) * fall + E * (s + fall) + (1 + 90 * 30) * least)
+    return (v * s, s + v * s * t * dz, (rel_s + E) * v_s + 90 * least,
+            rel_s * s + (rel_s + rel_t + 8 * E) * fall + E * (s + fall) + (1 + 90 * 30) * least)
 
 
 def gated_ffn(x, gate, up, down, name, alpha):

@@ -12,7 +12,7 @@ from oracle.transformer import _tiny, unit, within
 
 pytestmark = pytest.mark.gpu
 TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
-ACTS = [("QuickGelu", 1.0), ("QuickGelu", 1.702), ("Gelu", None), ("Sigmoid", None),
+ACTS = [("QuickGelu", 1.0), ("QuickGelu", 1.702), ("Gelu", None), ("FastGelu", None), ("Sigmoid", None),
         ("Relu", None)]
 
 
