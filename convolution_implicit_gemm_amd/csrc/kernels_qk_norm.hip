@@ -10,8 +10,7 @@
 // meet in one of three ways:
 //   kHalves   the two halves of the turned part are whole pieces: a lane has pairs of
 //             pieces, one of either half, and behind the turned part neighbours
-//   kNext     interleaved: a lane has neighbouring pieces; the table goes on behind
-//             the turned part with angles of zero
+//   kNext     interleaved: a lane has neighbouring pieces
 //   kCross    halves that are no whole pieces: neighbouring pieces, and a value's
 //             other half comes through LDS, where the group has left its values.
 //             Pieces of 2 to 8 bytes instead, as kHalves would need, took 149 us
@@ -66,14 +65,20 @@ struct QkK {
   FastDiv len;
 };
 
+// What is known of every lane at launch (FULL).
+enum Full : int {
+  kSome = 0,
+  kWhole,  // kNext, kCross: every item is a whole pair of pieces
+  kTurns   // kHalves, kNext: that, and all of them turn
+};
+
 // The pieces of item i of a head: where they begin, whether there are any, and
-// (kHalves) whether they turn.  FULL: every lane's items are whole pairs of pieces,
-// and (kHalves) all of them turn.
+// (kHalves) whether they turn.
 struct Item {
   int at[2];
   bool on[2], turn;
 };
-template <int W, int MEET, bool FULL>
+template <int W, int MEET, int FULL>
 __device__ __forceinline__ Item item_of(const QkK& a, int i) {
   Item m;
   if (MEET == kHalves && (FULL || i < a.turned)) {
@@ -104,7 +109,7 @@ __device__ __forceinline__ int table_at(int e) { return e + e / (MEET == kCross 
 // Every pair of a lane's values turned by SIGN times its angle.  kCross: own is where
 // run n's values go in LDS, other where the other halves of all values are (a zero
 // for those that have none).
-template <int W, int MEET, bool FULL, int SIGN>
+template <int W, int MEET, int FULL, int SIGN>
 __device__ __forceinline__ void turn_values(const QkK& a, const Item (&items)[kHeld / (2 * W)], const float2* cs,
                                             float* cross, const int (&own)[kHeld / (2 * W)],
                                             const int (&other)[kHeld], float (&v)[kHeld]) {
@@ -128,8 +133,10 @@ __device__ __forceinline__ void turn_values(const QkK& a, const Item (&items)[kH
         for (int j = 0; j < 2 * W; j += 2) {
           const float2 c = cs[table_at<W, MEET>(items[n].at[0] >> 1) + (j >> 1)];
           const float s = SIGN * c.y, x = z[j], y = z[j + 1];
-          z[j] = x * c.x - y * s;
-          z[j + 1] = y * c.x + x * s;
+          // behind the turned part nothing of the neighbour's, not even 0 * inf
+          const bool turns = FULL == kTurns || items[n].at[0] + j < 2 * a.pairs;
+          z[j] = turns ? x * c.x - y * s : x;
+          z[j + 1] = turns ? y * c.x + x * s : y;
         }
       } else if (FULL || items[n].turn) {
 #pragma unroll
@@ -173,8 +180,10 @@ struct Held {
   }
 };
 
-template <typename T, int MEET, bool FULL, bool BACK>
-__global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
+// Four blocks to a compute unit in 16 bits (kCross has no LDS for them): a few registers
+// more than they leave cost the interleaved backward pass of 256 x 196 tokens 12 %.
+template <typename T, int MEET, int FULL, bool BACK>
+__global__ __launch_bounds__(256, sizeof(T) == 2 && MEET != kCross ? 4 : 1) void k_qk_norm(QkK a) {
   constexpr int W = 16 / sizeof(T), N = kHeld / (2 * W);  // N: items of a lane
   extern __shared__ __attribute__((aligned(16))) char lds[];
   // backward: the lanes' sums [q, k][kHeld / 4][256][4]; kCross: the groups' values, a
@@ -202,9 +211,8 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkK a) {
     }
     if (threadIdx.x == 0) cross[kCrossed - 1] = 0.f;
   }
-  if constexpr (MEET != kHalves) {  // behind the turned part
-    const int turned = MEET == kCross ? 2 * a.pairs : a.pairs;
-    const int rest = (MEET == kCross ? kHeld : kHeld / 2) * a.lanes - turned;
+  if constexpr (MEET == kCross) {  // behind the turned part
+    const int turned = 2 * a.pairs, rest = kHeld * a.lanes - turned;
     for (int i = threadIdx.x; i < a.tok * rest; i += 256) {
       const int t = i / rest;
       table[t * a.entries + table_at<W, MEET>(turned + i - t * rest)] = make_float2(1.f, 0.f);
@@ -418,7 +426,7 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
   const int items = meet == kHalves ? k.turned + (k.pieces - 2 * k.turned + 1) / 2 : (k.pieces + 1) / 2;
   const int held = kHeld / (2 * w);
   k.lanes = (items + held - 1) / held;
-  const bool full = k.lanes * kHeld == k.d && (meet != kHalves || 2 * k.pairs == k.d);
+  const bool whole = k.lanes * kHeld == k.d, turns = whole && 2 * k.pairs == k.d;
   k.entries = meet == kHalves ? k.pairs : (meet == kNext ? kHeld / 2 : kHeld) * k.lanes;
   k.tok = tokens_of_block(d, (meet == kCross ? 1024 : 512) / k.entries);
   const int run = meet == kCross ? 2 * w : w;
@@ -434,15 +442,20 @@ int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
   if (blocks > 0)
     with_type(d.dtype, [&](auto tag) {
       using T = typename decltype(tag)::type;
-      auto go = [&](auto m) {
-        constexpr int how = decltype(m)::value;
-        auto fn = back ? (full ? k_qk_norm<T, how, true, true> : k_qk_norm<T, how, false, true>)
-                       : (full ? k_qk_norm<T, how, true, false> : k_qk_norm<T, how, false, false>);
-        hipLaunchKernelGGL(fn, dim3(blocks), dim3(256), lds, st, k);
+      auto go = [&](auto m, auto f) {
+        constexpr int how = decltype(m)::value, full = decltype(f)::value;
+        hipLaunchKernelGGL((back ? k_qk_norm<T, how, full, true> : k_qk_norm<T, how, full, false>), dim3(blocks),
+                           dim3(256), lds, st, k);
       };
-      if (meet == kNext) go(std::integral_constant<int, kNext>{});
-      else if (meet == kHalves) go(std::integral_constant<int, kHalves>{});
-      else go(std::integral_constant<int, kCross>{});
+      constexpr std::integral_constant<int, kSome> some{};
+      constexpr std::integral_constant<int, kWhole> all_whole{};
+      constexpr std::integral_constant<int, kTurns> all_turn{};
+      if (constexpr std::integral_constant<int, kNext> next{}; meet == kNext)
+        turns ? go(next, all_turn) : whole ? go(next, all_whole) : go(next, some);
+      else if (constexpr std::integral_constant<int, kHalves> halves{}; meet == kHalves)
+        turns ? go(halves, all_turn) : go(halves, some);
+      else if (constexpr std::integral_constant<int, kCross> cross{}; true)
+        whole ? go(cross, all_whole) : go(cross, some);
     });
   if (sums)  // without tokens they are zero
     hipLaunchKernelGGL(k_qk_norm_join, dim3((2 * k.d + 15) / 16), dim3(1024), 0, st, a.part, blocks, k.d,
