@@ -172,7 +172,7 @@ def qk_norm_rotary(q, k, q_weight, k_weight, positions, inv_freq, axes, *, eps=1
     axis are fine; head_dim at most 256, in whole 16-byte pieces.  q_weight, k_weight: [head_dim], q's
     dtype, shared by the heads, or None (ones).  positions, inv_freq, axes and interleaved as rotary
     takes them; values behind 2 * pairs are normed and not turned.  out_q / out_k: where to write (q
-    and k themselves are allowed)."""
+    and k themselves are allowed, each over itself; what overlaps another tensor is refused)."""
     if _t.torch is None or _lib is None:
         _setup()
     eps = float(eps)
@@ -198,7 +198,7 @@ def qk_norm_rotary_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_fre
     its arguments; dk None where k is.  dq and dk have q's dtype, the weights' gradients are float32
     [head_dim], summed over batch, positions and heads (None where there is no weight, or with
     weight_grad=False).  out_q / out_k: where to write (the gradients given, or q and k, are
-    allowed)."""
+    allowed, each over itself; what overlaps another tensor is refused)."""
     if _t.torch is None or _lib is None:
         _setup()
     eps = float(eps)

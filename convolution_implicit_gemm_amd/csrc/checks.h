@@ -37,13 +37,13 @@ inline int64_t product(int64_t a, int64_t b, int64_t c, int64_t limit) {
 inline constexpr int64_t kMaxElements = int64_t(1) << 40;
 
 // Launch by f() and report what came of it; the bookkeeping of a launch may run out
-// of host memory.
+// of host memory.  A code other than the launch's own has its text already.
 template <typename F>
 int launched(F&& f) noexcept {
   int rc = FUSEDCONV_ERR_ALLOC;
   try {
     rc = f();
-    if (rc == FUSEDCONV_OK) return rc;
+    if (rc != FUSEDCONV_ERR_LAUNCH) return rc;
     return set_last_error(
         rc, std::string("kernel launch failed: ") + hipGetErrorString(hipGetLastError()));
   } catch (...) {

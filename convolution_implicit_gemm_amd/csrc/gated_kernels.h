@@ -20,7 +20,9 @@
 
 #include <algorithm>
 
+#include "checks.h"
 #include "internal.h"
+#include "overlap.h"
 #include "product_tile.h"
 
 namespace fc {
@@ -260,8 +262,11 @@ int launch_product(ProductK k, const ProductPlan& plan, hipStream_t st) {
   }
 }
 
+constexpr char kOverlap[] = "outputs and the workspace must overlap neither inputs nor each other";
+
 template <typename T>
 int forward(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a) {
+  if (gated_overlaps(p, plan, a, false)) return fail(FUSEDCONV_ERR_ATTR_VALUE, kOverlap);
   const hipStream_t st = (hipStream_t)a.stream;
   constexpr int64_t es = sizeof(T);
   void* h = a.ws;
@@ -288,6 +293,7 @@ int forward(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a) {
 
 template <typename T>
 int backward(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a) {
+  if (gated_overlaps(p, plan, a, true)) return fail(FUSEDCONV_ERR_ATTR_VALUE, kOverlap);
   const hipStream_t st = (hipStream_t)a.stream;
   constexpr int64_t es = sizeof(T);
   char* ws = (char*)a.ws;

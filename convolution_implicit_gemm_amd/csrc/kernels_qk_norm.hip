@@ -33,6 +33,8 @@
 #include <type_traits>
 
 #include "block.h"
+#include "checks.h"
+#include "overlap.h"
 #include "turns.h"
 #include "vec.h"
 
@@ -392,6 +394,8 @@ int tokens_of_block(const fusedconv_qk_norm_rotary_desc& d, int most) {
 }
 
 int launch(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
+  if (qk_overlaps(d, a, back))
+    return fail(FUSEDCONV_ERR_ATTR_VALUE, "an output overlaps another tensor (Q, K and their gradients may be written over themselves)");
   QkK k{};
   auto side = [&](QkSide& s, const void* x, const void* w, const void* dy, void* y, const int64_t* xs,
                   const int64_t* ys, const int64_t* ds, int64_t heads) {

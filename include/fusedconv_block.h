@@ -33,7 +33,8 @@ extern "C" {
  * head_dim: whole 16-byte pieces, at most 256.  Strides in elements {batch, len,
  * head}, multiples of 16 bytes, the last axis contiguous (0 repeats an input; an
  * output's elements must not overlap).  A result may be its own input, and dx may
- * be its dy or its x (same pointer and strides); outputs overlap nothing else.
+ * be its dy or its x (same pointer and strides); outputs that overlap anything else
+ * are refused (FUSEDCONV_ERR_ATTR_VALUE).
  */
 typedef struct fusedconv_qk_norm_rotary_desc {
   int32_t dtype;
@@ -94,7 +95,8 @@ void fusedconv_qk_norm_rotary_destroy(fusedconv_qk_norm_rotary* h);
  * taken twice): whatever the sizes of dy, the weights and u, a factor keeps its bits
  * down to 2^-18 of the largest one or further.
  *
- * Outputs overlap neither inputs nor each other.
+ * Outputs and the workspace overlap neither inputs nor each other: such a call is
+ * refused (FUSEDCONV_ERR_ATTR_VALUE).
  */
 typedef struct fusedconv_gated_ffn_desc {
   int32_t dtype;
