@@ -307,31 +307,38 @@ __device__ __forceinline__ void finish_hidden8(const ProductK& a, int l, int r, 
 // the LDS address, is an operand.
 constexpr uint32_t kOutside = 0x80000000u;
 typedef uint32_t Buffer __attribute__((ext_vector_type(4)));
+// A scalar register that a vector instruction has written (readfirstlane) may be read
+// by a memory instruction five wait states later; the compiler does not see that a copy
+// is one.  An unoptimised build, which has the buffer in vector registers (as
+// FC_WAVE_POINTER says), makes it scalar in front of every copy.
+#ifdef __OPTIMIZE__
+#define FC_WAVE_BUFFER(b) (b)
+#define FC_BUFFER_READY(b) asm volatile("s_nop 4" : "+s"(b))
+#define FC_COPY_WAIT "s_nop 0"
+#else
+#define FC_WAVE_WORD(b, n) (uint32_t)__builtin_amdgcn_readfirstlane((b)[n])
+#define FC_WAVE_BUFFER(b) (Buffer{FC_WAVE_WORD(b, 0), FC_WAVE_WORD(b, 1), FC_WAVE_WORD(b, 2), FC_WAVE_WORD(b, 3)})
+#define FC_BUFFER_READY(b)
+#define FC_COPY_WAIT "s_nop 4"
+#endif
 __device__ __forceinline__ Buffer buffer_at(const char* base) {
   const uint64_t at = (uint64_t)base;
   // raw bytes: no stride, kOutside of them
   Buffer b{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at),
            (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32) & 0xffffu), kOutside, 0x00020000u};
-  // A scalar register that a vector instruction has written (readfirstlane) may be
-  // read by a memory instruction five wait states later; the compiler does not see
-  // that the copies below are any.
-#ifdef __OPTIMIZE__
-  asm volatile("s_nop 4" : "+s"(b));
-#endif
+  FC_BUFFER_READY(b);
   return b;
 }
 __device__ __forceinline__ void copy_buffer_to_lds(uint32_t to, uint32_t off, Buffer from) {
-#ifdef __OPTIMIZE__
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(
+  asm volatile(FC_COPY_WAIT "\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(
                    __builtin_amdgcn_readfirstlane(to)),
-               "v"(off), "s"(from)
+               "v"(off), "s"(FC_WAVE_BUFFER(from))
                : "memory");
-#else  // unoptimised code has no scalar registers for an operand: the same by a load and a store
-  const char* base = (const char*)(from[0] | (uint64_t)from[1] << 32);
-  *(__attribute__((address_space(3))) Buffer*)(to + 16 * (threadIdx.x & 63)) =
-      off < kOutside ? *(const Buffer*)(base + off) : Buffer{0, 0, 0, 0};
-#endif
 }
+#undef FC_WAVE_BUFFER
+#undef FC_BUFFER_READY
+#undef FC_COPY_WAIT
+#undef FC_WAVE_WORD
 
 // Terms 16 * step .. + 15 (natural order: 8 * (lane / 32) ...) of the columns
 // 32 * t .. + 31 of a tile whose rows are terms.  ds_read_b64_tr_b16 as in
