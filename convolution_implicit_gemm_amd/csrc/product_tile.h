@@ -440,7 +440,6 @@ struct Shape {
   // three stages, or two and a side of a third
   static constexpr int kLds = RB == 256 ? 2 * kStage + LB * BYTES : 3 * kStage;
 };
-constexpr int kMeetRow = 68;  // floats of a row where a wave turns its results round
 
 // A tile's rows and columns: groups of 8 row tiles walk over the columns together,
 // so that blocks that run at one time on an XCD share both sides in its L2.
