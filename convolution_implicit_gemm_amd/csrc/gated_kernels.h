@@ -33,9 +33,9 @@ namespace {
 // rows of the weights (of gate and of up), its waves share the terms, 256 bytes of
 // every row a wave at a time, with the next ones on their way; the waves' sums meet in
 // LDS.  Products are 16 x 16 with the weights as the first operand: a lane ends
-// with four neighbouring results of one row of x.  4096 x 11008, bf16, both
-// launches: one row 59 us (271 MB, 4.6 TB/s), 16 rows 74 us, 32 rows 97 us: every
-// block reads all of x, from the L2, beside its weights.
+// with four neighbouring results of one row of x.  4096 x 11008, bf16, both kernels on
+// weights out of memory: one row 65 us (271 MB, 4.1 TB/s), 16 rows 76, 32 rows 100:
+// every block reads all of x, from the L2, beside its weights.
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t Chunk __attribute__((ext_vector_type(4)));  // 16 bytes: terms of one row
 

@@ -72,8 +72,11 @@ size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 void plan_gated(const GatedProblem& p, GatedPlan& plan) {
   const int es = p.dtype == 0 ? 4 : 2, kb = 64 / es;
   const int64_t m = p.m, c = p.c, f = p.f, o = p.o;
-  // Up to 32 rows go by k_gated_few: 32 rows, bf16, 1024 x 2736 15 us, tiles 25; 4096 x
-  // 4096 32 and 34; 2048 x 5632 36 and 33; 4096 x 11008 87 and 80 (20 rows 72 and 80).
+  // Up to 32 rows go by k_gated_few.  It and tiles, us of a call replayed on the same
+  // tensors, bf16, 16 / 24 / 32 rows: 1024 x 2736 18 / 17 / 18 and 27 / 28 / 28; 4096 x
+  // 4096 29 / 33 / 37 and 37; 2048 x 5632 31 / 39 / 41 and 36; 4096 x 11008 67 / 81 / 91
+  // and 83 / 84 / 84.  From some 24 rows of the larger weights on, tiles are the faster
+  // ones, by up to 14 % (f32: 32 rows of 4096 x 11008 218 and 187).
   plan.few = m <= 32;
   plan.gate = plan_product(p, kGate, ceil_div(c, kb), 1, {m, 0, 0}, {f, 0, 0});
   plan.down = plan_product(p, kDown, ceil_div(f, kb), 1, {m, 0, 0}, {o, 0, 0});

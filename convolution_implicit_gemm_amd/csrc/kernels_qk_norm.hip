@@ -16,7 +16,9 @@
 //             Pieces of 2 to 8 bytes instead, as kHalves would need, took 149 us
 //             (36 pairs of 72 values; backward 273) and 202 us (18 pairs of 88; 385)
 //             where this takes 111 (220) and 123 (244): 256 x 196 tokens, 12 heads in
-//             Q and K, bf16; a copy 69 (103) and 84 (126).  LDS bounds it.
+//             Q and K, bf16; a copy 69 (103) and 84 (126).  Latency bounds it: waves wait
+//             64 % of their time, 7 of that for the LDS, with nothing of the next head on
+//             its way.
 // A group has as many lanes as its head fills (heads of 80: 108 us in 8 lanes, 88 in
 // 5); where that is no power of two its sums take a few shuffles more.
 //
@@ -25,8 +27,8 @@
 // tokens, and a second launch adds their sums in a fixed order.
 //
 // Memory bounds both directions: 256 x 196 tokens, 12 heads of 64 in Q and K, bf16,
-// forward 65 us (308 MB, 4.8 TB/s), backward 99 us (463 MB, 4.7 TB/s); a copy of
-// 1 GiB runs at 5.0.
+// forward 65 us (308 MB, 4.7 TB/s), backward 98 to 102 us (463 MB, 4.5 to 4.7 TB/s); a
+// copy of 1 GiB runs at 5.0.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
