@@ -96,12 +96,16 @@ inline bool meet(const Extent& a, const Extent& b) {
   return m.search(0, between);
 }
 
+// A step of an axis, in bytes; that of one entry is any number and not looked at.
+inline int64_t step_of(int64_t count, int64_t stride, int64_t size) { return count > 1 ? stride * size : 0; }
+
 // Norms of queries and keys: a result may be its own input (backward: the gradient of Q
 // the gradient given or Q, and so on for K); outputs meet nothing else.
 inline bool qk_overlaps(const fusedconv_qk_norm_rotary_desc& d, const QkArgs& a, bool back) {
   const int64_t es = d.dtype == FUSEDCONV_F32 ? 4 : 2, row = d.head_dim * es;
   const auto heads = [&](const void* p, const int64_t (&s)[3], int64_t n) {
-    return Extent{p, row, {d.batch, d.len, n}, {s[0] * es, s[1] * es, s[2] * es}};
+    return Extent{p, row, {d.batch, d.len, n},
+                  {step_of(d.batch, s[0], es), step_of(d.len, s[1], es), step_of(n, s[2], es)}};
   };
   const auto flat = [](const void* p, int64_t bytes) { return Extent{p, bytes}; };
   const int64_t tokens = (d.position_batch_stride ? d.batch : 1) * d.len;
@@ -141,7 +145,7 @@ inline bool gated_overlaps(const GatedProblem& p, const GatedPlan& plan, const G
   const int64_t es = p.dtype == FUSEDCONV_F32 ? 4 : 2, m = p.m, c = p.c, f = p.f, o = p.o;
   const auto flat = [](const void* at, int64_t bytes) { return Extent{at, bytes}; };
   const auto rows = [&](const void* at, int64_t n, int64_t step) {
-    return Extent{at, n * es, {1, 1, m}, {0, 0, step * es}};
+    return Extent{at, n * es, {1, 1, m}, {0, 0, step_of(m, step, es)}};
   };
   const Extent in[] = {
       rows(a.x, c, p.x_stride),

@@ -19,7 +19,8 @@ extern "C" {
  * a weight per value and turned by its positions, in one pass:
  *     r = 1 / sqrt(mean(x^2) + eps),  n = x * r * weight,  y = R(t) n
  * with R(t) as fusedconv_rotary_run() turns (pairs, axes, interleaved, positions
- * as there; values from 2 * pairs on are normed and not turned).  q_weight and
+ * as there; values from 2 * pairs on are normed and not turned).  Squares are summed
+ * in fp32: a head whose sum is beyond 3.4e38 gives zeros.  q_weight and
  * k_weight: T[head_dim] each, shared by the heads, or not declared (ones).
  *
  * Backward, for the gradient dy of y:

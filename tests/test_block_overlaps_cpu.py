@@ -225,3 +225,22 @@ def test_gated_calls_against_bytes(ask):
     got = ask(lines)
     assert got == want, next(z for z in zip(lines, got, want) if z[1] != z[2])
     assert 1000 < sum(want) < 5000
+
+
+def test_strides_of_single_entries_are_not_looked_at(ask):
+    """An axis of one entry has any stride, up to the ends of its type (the probe is built with the
+    undefined-behaviour sanitizer)."""
+    lines = []
+    for wild in (2 ** 63 - 1, -2 ** 63, 2 ** 62, -3):
+        for back in (0, 1):
+            strides = [(wild, wild, wild)] * 6
+            ptr = [n * 4096 for n in range(14)]
+            if not back:
+                for n in (2, 3, 11, 12, 13):
+                    ptr[n] = -1
+            lines.append(["qk", 0, 1, 1, 1, 1, 1, 8, 4, 1, 0, *itertools.chain(*strides), *ptr, back, *[0] * (48 - 43)])
+            lines.append([*lines[-1]])
+            lines[-1][1 + 10 + 18 + 9] = ptr[0] + 16  # Q's result over Q's second half
+        lines.append(["gated", 1, 1, 8, 8, 8, wild, wild, 16, 112, *[n * 8192 for n in range(7)], 7 * 8192, -1, -1, -1, -1,
+                      12 * 8192, 0, 0])
+    assert ask(lines) == [False, True, False, True, False] * 4
