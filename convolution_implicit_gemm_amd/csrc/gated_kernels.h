@@ -14,7 +14,7 @@
 // 2^8 and 2^9; what they pass on is divided by it again.  What dh, u and the slope make
 // of dy is known behind the product only: it keeps the largest factor, and where that is
 // beyond f16 or below 2^4 a second launch, which otherwise ends at once (16 rows of
-// 1024 x 2736: 42 us without it, 43.5 with it), takes the product again with the scale
+// 1024 x 2736: 36 us a call before there was one, 37.6 with it), takes the product again with the scale
 // that fits it.
 #pragma once
 
@@ -192,9 +192,9 @@ __global__ __launch_bounds__(1024) void k_gated_tops(const T* dy, int64_t stride
                                                      uint32_t* words) {
   __shared__ float meet[16];
   constexpr int P = 16 / sizeof(T);
-  const int per = cols / P, blocks = gridDim.x, waves = 16 * blocks, lane = threadIdx.x & 63;
+  const int own = blockDim.x >> 6, per = cols / P, blocks = gridDim.x, waves = own * blocks, lane = threadIdx.x & 63;
   float top = 0.f;
-  for (int64_t row = 16 * blockIdx.x + (threadIdx.x >> 6); row < rows; row += 4 * waves)
+  for (int64_t row = own * blockIdx.x + (threadIdx.x >> 6); row < rows; row += 4 * waves)
     for (int i = lane; i < per; i += 64) {
       Piece<T, P> x[4];
 #pragma unroll
@@ -212,13 +212,12 @@ __global__ __launch_bounds__(1024) void k_gated_tops(const T* dy, int64_t stride
   if (lane == 0) meet[threadIdx.x >> 6] = top;
   __syncthreads();
   if (threadIdx.x == 0) {
-#pragma unroll
-    for (int n = 1; n < 16; ++n) top = fmaxf(top, meet[n]);
+    for (int n = 1; n < own; ++n) top = fmaxf(top, meet[n]);
     words[FactorScale::kTops + blockIdx.x] = __float_as_uint(top);
   }
-  for (int i = blockIdx.x + blocks * (1 + threadIdx.x); i < FactorScale::kParts; i += blocks * 1024)
+  for (int i = blockIdx.x + blocks * (1 + threadIdx.x); i < FactorScale::kParts; i += blocks * blockDim.x)
     words[FactorScale::kTops + i] = 0;
-  for (int i = blockIdx.x + blocks * threadIdx.x; i < 64; i += blocks * 1024)
+  for (int i = blockIdx.x + blocks * threadIdx.x; i < 64; i += blocks * blockDim.x)
     words[FactorScale::kSlots + i * FactorScale::kStep] = 0;
 }
 
@@ -312,9 +311,11 @@ int backward(const GatedProblem& p, const GatedPlan& plan, const GatedArgs& a) {
   if (p.m > 0) {
     if constexpr (is_scaled<T>) {
       k.scale = (uint32_t*)(ws + 3 * plan.hidden_bytes);
-      const int64_t blocks = std::min((p.m + int64_t(15)) / 16, (int64_t)FactorScale::kParts);
-      hipLaunchKernelGGL((k_gated_tops<T>), dim3((unsigned)blocks), dim3(1024), 0, st, (const T*)a.dy, p.dy_stride,
-                         p.m, p.o, k.scale);
+      // a wave to a row, up to 16 of them in each of a few blocks
+      const int waves = p.m <= 4 * FactorScale::kParts ? 4 : 16;
+      const int64_t blocks = std::min((p.m + int64_t(waves) - 1) / waves, (int64_t)FactorScale::kParts);
+      hipLaunchKernelGGL((k_gated_tops<T>), dim3((unsigned)blocks), dim3(64 * waves), 0, st, (const T*)a.dy,
+                         p.dy_stride, p.m, p.o, k.scale);
     }
     k.p[0] = Product{a.dy, a.down, nullptr, nullptr, nullptr, p.dy_stride * es, p.f * es, p.m, p.f, p.o};
     for (int again = 0; again <= (int)is_scaled<T>; ++again) {

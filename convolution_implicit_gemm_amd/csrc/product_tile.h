@@ -211,9 +211,10 @@ __device__ __forceinline__ float wave_max(float v) {
   for (int off = 1; off < 64; off <<= 1) v = fmaxf(v, __shfl_xor(v, off));
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
 }
-__device__ __forceinline__ float first_scale(const uint32_t* words) {
-  const Piece<float, 4> x =
-      load_piece<float, 4>((const float*)words + FactorScale::kTops + 4 * (threadIdx.x & 63));
+__device__ __forceinline__ Piece<float, 4> load_tops(const uint32_t* words) {
+  return load_piece<float, 4>((const float*)words + FactorScale::kTops + 4 * (threadIdx.x & 63));
+}
+__device__ __forceinline__ float first_scale(const Piece<float, 4>& x) {
   const float top = wave_max(fmaxf(fmaxf(x.v[0], x.v[1]), fmaxf(x.v[2], x.v[3])));
   return top > 0.f ? ldexpf(1.f, 8 - ilogbf(top)) : 1.f;
 }
@@ -222,7 +223,7 @@ template <typename T, int FORM>
 __device__ __forceinline__ bool second_scale(const ProductK& a, float& scale) {
   if constexpr (FORM == kHidden && is_scaled<T>) {
     if (!a.again) return true;
-    const float first = first_scale(a.scale);
+    const float first = first_scale(load_tops(a.scale));
     const float top = wave_max(
         __uint_as_float(a.scale[FactorScale::kSlots + (threadIdx.x & 63) * FactorScale::kStep]));
     // factors below 2^-40 of it are no longer followed: no result would hold them
@@ -531,7 +532,7 @@ __device__ __forceinline__ void finish_tile(const ProductK& a, const Work<T, LB,
   static_assert(4 * 32 * AT * ROW * 4 <= Shape<T, LB, RB, FORM>::kLds);
   float* meet = (float*)lds + w.wave * 32 * AT * ROW;
   float scale = 1.f, top = 0.f;  // kHidden
-  if constexpr (FORM == kHidden && is_scaled<T>) scale = a.again ? w.scale : first_scale(a.scale);
+  if constexpr (FORM == kHidden && is_scaled<T>) scale = a.again ? w.scale : first_scale(load_tops(a.scale));
   each_index<0, LT / AT * RP>([&](auto step) {
     constexpr int t0 = step / RP * AT, part = step % RP;
     const int col0 = (RP * (w.wave >> 1) + part) * COLS;  // of the tile
@@ -767,8 +768,6 @@ __global__ __launch_bounds__(256) void k_product_join(ProductK a) {
   constexpr int rows = 2048 / RB, strips = LB / rows, groups = RB / 8;
   float scale = 1.f;
   if (!second_scale<T, FORM>(a, scale)) return;
-  if constexpr (FORM == kHidden && is_scaled<T>)
-    if (!a.again) scale = first_scale(a.scale);
   const int item = a.whole + block_number() / strips;
   if ((int64_t)(item - a.whole) * a.splits >= a.split_items) return;
   const int which = a.products > 1 ? (item >= a.p[1].first) + (a.products > 2 && item >= a.p[2].first) : 0;
@@ -804,12 +803,22 @@ __global__ __launch_bounds__(256) void k_product_join(ProductK a) {
     if (FORM != kHidden && r >= p.cols) return;
     float v[8];
     if constexpr (FORM == kHidden) {
-      float top = 0.f;
-      if (l < p.rows && r < p.cols) {
-        float g[8], u[8];
+      const bool in = l < p.rows && r < p.cols;
+      Held8<T> gh, uh;
+      Piece<float, 4> tops;
+      if constexpr (is_scaled<T>) tops = load_tops(a.scale);
+      if (in) {
+        gh.load((const T*)a.g + (int64_t)l * a.f + r);
+        uh.load((const T*)a.u + (int64_t)l * a.f + r);
         sum(8 * at, v);
-        load8((const T*)a.g + (int64_t)l * a.f + r, g);
-        load8((const T*)a.u + (int64_t)l * a.f + r, u);
+      }
+      if constexpr (is_scaled<T>)
+        if (!a.again) scale = first_scale(tops);
+      float top = 0.f;
+      if (in) {
+        float g[8], u[8];
+        gh.values(g);
+        uh.values(u);
         finish_hidden8<T>(a, l, r, v, g, u, scale, top);
       }
       record_top<T>(a, top);
