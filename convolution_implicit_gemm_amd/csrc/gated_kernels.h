@@ -14,8 +14,8 @@
 // 2^8 and 2^9; what they pass on is divided by it again.  What dh, u and the slope make
 // of dy is known behind the product only: it keeps the largest factor, and where that is
 // beyond f16 or below 2^4 a second launch, which otherwise ends at once (16 rows of
-// 1024 x 2736: 36 us a call before there was one, 37.6 with it), takes the product again with the scale
-// that fits it.
+// 1024 x 2736: 36 us a call before there was one, 37.6 with it), takes the product again
+// with the scale that fits it.
 #pragma once
 
 #include <algorithm>

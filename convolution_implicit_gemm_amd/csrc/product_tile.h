@@ -197,9 +197,9 @@ struct Held8 {
 // dy's largest magnitude to 2^8.  kHidden keeps the largest factor that this gave, and
 // where that is beyond f16 or below 2^4 runs again with the scale that takes it to 2^14.
 // So the largest factor lies 2^18 or more above 2^-14, where values begin to lose bits.
-// What is behind it divides by the one held.  The largest factors are kept in slots, a line each: 6000
-// waves' atomics on one address took 200 us of the 18464 rows' backward pass (1024 x
-// 2736).
+// What is behind it divides by the one held.  The largest factors are kept in slots, a
+// line each: 6000 waves' atomics on one address took 200 us of the 18464 rows' backward
+// pass (1024 x 2736).
 struct FactorScale {
   static constexpr int kHeld = 0, kTops = 32, kParts = 256, kSlots = kTops + kParts, kStep = 32;
   static constexpr int kWords = kSlots + 64 * kStep;
